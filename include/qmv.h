@@ -172,11 +172,14 @@ enum qmv_format {
   QMV_F32 = 8
 };
 
+/* Types of float tensors (norm, cache and attention entry points). */
+enum qmv_dtype { QMV_DT_F32 = 0, QMV_DT_F16 = 1, QMV_DT_BF16 = 2 };
+
 enum qmv_status {
   QMV_OK = 0,
-  QMV_ERR_FORMAT = -1,    /* unknown format code */
+  QMV_ERR_FORMAT = -1,    /* unknown format or dtype code */
   QMV_ERR_SHAPE = -2,     /* M <= 0, K not a multiple of the group size, ... */
-  QMV_ERR_NTOK = -3,      /* n_tok not in [1, 64] or top_k not in [1, 8] */
+  QMV_ERR_NTOK = -3,      /* n_tok not in [1, 64] (or the call's own range) or top_k not in [1, 8] */
   QMV_ERR_NULL = -4,      /* a required pointer is NULL */
   QMV_ERR_ALIGN = -5,     /* a pointer is not 16-byte aligned */
   QMV_ERR_WORKSPACE = -6, /* workspace too small */
@@ -190,6 +193,9 @@ enum qmv_status {
 #define QMV_DEVERR_EXPERT_DUP 0x2   /* an expert id repeated within a token */
 #define QMV_DEVERR_TIMEOUT 0x4      /* a pipeline wait exceeded its limit */
 #define QMV_DEVERR_RANGE 0x8        /* debug build: an access failed its range check (and was skipped) */
+
+#define QMV_DEVERR_PAGE 0x10  /* a page index outside the cache (its tokens are left out) */
+#define QMV_DEVERR_BATCH 0x20 /* lens / starts that contradict the call's sizes (clamped) */
 
 #define QMV_MAX_TOKENS 64
 #define QMV_MAX_PREFILL_TOKENS 16384 /* moe_qmv_prefill_run */
@@ -417,6 +423,148 @@ int moe_qmv_prefill_run(const moe_experts* e, const int32_t* ids, const float* g
 int moe_route_run(int fmt, const void* Wr, const float* x, int n_experts, int64_t hidden,
                   int n_tok, int top_k, int gating, float* logits, int32_t* ids, float* gates,
                   cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The attention half of a decode layer: norm, 8-bit key / value cache,
+ * attention, page selection.  (The pages name norm fusion, "Castagna Veloce",
+ * section "Fused operations", and an 8-bit KV cache, "Running GLM-5.3 on Two
+ * 8-GPU AMD W7900D Machines", section "Why 4-bit today: room for 5/6-bit, but
+ * not FP8"; the layouts and formulas are this library's own.)
+ * Float tensors here are of one qmv_dtype per call (the norm's weights are
+ * always fp32); arithmetic is fp32 throughout.
+ * ------------------------------------------------------------------------ */
+
+/* Root-mean-square norm with the residual's addition:
+ *   s = x + r,   y_i = (s_i * (1 / sqrt(mean(s^2) + eps))) * w_i
+ * per row of K values, in fp32 (s enters the norm before it is rounded to
+ * dtype).  x [rows][K] with rows ldx >= K elements apart, r [rows][K] or NULL
+ * (s = x), w fp32 [K].  Results, each NULL where it is not wanted (at least
+ * one is): res [rows][K] = s and y [rows][K] in dtype, and y quantized by the
+ * activation rule into the Q8 activation layout of qmv_quantize_act (q int8
+ * [rows][K], d fp32 and sum int32 [rows][K/32], given together), which
+ * qmv_run_q8 takes: no matvec then quantizes its input again.  res and y may
+ * be r or (with ldx = K) x.
+ * Constraints: 1 <= K <= QMV_MAX_NORM (any K without q; with q K % 256 == 0
+ * and ldx * element size a multiple of 16, else QMV_ERR_ALIGN), 1 <= rows <=
+ * 2^24, eps >= 0. */
+#define QMV_MAX_NORM 32768
+int qmv_rms_norm(int dtype, const void* x, int64_t ldx, const void* r, const float* w, float eps, int64_t rows,
+                 int64_t K, void* res, void* y, int8_t* q, float* d, int32_t* sum, cudaStream_t stream);
+
+/* The values d * q that Q8 activations stand for, in dtype: out [rows][K].
+ * K % 256 == 0. */
+int qmv_dequantize_act(int dtype, const int8_t* q, const float* d, int64_t rows, int64_t K, void* out,
+                       cudaStream_t stream);
+
+/* A paged cache of keys and values in 8 bits, with one scale for the keys and
+ * one for the values of each (page of page_tokens tokens, kv head).
+ *   pages: [n_pages][n_kv_heads] records of qmv_kv_page_bytes = 16 + 2 P D
+ *     bytes (P = page_tokens, D = head_dim): fp32 key scale, fp32 value scale,
+ *     8 spare bytes; key codes [D / 64][P][64]; value codes [D][P].  A code
+ *     byte b stands for scale * (b - 128), b in [1, 255].
+ *   bounds (NULL if qmv_kv_select is not used): [n_pages][n_kv_heads] records
+ *     of qmv_kv_bounds_bytes = 16 + 2 D bytes: fp32 key scale, 12 spare bytes,
+ *     the smallest and then the largest key code (int8, b - 128) of each
+ *     dimension over the page's tokens.
+ * P is 16, 32 or 64; D is 64, 128, 192 or 256; 1 <= n_kv_heads <= 1024;
+ * 1 <= n_pages < 2^31.  Neither array needs initial values. */
+typedef struct qmv_kv_cache {
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_tokens;
+  int32_t n_pages;
+  void* pages;
+  void* bounds;
+} qmv_kv_cache;
+
+/* A ragged batch over such a cache: sequence s holds lens[s] tokens in the
+ * pages table[s][0 .. ceil(lens[s] / P)) (entries past those are not read),
+ * and its LAST starts[s+1] - starts[s] tokens are this call's: rows starts[s]
+ * .. of q, k or v, at positions lens[s] - (starts[s+1] - starts[s]) ... .
+ * starts NULL: one token per sequence (n_tok = n_seq).
+ *   table int32 [n_seq][max_pages], lens int32 [n_seq], starts int32
+ *   [n_seq + 1] ascending from 0 to n_tok: device memory.
+ *   1 <= n_seq <= QMV_MAX_SEQS, 1 <= n_tok <= QMV_MAX_BATCH_TOKENS (qmv_kv_read:
+ *   2^24), 1 <= max_pages <= 2^20.
+ * The same lens serve qmv_kv_append, qmv_kv_select and qmv_kv_attend of one
+ * step.  What only the device can see is checked there: a page index outside
+ * [0, n_pages) sets QMV_DEVERR_PAGE and its tokens are left out; lens or
+ * starts that contradict n_tok, max_pages or each other set QMV_DEVERR_BATCH
+ * and are clamped.  Rows of tokens that no sequence covers are not written. */
+#define QMV_MAX_SEQS 1024
+#define QMV_MAX_BATCH_TOKENS 65535
+typedef struct qmv_kv_batch {
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* starts;
+  int32_t n_seq;
+  int32_t max_pages;
+  int32_t n_tok;
+  int32_t reserved;
+} qmv_kv_batch;
+
+/* Bytes of one page record / bounds record of one head (negative QMV_ERR_*
+ * for a head_dim or page_tokens that the cache does not take). */
+int64_t qmv_kv_page_bytes(int head_dim, int page_tokens);
+int64_t qmv_kv_bounds_bytes(int head_dim);
+
+/* Writes the batch's keys and values k, v [n_tok][n_kv_heads][D] (tokens
+ * k_stride / v_stride elements apart) into the cache.  Per (page, head), for
+ * keys and values alike, with amax over the call's tokens of the page:
+ *   d' = amax / 127; a page that already holds tokens of the sequence keeps
+ *   d = max(d_old, d'), and if that grew, its codes become
+ *   rne(c * (d_old / d)); new codes are clamp(rne(x * (1 / d)), -127, 127)
+ * (fp32, IEEE round-to-nearest, as the activation rule; the code of 0 * inf
+ * is 0).  The scales and the order of the tokens thus decide every bit.  A
+ * page is begun (its old scale and codes ignored) by the token of its first
+ * slot; a call that writes positions again (after lens went back) keeps the
+ * larger scale, and the bounds then still cover the page's codes.
+ * Two sequences of a call must not append to the same page.  Non-finite k, v
+ * are outside the contract.  Alignment: 16 bytes for k, v and their strides. */
+int qmv_kv_append(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const void* k, int64_t k_stride,
+                  const void* v, int64_t v_stride, cudaStream_t stream);
+
+/* The inverse: the batch's tokens as values, k and v [n_tok][n_kv_heads][D]
+ * in dtype (starts may cover whole sequences; tokens before the sequence's
+ * first or in pages left out are 0). */
+int qmv_kv_read(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, void* k, void* v, cudaStream_t stream);
+
+/* Attention of the batch's tokens over the cache: with pos the token's
+ * position and g the kv head of query head h (h / (n_heads / n_kv_heads)),
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_g[j]) v_g[j]
+ * over the positions j <= pos (causal nonzero) or j < lens (causal 0), with
+ * window > 0 also j > pos - window.  A token that sees nothing gets zeros.
+ * pages int32 [n_tok][n_kv_heads][n_sel] (NULL: all pages): only the page
+ * indices of the sequence listed there for the token and kv head are read
+ * (negative entries are skipped; an index listed twice counts twice).
+ * q [n_tok][n_heads][D] (tokens q_stride elements apart), out
+ * [n_tok][n_heads][D], n_heads a multiple of n_kv_heads.  Keys and values
+ * enter as their exact codes; q and the softmax weights as two f16 parts (22
+ * bits); sums and the softmax statistics are fp32.  The work is cut into equal
+ * shares over the whole batch whatever its lengths, in a grid that does not
+ * depend on them (a captured graph stays valid as lens grow), and joined in a
+ * fixed order: results are bitwise reproducible.
+ * ws: qmv_kv_attend_workspace_bytes(c, n_heads) bytes, any content. */
+size_t qmv_kv_attend_workspace_bytes(const qmv_kv_cache* c, int n_heads);
+int qmv_kv_attend(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const void* q, int64_t q_stride,
+                  void* out, int n_heads, float scale, int causal, int window, const int32_t* pages, int n_sel,
+                  void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Pages worth attending to: for token t and kv head g, from the bounds alone,
+ *   q of each of the head's query heads quantized per head (d_h = amax / 127,
+ *   codes as the activation rule's),
+ *   u_h(page) = sum_i max(q_i * min_i, q_i * max_i)   (int32, exact)
+ *   score(page) = max_h fl(d_h * u_h) * key scale     (fp32)
+ * an upper bound of the page's quantized logits.  ids[t][g][0 .. n_sel) are
+ * the page holding the token's own position and the n_sel - 1 others of the
+ * largest score among the pages before it (equal scores: the lower index),
+ * in ascending order, -1 after the last where there are fewer.  The scores
+ * have no rounding that depends on an order, so neither do the picks.
+ * ids int32 [n_tok][n_kv_heads][n_sel], 1 <= n_sel <= 2^20; the cache has
+ * bounds.  ws: qmv_kv_select_workspace_bytes(c, b) bytes, any content. */
+size_t qmv_kv_select_workspace_bytes(const qmv_kv_cache* c, const qmv_kv_batch* b);
+int qmv_kv_select(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const void* q, int64_t q_stride,
+                  int n_heads, int32_t* ids, int n_sel, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Diagnostic (no counterpart on the pages): the activation quantizer uses
  * branch-free FMA sequences for d = amax / 127 and 1 / d; this compares them

@@ -30,6 +30,8 @@ DEVERR_EXPERT_RANGE = 0x1
 DEVERR_EXPERT_DUP = 0x2
 DEVERR_TIMEOUT = 0x4
 DEVERR_RANGE = 0x8
+DEVERR_PAGE = 0x10
+DEVERR_BATCH = 0x20
 
 
 class QmvError(RuntimeError):
@@ -42,6 +44,17 @@ class MoeExperts(ctypes.Structure):
     _fields_ = [("n_experts", ctypes.c_int32), ("hidden", ctypes.c_int32), ("ffn", ctypes.c_int32),
                 ("fmt_gate_up", ctypes.c_int32), ("fmt_down", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("w_gate_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("pages", ctypes.c_void_p), ("bounds", ctypes.c_void_p)]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("n_seq", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_tok", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _i64, _vp, _int, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -65,6 +78,18 @@ _SIGS = {
     "moe_route_run": (_int, [_int, _vp, _vp, _int, _i64, _int, _int, _int, _vp, _vp, _vp, _vp]),
     "qmv_run_residual": (_int, [_int, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _vp, _sz, _vp]),
     "qmv_run_siblings": (_int, [_int, _vp, _vp, _vp, _vp, _vp, _i64, _int, _vp, _sz, _vp]),
+    "qmv_rms_norm": (_int, [_int, _vp, _i64, _vp, _vp, ctypes.c_float, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qmv_dequantize_act": (_int, [_int, _vp, _vp, _i64, _i64, _vp, _vp]),
+    "qmv_kv_page_bytes": (_i64, [_int, _int]),
+    "qmv_kv_bounds_bytes": (_i64, [_int]),
+    "qmv_kv_append": (_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), _int, _vp, _i64, _vp, _i64, _vp]),
+    "qmv_kv_read": (_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), _int, _vp, _vp, _vp]),
+    "qmv_kv_attend_workspace_bytes": (_sz, [ctypes.POINTER(KvCache), _int]),
+    "qmv_kv_attend": (_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), _int, _vp, _i64, _vp, _int,
+                             ctypes.c_float, _int, _int, _vp, _int, _vp, _sz, _vp]),
+    "qmv_kv_select_workspace_bytes": (_sz, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch)]),
+    "qmv_kv_select": (_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), _int, _vp, _i64, _int, _vp, _int,
+                             _vp, _sz, _vp]),
     "qmv_get_device_error": (_int, [_vp, ctypes.POINTER(_int)]),
     "qmv_debug_shrink_outputs": (_int, [_i64]),
     "qmv_wait_probe": (_int, [ctypes.c_longlong, _vp, _vp]),
@@ -375,6 +400,232 @@ def route_run(fmt: int, Wr: torch.Tensor, x: torch.Tensor, n_experts: int, hidde
                                 int(gating), _ptr(logits), _ptr(ids), _ptr(gates), _stream(stream)),
            "moe_route_run")
     return ids, gates, logits
+
+
+# ---------------------------------------------------------------------------
+# The attention half of a decode layer
+# ---------------------------------------------------------------------------
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+MAX_SEQS = 1024
+MAX_BATCH_TOKENS = 65535
+
+
+def _dtype(t: torch.Tensor) -> int:
+    dt = DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"float32, float16 or bfloat16 tensor wanted, got {t.dtype}")
+    return dt
+
+
+def _ints(t: torch.Tensor | None):
+    if t is not None and t.dtype != torch.int32:
+        raise ValueError(f"int32 tensor wanted, got {t.dtype}")
+    return _ptr(t)
+
+
+def _typed(t: torch.Tensor | None, dtype: torch.dtype, shape, what: str):
+    """The address of a contiguous CUDA tensor of this type and shape."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: {dtype} {tuple(shape)} wanted, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _rows(t: torch.Tensor, what: str):
+    """The address and token stride of [n_tok][heads][D], heads and dimensions contiguous."""
+    if not t.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    n, h, d = t.shape
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{what}: the heads and dimensions of a token must be contiguous")
+    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+
+
+def rms_norm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, r: torch.Tensor | None = None, want: str = "float",
+             y: torch.Tensor | None = None, q8=None, res: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm with the residual's addition (qmv_rms_norm): s = x + r,
+    y = s / sqrt(mean(s^2) + eps) * w per row.  x [n][K] (rows may be strided), r like x
+    or None, w fp32 [K].  want: "float" (y in x's type), "q8" (y in the library's Q8
+    activation layout, for run_q8) or "both".  Returns (y, (q, d, s), res), None for what
+    was not asked for (res = s in x's type: only with r); y, q8 and res may be given as
+    outputs, res also as r itself."""
+    if want not in ("float", "q8", "both"):
+        raise ValueError(f"want is 'float', 'q8' or 'both', got {want!r}")
+    n, K = x.shape
+    dt, dev = _dtype(x), x.device
+    if not x.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    if K > 1 and x.stride(1) != 1:
+        raise ValueError("x: the values of a row must be contiguous")
+    if y is None and want != "q8":
+        y = torch.empty((n, K), dtype=x.dtype, device=dev)
+    if q8 is None and want != "float":
+        if K % 256:
+            raise QmvError(-2, "qmv_rms_norm")
+        q8 = (torch.empty((n, K), dtype=torch.int8, device=dev),
+              torch.empty((n, K // 32), dtype=torch.float32, device=dev),
+              torch.empty((n, K // 32), dtype=torch.int32, device=dev))
+    if res is None and r is not None:
+        res = torch.empty((n, K), dtype=x.dtype, device=dev)
+    q, d, s = q8 if q8 is not None else (None, None, None)
+    _check(load().qmv_rms_norm(dt, x.data_ptr(), x.stride(0) if n > 1 else K, _typed(r, x.dtype, (n, K), "r"),
+                               _typed(w, torch.float32, (K,), "w"), eps, n, K, _typed(res, x.dtype, (n, K), "res"),
+                               _typed(y, x.dtype, (n, K), "y"), _typed(q, torch.int8, (n, K), "q8"),
+                               _typed(d, torch.float32, (n, K // 32), "q8"),
+                               _typed(s, torch.int32, (n, K // 32), "q8"), _stream(stream)), "qmv_rms_norm")
+    return y, q8, res
+
+
+def dequantize_act(q: torch.Tensor, d: torch.Tensor, dtype: torch.dtype = torch.float32,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values [n][K] that Q8 activations (q, d of quantize_act or rms_norm) stand for."""
+    n, K = q.shape
+    if out is None:
+        out = torch.empty((n, K), dtype=dtype, device=q.device)
+    _check(load().qmv_dequantize_act(_dtype(out), _typed(q, torch.int8, (n, K), "q"),
+                                     _typed(d, torch.float32, (n, K // 32), "d"), n, K,
+                                     _typed(out, out.dtype, (n, K), "out"), _stream(stream)), "qmv_dequantize_act")
+    return out
+
+
+def kv_page_bytes(head_dim: int, page_tokens: int) -> int:
+    n = load().qmv_kv_page_bytes(int(head_dim), int(page_tokens))
+    _check(n if n < 0 else 0, "qmv_kv_page_bytes")
+    return int(n)
+
+
+def kv_bounds_bytes(head_dim: int) -> int:
+    n = load().qmv_kv_bounds_bytes(int(head_dim))
+    _check(n if n < 0 else 0, "qmv_kv_bounds_bytes")
+    return int(n)
+
+
+def kv_cache(n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int, pages: torch.Tensor | None = None,
+             bounds: torch.Tensor | bool | None = None, device=None) -> KvCache:
+    """The descriptor of a paged 8-bit key / value cache (qmv_kv_cache).  pages uint8
+    [n_pages][n_kv_heads][kv_page_bytes] and bounds uint8 [n_pages][n_kv_heads]
+    [kv_bounds_bytes] are made where not given (bounds: only for True).  It holds
+    references to both tensors (`.page_tensor`, `.bounds_tensor`)."""
+    pb = kv_page_bytes(head_dim, page_tokens)
+    if n_kv_heads < 1 or n_pages < 1:
+        raise QmvError(-2, "kv_cache")
+    if pages is None:
+        pages = torch.empty((n_pages, n_kv_heads, pb), dtype=torch.uint8, device=device or "cuda")
+    if bounds is True:
+        bounds = torch.empty((n_pages, n_kv_heads, kv_bounds_bytes(head_dim)), dtype=torch.uint8, device=pages.device)
+    elif bounds is False:
+        bounds = None
+    c = KvCache(n_kv_heads, head_dim, page_tokens, n_pages,
+                _typed(pages, torch.uint8, (n_pages, n_kv_heads, pb), "pages"),
+                _typed(bounds, torch.uint8, (n_pages, n_kv_heads, kv_bounds_bytes(head_dim)), "bounds"))
+    c.page_tensor, c.bounds_tensor = pages, bounds
+    return c
+
+
+def _batch(table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor | None, n_tok: int) -> KvBatch:
+    n_seq, max_pages = table.shape
+    if lens.numel() != n_seq or (starts is not None and starts.numel() != n_seq + 1):
+        raise ValueError(f"lens [{n_seq}] and starts [{n_seq + 1}] wanted for a table of {n_seq} sequences")
+    return KvBatch(_ints(table), _ints(lens), _ints(starts), n_seq, max_pages, n_tok, 0)
+
+
+def _kv_shape(cache: KvCache, t: torch.Tensor, heads: int, what: str):
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or t.shape[1] != heads:
+        raise ValueError(f"{what}: [n_tok][{heads}][{cache.head_dim}] wanted, got {tuple(t.shape)}")
+
+
+def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+              starts: torch.Tensor | None = None, stream=None) -> None:
+    """Write the last tokens of each sequence into the cache (qmv_kv_append).  k, v
+    [n_tok][n_kv_heads][D] (tokens may be strided); table int32 [n_seq][max_pages], lens
+    int32 [n_seq] counting these tokens, starts int32 [n_seq + 1] (None: one token per
+    sequence)."""
+    _kv_shape(cache, k, cache.n_kv_heads, "k")
+    _kv_shape(cache, v, cache.n_kv_heads, "v")
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must be of one type and length")
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    b = _batch(table, lens, starts, k.shape[0])
+    _check(load().qmv_kv_append(ctypes.byref(cache), ctypes.byref(b), _dtype(k), kp, ks, vp, vs, _stream(stream)),
+           "qmv_kv_append")
+
+
+def kv_read(cache: KvCache, table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor | None = None,
+            n_tok: int | None = None, dtype: torch.dtype = torch.float32, k: torch.Tensor | None = None,
+            v: torch.Tensor | None = None, stream=None):
+    """The last tokens of each sequence as values (qmv_kv_read): (k, v), each
+    [n_tok][n_kv_heads][D].  n_tok is starts[-1] (a host number; None with starts None)."""
+    if n_tok is None:
+        if starts is not None:
+            raise ValueError("n_tok is needed with starts")
+        n_tok = lens.numel()
+    shape = (n_tok, cache.n_kv_heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=table.device)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=table.device)
+    b = _batch(table, lens, starts, n_tok)
+    _check(load().qmv_kv_read(ctypes.byref(cache), ctypes.byref(b), _dtype(k), _typed(k, k.dtype, shape, "k"),
+                              _typed(v, k.dtype, shape, "v"), _stream(stream)), "qmv_kv_read")
+    return k, v
+
+
+def kv_attend_workspace_bytes(cache: KvCache, n_heads: int) -> int:
+    return int(load().qmv_kv_attend_workspace_bytes(ctypes.byref(cache), int(n_heads)))
+
+
+def kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+              starts: torch.Tensor | None = None, scale: float | None = None, causal: bool = True, window: int = 0,
+              pages: torch.Tensor | None = None, ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """Attention of the last tokens of each sequence over the cache (qmv_kv_attend).
+    q [n_tok][n_heads][D] (tokens may be strided), scale 1 / sqrt(D) if None, pages int32
+    [n_tok][n_kv_heads][n_sel] (kv_select's) or None for all.  Returns out like q."""
+    n, heads, D = q.shape
+    _kv_shape(cache, q, heads, "q")
+    if out is None:
+        out = torch.empty((n, heads, D), dtype=q.dtype, device=q.device)
+    if ws is None:
+        ws = torch.empty(max(16, kv_attend_workspace_bytes(cache, heads)), dtype=torch.uint8, device=q.device)
+    n_sel = 0
+    if pages is not None:
+        if pages.dim() != 3 or tuple(pages.shape[:2]) != (n, cache.n_kv_heads):
+            raise ValueError(f"pages: [{n}][{cache.n_kv_heads}][n_sel] wanted, got {tuple(pages.shape)}")
+        n_sel = pages.shape[2]
+    qp, qs = _rows(q, "q")
+    b = _batch(table, lens, starts, n)
+    _check(load().qmv_kv_attend(ctypes.byref(cache), ctypes.byref(b), _dtype(q), qp, qs,
+                                _typed(out, q.dtype, (n, heads, D), "out"), heads,
+                                D ** -0.5 if scale is None else scale, int(causal), int(window), _ints(pages), n_sel,
+                                _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "qmv_kv_attend")
+    return out
+
+
+def kv_select_workspace_bytes(cache: KvCache, n_tok: int, max_pages: int) -> int:
+    b = KvBatch(None, None, None, 1, max_pages, n_tok, 0)
+    return int(load().qmv_kv_select_workspace_bytes(ctypes.byref(cache), ctypes.byref(b)))
+
+
+def kv_select(cache: KvCache, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, n_sel: int,
+              starts: torch.Tensor | None = None, ws: torch.Tensor | None = None, ids: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """The n_sel pages worth attending to for each token and kv head (qmv_kv_select): ids
+    int32 [n_tok][n_kv_heads][n_sel], ascending, -1 after the last; for kv_attend's pages.
+    The cache must have bounds."""
+    n, heads, _ = q.shape
+    _kv_shape(cache, q, heads, "q")
+    if ids is None:
+        ids = torch.empty((n, cache.n_kv_heads, n_sel), dtype=torch.int32, device=q.device)
+    qp, qs = _rows(q, "q")
+    b = _batch(table, lens, starts, n)
+    if ws is None:
+        ws = torch.empty(max(16, kv_select_workspace_bytes(cache, n, b.max_pages)), dtype=torch.uint8, device=q.device)
+    _check(load().qmv_kv_select(ctypes.byref(cache), ctypes.byref(b), _dtype(q), qp, qs, heads,
+                                _typed(ids, torch.int32, (n, cache.n_kv_heads, n_sel), "ids"), n_sel, _ptr(ws),
+                                ws.numel() * ws.element_size(), _stream(stream)), "qmv_kv_select")
+    return ids
 
 
 def check_rounding(stream=None):

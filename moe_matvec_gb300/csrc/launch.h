@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/qmv.h"
+
 namespace qmv {
 
 struct DenseParams;
@@ -79,11 +81,37 @@ cudaError_t launch_splitk_reduce(const float* partial, float* y, const float* ad
 cudaError_t launch_quantize_weights(int fmt, const float* w, long long M, int K, void* W, cudaStream_t stream);
 cudaError_t launch_check_rounding(unsigned long long* bad, cudaStream_t stream);
 
+// Norm (norm.cu): the arguments of qmv_rms_norm; vec: eight values a thread
+// (K and ldx multiples of 8).
+constexpr int NORM_MAX_STEPS = QMV_MAX_NORM / 8 / 1024;
+struct NormParams {
+  const void* x;
+  const void* r;
+  const float* w;
+  void* res;
+  void* y;
+  int8_t* q;
+  float* d;
+  int32_t* s;
+  long long ldx, rows;
+  int K;
+  float eps;
+#ifdef QMV_DEBUG
+  unsigned* err;
+  long long x_len, n, out_len;
+#endif
+};
+cudaError_t launch_rms_norm(int dtype, const NormParams& p, bool vec, cudaStream_t stream, bool pdl);
+cudaError_t launch_act_dequant(int dtype, const int8_t* q, const float* d, long long n, void* out, cudaStream_t stream,
+                               bool pdl);
+
 // 2-D TMA map over `rows` rows of `row_bytes` bytes (8-byte elements), box
 // box_rows x box_bytes; false if the driver's encoder is unavailable or
 // rejects the arguments.
 bool encode_rows(CUtensorMap* map, const void* W, long long rows, long long row_bytes, int box_bytes, int box_rows);
 
+// QMV_OK if the current device is one this library runs on, else QMV_ERR_*.
+int check_device();
 // Maximum dynamic shared memory a CTA may use on the current device.
 int device_smem_optin();
 unsigned* device_error_word();  // address of the device error word (current device)

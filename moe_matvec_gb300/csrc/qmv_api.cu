@@ -132,7 +132,7 @@ constexpr long long MAX_K = 1ll << 20;
 constexpr long long FLOAT_ACT_BYTES = 96 * 1024;
 constexpr long long MAX_M = 1ll << 30;
 
-static int check_device() {
+int check_device() {
   const DevInfo* d = dev_info();
   if (!d) return QMV_ERR_CUDA;
   if (d->major != 10 || d->minor != 3) return QMV_ERR_DEVICE;

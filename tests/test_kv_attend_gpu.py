@@ -1,0 +1,293 @@
+"""Attention over the paged 8-bit cache, and page selection, against 64 bits.
+
+Tolerance of an fp32 output: with A the largest |scale| max|q| sum|k| of the
+row, a logit is off by at most 2^-23 A from q's two f16 parts, 16 * 2^-23 A from
+the products' fp32 sums and 2^-22 A from the scaling; the softmax weight by
+twice that (its own and the maximum's share of the sum).  Weights and their
+f16 parts add 2^-21, and sums of up to a few hundred fp32 terms 2^-17 of
+sum p |v|.  In all |out - out64| <= (2^-17 A + 2^-16) sum p |v|, plus half a unit
+of the output's type.  Picks are whole numbers and have to be equal."""
+import numpy as np
+import pytest
+import torch
+
+from moe_matvec_gb300 import api
+from tests import kv_ref
+from tests.test_kv_cache_gpu import Pair, dev32, randn, tables
+
+pytestmark = pytest.mark.gpu
+
+UNIT = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+DT = list(UNIT)
+
+
+def filled(rng, H, D, P, lens, n_pages=None, scale=1.0):
+    """A cache holding lens[s] random tokens per sequence; unused pages and slots hold 0xFF (scales NaN)."""
+    n_pages = n_pages or sum(-(-n // P) for n in lens) + 3
+    pair = Pair(H, D, P, n_pages)
+    table = tables(rng, lens, P, n_pages)
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    if starts[-1]:
+        step = 16384
+        assert starts[-1] <= step
+        k, v = randn(rng, starts[-1], H, D, scale=scale), randn(rng, starts[-1], H, D)
+        pair.append(k, v, table, lens, starts)
+        pair.check()
+    return pair, table
+
+
+def check(pair, q, table, lens, starts, out, scale=None, **kw):
+    D = q.shape[2]
+    scale = D ** -0.5 if scale is None else scale
+    st = np.arange(len(lens) + 1) if starts is None else np.asarray(starts)
+    want, mag, arg = kv_ref.attend(pair.ref, q.float().cpu().numpy(), table, lens, st, scale, **kw)
+    got = out.double().cpu().numpy()
+    bound = (2.0 ** -17 * arg + 2.0 ** -16) * mag + UNIT[out.dtype] * np.abs(want) + (2.0 ** -25 if out.dtype == torch.float16 else 1e-38)
+    err = np.abs(got - want)
+    assert np.isfinite(got).all()
+    assert (err <= bound).all(), f"worst {np.max(err / bound)} of the bound"
+    assert api.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("P", [16, 32, 64])
+def test_single_tokens_ragged_lengths(lib, dtype, D, P):
+    rng = np.random.default_rng(D * P)
+    lens = [1, 0, P - 1, P, P + 1, 63, 64, 65, 127, 200, 777]
+    pair, table = filled(rng, 2, D, P, lens)
+    q = randn(rng, len(lens), 6, D, dtype=dtype, scale=2)
+    out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens))
+    assert (out[1] == 0).all()
+    check(pair, q, table, lens, None, out)
+
+
+@pytest.mark.parametrize("H,G", [(1, 1), (2, 3), (1, 7), (3, 8), (1, 9), (2, 16), (1, 33), (8, 1)])
+def test_head_groups(lib, H, G):
+    rng = np.random.default_rng(H * 100 + G)
+    lens = [130, 5, 300]
+    pair, table = filled(rng, H, 128, 32, lens)
+    q = randn(rng, 3, H * G, 128)
+    check(pair, q, table, lens, None, api.kv_attend(pair.dev, q, dev32(table), dev32(lens)))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [0, 1, 17, 64, 100])
+def test_several_tokens_masks_and_windows(lib, causal, window):
+    rng = np.random.default_rng(window + causal)
+    lens, news = [150, 9, 40, 0, 300], [5, 9, 1, 0, 21]
+    st = np.concatenate([[0], np.cumsum(news)])
+    for D, P, G in ((64, 16, 4), (128, 64, 3)):
+        pair, table = filled(rng, 2, D, P, lens)
+        q = randn(rng, st[-1], 2 * G, D, scale=1.5)
+        out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), dev32(st), causal=causal, window=window)
+        check(pair, q, table, lens, st, out, causal=causal, window=window)
+
+
+def test_a_whole_prompt(lib):
+    rng = np.random.default_rng(30)
+    lens = [260, 33]
+    st = [0, 260, 293]
+    pair, table = filled(rng, 2, 64, 64, lens)
+    q = randn(rng, 293, 8, 64)
+    check(pair, q, table, lens, st, api.kv_attend(pair.dev, q, dev32(table), dev32(lens), dev32(st)))
+
+
+@pytest.mark.parametrize("n_seq,length", [(1, 9000), (3, 5000), (70, 150), (300, 40)])
+def test_long_and_many_sequences(lib, n_seq, length):
+    rng = np.random.default_rng(n_seq)
+    lens = [int(v) for v in rng.integers(1, length, n_seq)]
+    lens[0] = length
+    pair, table = filled(rng, 1, 128, 64, lens)
+    q = randn(rng, n_seq, 4, 128, scale=3)
+    out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens))
+    check(pair, q, table, lens, None, out)
+    # bitwise reproducible
+    assert torch.equal(out, api.kv_attend(pair.dev, q, dev32(table), dev32(lens)))
+
+
+def test_peaked_and_extreme_logits(lib):
+    rng = np.random.default_rng(31)
+    lens = [500, 500, 500]
+    pair, table = filled(rng, 1, 128, 64, lens, scale=8)
+    q = randn(rng, 3, 8, 128)
+    q[0] *= 100     # one token takes all the weight
+    q[1] = 0        # uniform weights
+    q[2] *= 1e-20
+    for scale in (None, 0.0, -0.3, 5.0):
+        out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), scale=scale)
+        check(pair, q, table, lens, None, out, scale=scale)
+
+
+def test_pages_of_very_different_scales(lib):
+    # an outlier page a thousand times larger than its neighbours
+    rng = np.random.default_rng(32)
+    H, D, P = 1, 128, 16
+    pair = Pair(H, D, P, 20)
+    table = tables(rng, [200], P, 20)
+    k, v = randn(rng, 200, H, D), randn(rng, 200, H, D)
+    v[48:64] *= 1000
+    v[64:80] *= 1e-3
+    k[80:96] = 0
+    v[96:112] = 0
+    pair.append(k, v, table, [200], [0, 200])
+    q = randn(rng, 1, 5, D)
+    check(pair, q, table, [200], None, api.kv_attend(pair.dev, q, dev32(table), dev32([200])))
+
+
+def test_strided_queries_and_given_buffers(lib):
+    rng = np.random.default_rng(33)
+    lens = [100, 77]
+    pair, table = filled(rng, 2, 128, 32, lens)
+    fused = randn(rng, 2, 12, 128)
+    q = fused[:, 2:10]
+    ws = torch.full((api.kv_attend_workspace_bytes(pair.dev, 8),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full((2, 8, 128), float("nan"), device="cuda")
+    r = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), ws=ws, out=out)
+    assert r is out
+    check(pair, q, table, lens, None, out)
+
+
+def test_non_finite_rows_stay_their_own(lib):
+    rng = np.random.default_rng(34)
+    lens = [90, 70]
+    pair, table = filled(rng, 1, 64, 16, lens)
+    q = randn(rng, 2, 4, 64)
+    bad = q.clone()
+    bad[0, 1, 3] = float("nan")
+    a = api.kv_attend(pair.dev, q, dev32(table), dev32(lens))
+    b = api.kv_attend(pair.dev, bad, dev32(table), dev32(lens))
+    keep = torch.ones(2, 4, dtype=torch.bool)
+    keep[0, 1] = False
+    assert torch.equal(a[keep.cuda()], b[keep.cuda()]) and b[0, 1].isnan().all()
+
+
+def test_missing_pages_are_left_out_and_flagged(lib):
+    rng = np.random.default_rng(35)
+    pair, table = filled(rng, 1, 64, 16, [80, 20])
+    q = randn(rng, 2, 2, 64)
+    bad = table.copy()
+    bad[0, 2] = -1
+    bad[0, 3] = 1000
+    out = api.kv_attend(pair.dev, q, dev32(bad), dev32([80, 20]))
+    assert api.get_device_error() == api.DEVERR_PAGE
+    only = dev32(np.array([[[0, 1, 4]], [[0, 1, -1]]]))
+    assert torch.equal(out, api.kv_attend(pair.dev, q, dev32(table), dev32([80, 20]), pages=only)) or torch.allclose(
+        out, api.kv_attend(pair.dev, q, dev32(table), dev32([80, 20]), pages=only), rtol=1e-5, atol=1e-6)
+    assert api.get_device_error() == 0
+
+
+def test_graph_replays_as_lengths_grow(lib):
+    rng = np.random.default_rng(36)
+    H, D, P = 2, 128, 64
+    pair = Pair(H, D, P, 12)
+    table = tables(rng, [200, 300], P, 12)
+    lens = dev32([100, 130])
+    pair.append(randn(rng, 230, H, D), randn(rng, 230, H, D), table, [100, 130], [0, 100, 230])
+    k, v, q = randn(rng, 2, H, D), randn(rng, 2, H, D), randn(rng, 2, 8, D)
+    td = dev32(table)
+    ws = torch.empty(api.kv_attend_workspace_bytes(pair.dev, 8), dtype=torch.uint8, device="cuda")
+    out = torch.empty(2, 8, D, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        api.kv_attend(pair.dev, q, td, lens, ws=ws, out=out)  # first launches configure the kernel
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            lens.add_(1)
+            api.kv_append(pair.dev, k, v, td, lens)
+            api.kv_attend(pair.dev, q, td, lens, ws=ws, out=out)
+    torch.cuda.synchronize()
+    for step in range(1, 6):
+        k.copy_(randn(rng, 2, H, D))
+        v.copy_(randn(rng, 2, H, D, scale=step))
+        g.replay()
+        torch.cuda.synchronize()
+        now = [100 + step, 130 + step]
+        pair.ref.append(k.cpu().numpy(), v.cpu().numpy(), table, now, [0, 1, 2])
+        assert np.array_equal(pair.dev.page_tensor.cpu().numpy(), pair.ref.pages)
+        check(pair, q, table, now, None, out)
+
+
+# ---------------------------------------------------------------- selection
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D,P,G", [(64, 16, 1), (128, 32, 4), (192, 16, 3), (256, 64, 8)])
+def test_picks_are_the_definitions(lib, dtype, D, P, G):
+    rng = np.random.default_rng(D + G)
+    lens = [1, P, 12 * P + 3, 40 * P - 1, 0]
+    pair, table = filled(rng, 2, D, P, lens)
+    q = randn(rng, len(lens), 2 * G, D, dtype=dtype)
+    for n_sel in (1, 2, 5, 12, 13, 39, 64):
+        ids = api.kv_select(pair.dev, q, dev32(table), dev32(lens), n_sel).cpu().numpy()
+        want = kv_ref.select(pair.ref, q.float().cpu().numpy(), table, lens, np.arange(len(lens) + 1), n_sel)
+        assert np.array_equal(ids, want)
+        out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), pages=dev32(ids))
+        check(pair, q, table, lens, None, out, pages=ids)
+
+
+def test_ties_go_to_the_lower_page(lib):
+    rng = np.random.default_rng(41)
+    H, D, P = 1, 64, 16
+    pair = Pair(H, D, P, 700)
+    n = 690 * P
+    table = tables(rng, [n], P, 700)
+    few = randn(rng, 5 * P, H, D)
+    k = few.repeat(138, 1, 1)  # every page has 137 twins
+    pair.append(k, k, table, [n], [0, n])
+    for q in (randn(rng, 1, 3, D), torch.zeros(1, 3, D, device="cuda")):
+        for n_sel in (2, 100, 139, 400):
+            ids = api.kv_select(pair.dev, q, dev32(table), dev32([n]), n_sel).cpu().numpy()
+            assert np.array_equal(ids, kv_ref.select(pair.ref, q.cpu().numpy(), table, [n], [0, 1], n_sel))
+
+
+def test_picks_of_several_tokens(lib):
+    rng = np.random.default_rng(42)
+    H, D, P = 2, 128, 16
+    lens, news = [130, 47, 300], [3, 20, 1]
+    st = np.concatenate([[0], np.cumsum(news)])
+    pair, table = filled(rng, H, D, P, lens)
+    q = randn(rng, st[-1], 4, D)
+    ids = api.kv_select(pair.dev, q, dev32(table), dev32(lens), 3, dev32(st)).cpu().numpy()
+    assert np.array_equal(ids, kv_ref.select(pair.ref, q.cpu().numpy(), table, lens, st, 3))
+    for window in (0, 20):
+        out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), dev32(st), window=window, pages=dev32(ids))
+        check(pair, q, table, lens, st, out, window=window, pages=ids)
+
+
+def test_bounds_are_upper_bounds_of_the_quantized_logits(lib):
+    # score(page) >= max over the page's tokens and the group's heads of d_h dk (codes . codes)
+    rng = np.random.default_rng(43)
+    H, D, P, n = 1, 128, 32, 400
+    pair, table = filled(rng, H, D, P, [n])
+    q = randn(rng, 1, 4, D)
+    ids = api.kv_select(pair.dev, q, dev32(table), dev32([n]), 4).cpu().numpy()[0, 0]
+    best = np.full(-(-n // P), -np.inf)
+    bound = np.full(-(-n // P), -np.inf)
+    for g in range(4):
+        x = q[0, g].cpu().numpy()
+        d = np.abs(x).max() / np.float32(127)
+        c = kv_ref.rule(x, d)
+        for pg in range(-(-n // P)):
+            k, _ = pair.ref.codes(table[0, pg], 0)
+            dk, low, top = pair.ref.extremes(table[0, pg], 0)
+            m = min(P, n - pg * P)
+            best[pg] = max(best[pg], (k[:m] @ c).max() * float(d) * float(dk))
+            bound[pg] = max(bound[pg], np.maximum(c * low, c * top).sum() * float(d) * float(dk))
+    assert (best <= bound * (1 + 1e-6) + 1e-6).all()
+    assert ids[-1] == (n - 1) // P and len(set(ids)) == 4
+
+
+def test_pages_listed_by_the_caller(lib):
+    rng = np.random.default_rng(44)
+    lens = [200, 90]
+    pair, table = filled(rng, 2, 64, 16, lens)
+    q = randn(rng, 2, 6, 64)
+    # unordered, with gaps, past the sequence, none at all
+    ids = np.array([[[5, -1, 2, 11], [-1, -1, -1, -1]], [[0, 1, -1, 12], [3, -1, -1, 4]]], np.int32)
+    out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), pages=dev32(ids))
+    check(pair, q, table, lens, None, out, pages=ids)
+    assert (out[0, 3:] == 0).all()
+    far = ids.copy()
+    far[0, 0, 0] = 10_000_000  # no page of the table
+    api.kv_attend(pair.dev, q, dev32(table), dev32(lens), pages=dev32(far))
+    assert api.get_device_error() == api.DEVERR_PAGE
