@@ -8,10 +8,15 @@
 // lengths and single long sequences fill the GPU alike, and an item that
 // crosses shares leaves partial results that a second kernel joins in order.
 //
-// In a CTA one producer warp brings each tile's page records (scales, K and V
-// codes: one bulk copy per page) into a ring of stages; the tiles go to the
-// consumer warps in turn, each warp with its own running maximum, sum and
-// accumulator, merged when the share leaves the item.
+// In a CTA the tiles go to the consumer warps in turn, each warp with its own
+// running maximum, sum and accumulator, merged when the share leaves the item.
+// The page records of a tile (scales, K and V codes: one bulk copy per page)
+// land in a ring of stages.  A planner warp works out ahead which records the
+// tiles need (32 tiles at a time, a lane each) into a ring of plans; the warp
+// that has emptied a stage starts the copies of the tile that comes into it
+// next.  So no thread waits for stages to become free, and the fixed cost of a
+// copy (about 300 ns for one thread that waits, posts the bytes and copies,
+// against 350 ns of HBM time for a 16 KB tile) is spread over the warps.
 //
 // A consumer's arithmetic (mma.sync m16n8k16, f16 operands, fp32 sums): the
 // rows of A are 8 query rows in two f16 parts, q = hi + lo, rows 0-7 hi and
@@ -36,22 +41,30 @@
 namespace qmv {
 
 constexpr int AT_TILE = 64;        // tokens of a unit
-constexpr int AT_MAX_STAGES = 32;  // the producer looks ahead by its 32 lanes
+constexpr int AT_MAX_STAGES = 32;  // the planner stays 32 to 64 tiles ahead
+constexpr int AT_PLANS = 64;       // ring of plans, in two halves
 constexpr int AT_MAX_CTAS = 320;
 constexpr int AT_MAX_MT = 1;
-constexpr float AT_P_SCALE = 16384.f;  // softmax weights enter f16 times 2^14, far from its subnormals
+// Softmax weights enter f16 times 2^6 and may exceed 1 by 2^8 (a running
+// maximum is only followed when it is left behind by more than that) and, by
+// the reference scale, by 2: below 2^15, and 22 bits down to 2^-9 of the
+// largest, an error of 2^-31 of it below that.
+constexpr float AT_P_SCALE = 64.f;
+constexpr float AT_LAZY = 8.f;
 
-// Consumer warps beside the producer warp: as many as the registers of q and
-// the accumulators allow (the four quarters of an SM hold whole warps: 12
-// warps of up to 168 registers a thread, or 8 of up to 255)
-__host__ __device__ constexpr int at_warps(int D) { return D > 128 ? 7 : 11; }
+// Consumer warps beside the planner warp.  The quarters of an SM hold whole
+// warps: 8 of up to 255 registers a thread, or 12 of up to 168.  Eight: their
+// registers let the two products' loads, conversions and MMAs of a warp
+// overlap, and the stages outnumber the warps (32 x 8192 tokens of head_dim
+// 128: 75 us, against 86 with eleven consumers, which held every stage).
+constexpr int AT_WARPS = 7;
 // shared-memory bytes from one page record to the next: a lane's V piece of
 // page c / (P / 16) must fall into another bank group than its neighbours'
 __host__ __device__ constexpr int at_rec_stride(int D, int P) {
   return kv_page_bytes(D, P) + (P == 16 ? 16 : P == 32 ? 48 : 0);
 }
 __host__ __device__ constexpr int at_stage_bytes(int D, int P) { return AT_TILE / P * at_rec_stride(D, P); }
-__host__ __device__ constexpr int at_merge_floats(int D, int MT) { return at_warps(D) * 8 * MT * (D + 8 + 2); }
+__host__ __device__ constexpr int at_merge_floats(int D, int MT) { return AT_WARPS * 8 * MT * (D + 8 + 2); }
 
 // A partial result in the workspace: m and l of each row, then the rows.
 __host__ __device__ constexpr int at_slot_floats(int D, int MT) { return 8 * MT * (D + 2); }
@@ -134,6 +147,15 @@ __device__ __forceinline__ AttendItem locate(const AttendParams& p, const long l
   return it;
 }
 
+// What a tile is made of: for each of its pages the record's index in the
+// cache (page * H + head, below 2^41) or -1, and the page's index in the
+// sequence or -1.
+struct AttendPlan {
+  long long rec[4];
+  int idx[4];
+  uint32_t bytes, pad[3];
+};
+
 // Position of row r's token (the row space of `it`).
 __device__ __forceinline__ int row_pos(const AttendParams& p, const AttendItem& it, const KvSeq& q, int r) {
   return q.len - q.n + (it.tbase - q.t0) + r / p.G;
@@ -166,17 +188,18 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
+// the same with a zero sum to start from
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Four consecutive values of a float tensor of type dt.
@@ -191,33 +214,36 @@ __device__ __forceinline__ void store4(void* base, long long at, int dt, const f
   else store_vec<4>(static_cast<__nv_bfloat16*>(base) + at, v);
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__((at_warps(D) + 1) * 32, 1) kv_attend_kernel(const AttendParams p) {
-  constexpr int W = at_warps(D), R = 8 * MT, KS = D / 16, NV = D / 8, MSTRIDE = D + 8;
+template <int D, int P, int MT>
+__global__ void __launch_bounds__((AT_WARPS + 1) * 32, 1) kv_attend_kernel(const AttendParams p) {
+  constexpr int W = AT_WARPS, R = 8 * MT, KS = D / 16, NV = D / 8, MSTRIDE = D + 8;
+  constexpr int ppt = AT_TILE / P, rec_stride = at_rec_stride(D, P), stage_bytes = ppt * rec_stride;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int P = p.kv.P, ppt = AT_TILE / P, S = p.stages, n_seq = p.kv.n_seq;
-  const int rec_stride = at_rec_stride(D, P), stage_bytes = ppt * rec_stride;
+  const int S = p.stages, n_seq = p.kv.n_seq;
   // stages | merge rows | merge stats | meta | barriers | prefix sums | sequences
   uint8_t* cur = smem + (size_t)S * stage_bytes;
   float* merge = reinterpret_cast<float*>(cur);
   float* mstat = merge + W * R * MSTRIDE;  // [W][R][2]
   cur += at_merge_floats(D, MT) * sizeof(float);
-  int* meta = reinterpret_cast<int*>(cur);  // [S][4]: the sequence's page index of each page of the tile, or -1
-  cur += S * 16;
+  AttendPlan* plans = reinterpret_cast<AttendPlan*>(cur);
+  cur += AT_PLANS * sizeof(AttendPlan);
   uint64_t* full = reinterpret_cast<uint64_t*>(cur);
-  uint64_t* empty = full + S;
-  cur += 2 * S * sizeof(uint64_t);
+  cur += AT_PLANS * sizeof(uint64_t);
   long long* base = reinterpret_cast<long long*>(cur);
   KvSeq* seqs = reinterpret_cast<KvSeq*>(base + n_seq + 1);
   __shared__ long long wtot[W + 1];
+  __shared__ uint64_t plan_full[2], plan_done[2];  // of the halves of the ring of plans
+  __shared__ int stop;                             // a wait ran out: no copy is started any more
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   if (tid == 0) {
-    for (int i = 0; i < S; i++) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    for (int i = 0; i < AT_PLANS; i++) mbar_init(&full[i], 1);
+    for (int i = 0; i < 2; i++) {
+      mbar_init(&plan_full[i], 1);
+      mbar_init(&plan_done[i], AT_PLANS / 2);
     }
+    stop = 0;
     fence_mbar_init();
   }
   pdl_wait();
@@ -261,22 +287,22 @@ __global__ void __launch_bounds__((at_warps(D) + 1) * 32, 1) kv_attend_kernel(co
   if (tid == 0) base[n_seq] = total;
   __syncthreads();
 
+  const int units = (int)(u1 - u0);
   if (warp == W) {
-    // ---- producer: lane i prepares unit u + i, then the copies go out in order
-    const uint64_t policy = policy_evict_first();
-    for (long long ub = u0; ub < u1; ub += 32) {
-      const long long u = ub + lane;
-      int page[4] = {-1, -1, -1, -1}, idx[4] = {-1, -1, -1, -1};
-      int head = 0;
-      uint32_t bytes = 0;
-      if (u < u1) {
-        const AttendItem it = locate<MT>(p, base, seqs, u);
+    // ---- planner: lane i plans unit 32 b + i of the share
+    for (int b = 0; 32 * b < units; b++) {
+      AttendPlan plan;
+      plan.bytes = 0;
+#pragma unroll
+      for (int i = 0; i < 4; i++) plan.rec[i] = plan.idx[i] = -1;
+      if (32 * b + lane < units) {
+        const AttendItem it = locate<MT>(p, base, seqs, u0 + 32 * b + lane);
         const KvSeq q = seqs[it.s];
-        head = it.head;
         const int rows = min(it.row0 + R, it.nrows) - 1;
         // positions that some row of the item may see: [vis0, vis1)
         const int vis1 = p.causal ? row_pos(p, it, q, rows) + 1 : it.len;
         const int vis0 = p.window > 0 ? row_pos(p, it, q, it.row0) - p.window + 1 : 0;
+#pragma unroll
         for (int i = 0; i < ppt; i++) {
           int pg;
           if (p.sel) {
@@ -296,47 +322,61 @@ __global__ void __launch_bounds__((at_warps(D) + 1) * 32, 1) kv_attend_kernel(co
           if (pg < 0 || pos >= vis1 || pos >= it.len || pos + P <= vis0) continue;
           const int id = kv_page(p.kv, it.s, pg);
           if (id < 0) continue;
-          page[i] = id;
-          idx[i] = pg;
-          bytes += kv_page_bytes(D, P);
+          plan.rec[i] = (long long)id * p.kv.H + it.head;
+          plan.idx[i] = pg;
+          plan.bytes += kv_page_bytes(D, P);
         }
       }
-      bool dead = false;
-      for (int i = 0; i < 32; i++) {
-        if (lane == i && u < u1 && !dead) {
-          const long long n = u - u0;
-          const int st = (int)(n % S);
-          const uint32_t use = (uint32_t)(n / S);
-          if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1, p.kv.err)) dead = true;
-          if (!dead) {
-            *reinterpret_cast<int4*>(meta + 4 * st) = make_int4(idx[0], idx[1], idx[2], idx[3]);
-            mbar_arrive_expect_tx(&full[st], bytes);
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-              if (page[k] < 0) continue;
-              const long long at = ((long long)page[k] * p.kv.H + head) * kv_page_bytes(D, P);
-              uint8_t* dst = smem + (size_t)st * stage_bytes + k * rec_stride;
-              if (QMV_CHECK(in_range(at, kv_page_bytes(D, P), p.kv.pages_len, p.kv.err)) &&
-                  QMV_CHECK(smem_in_range(dst, kv_page_bytes(D, P), p.kv.err)))
-                bulk_copy_g2s_hint(dst, p.kv.pages + at, kv_page_bytes(D, P), &full[st], policy);
-              else
-                mbar_complete_tx(&full[st], kv_page_bytes(D, P));
-            }
-          }
-        }
-        __syncwarp();
-        dead = __any_sync(0xffffffffu, dead);
-      }
-      if (dead) break;
+      if (b >= 2 && !mbar_wait(&plan_done[b & 1], (b / 2 - 1) & 1, p.kv.err)) break;
+      plans[(32 * b + lane) % AT_PLANS] = plan;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&plan_full[b & 1]);
     }
     return;
   }
 
   // ---- consumers
   const int r = lane >> 2, c = lane & 3;
-  const uint32_t smem0 = smem_u32(smem);
+  const uint64_t policy = policy_evict_first();
   bool dead = false;
+  // Barriers are waited for by parity, so a warp may wait for a phase only once
+  // the phase before it is known to be complete.  The tiles' barriers belong to
+  // the plans (unit m: plan and barrier m % 64), not to the stages, whose
+  // successive tiles different warps wait for: when unit m's half of the plans
+  // is posted, every unit of the half's former content has been consumed, unit
+  // m - 64 among them; and the halves are posted in order, a warp that works on
+  // one having seen the one before.
+  auto planned = [&](int m) {
+    if (mbar_wait(&plan_full[(m >> 5) & 1], (m >> 6) & 1, p.kv.err)) return true;
+    dead = true;
+    stop = 1;
+    return false;
+  };
+  // Starts the copies of unit m of the share into stage t, which nothing reads
+  // any more (by whole warps; lane 0 posts the bytes and copies).
+  auto fill = [&](int m, int t) {
+    if (!planned(m)) return;
+    if (lane == 0 && *const_cast<volatile int*>(&stop) == 0) {
+      const AttendPlan& plan = plans[m % AT_PLANS];
+      uint64_t* const bar = &full[m % AT_PLANS];
+      mbar_arrive_expect_tx(bar, plan.bytes);
+      constexpr uint32_t rb = kv_page_bytes(D, P);
+#pragma unroll
+      for (int k = 0; k < ppt; k++) {
+        if (plan.rec[k] < 0) continue;
+        const long long at = plan.rec[k] * rb;
+        uint8_t* dst = smem + t * stage_bytes + k * rec_stride;
+        if (QMV_CHECK(in_range(at, rb, p.kv.pages_len, p.kv.err)) && QMV_CHECK(smem_in_range(dst, rb, p.kv.err)))
+          bulk_copy_g2s_hint(dst, p.kv.pages + at, rb, bar, policy);
+        else
+          mbar_complete_tx(bar, rb);
+      }
+    }
+  };
+  for (int m = warp; m < min(S, units) && !dead; m += W) fill(m, m);
   long long u = u0;
+  int n = warp, st = warp % S;  // the warp's next unit of the share and its stage
+  const int st_step = W % S;
   while (u < u1) {
     const AttendItem it = locate<MT>(p, base, seqs, u);
     const KvSeq sq = seqs[it.s];
@@ -368,11 +408,13 @@ __global__ void __launch_bounds__((at_warps(D) + 1) * 32, 1) kv_attend_kernel(co
       // two f16 parts hold 22 bits of it
       const int e = min(max((int)(__float_as_uint(amax) >> 23), 1), 253);
       const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
-      qs[mt] = __uint_as_float((uint32_t)e << 23) * p.scale_log2;
+      // (the sign of the scale goes into q: a larger product is then a larger logit)
+      const float down1 = p.scale_log2 < 0.f ? -down : down;
+      qs[mt] = __uint_as_float((uint32_t)e << 23) * fabsf(p.scale_log2);
 #pragma unroll
       for (int k = 0; k < KS; k++) {
-        split_f16(v[k][0] * down, v[k][1] * down, qa[mt][k][0], qa[mt][k][1]);
-        split_f16(v[k][2] * down, v[k][3] * down, qa[mt][k][2], qa[mt][k][3]);
+        split_f16(v[k][0] * down1, v[k][1] * down1, qa[mt][k][0], qa[mt][k][1]);
+        split_f16(v[k][2] * down1, v[k][3] * down1, qa[mt][k][2], qa[mt][k][3]);
       }
     }
     float o[MT][NV][4], m[MT], l[MT], vref = 0.f;
@@ -384,18 +426,21 @@ __global__ void __launch_bounds__((at_warps(D) + 1) * 32, 1) kv_attend_kernel(co
       for (int n = 0; n < NV; n++) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
     }
 
-    const int first = (int)(u - u0);  // the share's unit number of the segment's first tile
-    for (int i = (warp - first % W + W) % W; i < seg; i += W) {
-      const int n = first + i, st = n % S;
-      if (!dead && !mbar_wait(&full[st], (uint32_t)(n / S) & 1, p.kv.err)) dead = true;
-      if (dead) break;
-      const uint32_t stage = smem0 + st * stage_bytes;
+    const int seg_end = (int)(u - u0) + seg;
+    for (; n < seg_end && !dead; n += W) {
+      if (!planned(n)) break;
+      if (!mbar_wait(&full[n % AT_PLANS], (n / AT_PLANS) & 1, p.kv.err)) {
+        dead = true;
+        stop = 1;
+        break;
+      }
+      const uint8_t* stage = smem + st * stage_bytes;
       // the lane's 16 tokens: a piece of one page
-      const int sub = 16 * c / P, idx = meta[4 * st + sub];
-      const uint32_t rec = stage + sub * rec_stride;
+      const int sub = 16 * c / P, idx = plans[n % AT_PLANS].idx[sub];
+      const uint8_t* rec = stage + sub * rec_stride;
       float dk = 0.f, dv = 0.f;
       if (idx >= 0) {
-        const float2 sc = *reinterpret_cast<const float2*>(smem + (size_t)st * stage_bytes + sub * rec_stride);
+        const float2 sc = *reinterpret_cast<const float2*>(rec);
         dk = sc.x;
         dv = sc.y;
       }
@@ -405,73 +450,96 @@ __global__ void __launch_bounds__((at_warps(D) + 1) * 32, 1) kv_attend_kernel(co
       float s[MT][8][2];
       {
         const int ksub = 16 * (r >> 1) / P, kt = (16 * (r >> 1)) % P + (r & 1);
-        const uint32_t krow = stage + ksub * rec_stride + KV_HEADER + kt * 64 + 16 * c;
+        const uint8_t* krow = stage + ksub * rec_stride + KV_HEADER + kt * 64 + 16 * c;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
           float acc[MT][4];
 #pragma unroll
-          for (int mt = 0; mt < MT; mt++) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
-#pragma unroll
           for (int h = 0; h < D / 64; h++) {
-            const uint4 kw = lds128(krow + h * P * 64 + j * 128);
+            const uint4 kw = *reinterpret_cast<const uint4*>(krow + h * P * 64 + j * 128);
             const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {
               uint32_t b0, b1;
               codes_to_f16(w[k], b0, b1);
 #pragma unroll
-              for (int mt = 0; mt < MT; mt++) mma16816(acc[mt], qa[mt][4 * h + k], b0, b1);
+              for (int mt = 0; mt < MT; mt++) {
+                if (h == 0 && k == 0) mma16816_first(acc[mt], qa[mt][0], b0, b1);
+                else mma16816(acc[mt], qa[mt][4 * h + k], b0, b1);
+              }
             }
           }
 #pragma unroll
           for (int mt = 0; mt < MT; mt++) {
-            const float f = qs[mt] * dk;
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-              const int pos = pos0 + 2 * j + e;
-              s[mt][j][e] = pos < lim[mt] && pos >= low[mt] ? (acc[mt][e] + acc[mt][2 + e]) * f : -INFINITY;
-            }
+            s[mt][j][0] = acc[mt][0] + acc[mt][2];
+            s[mt][j][1] = acc[mt][1] + acc[mt][3];
           }
         }
       }
-      // values share one reference scale per warp, the largest so far
+      // tiles at an end of some row's range: products out of it become -inf
+      bool inside = true;
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++) inside = inside && pos0 >= low[mt] && pos0 + 16 <= lim[mt];
+      if (!__all_sync(0xffffffffu, inside)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+              if (pos0 + 2 * j + e >= lim[mt] || pos0 + 2 * j + e < low[mt]) s[mt][j][e] = -INFINITY;
+          }
+        }
+      }
+      // values share one reference scale per warp: raised when a page's is over twice it
       float vmax = fmaxf(dv, __shfl_xor_sync(0xffffffffu, dv, 1));
-      vmax = fmaxf(fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2)), vref);
-      const float vfix = vmax > 0.f ? vref / vmax : 1.f;
-      const float vrel = vmax > 0.f ? dv / vmax * AT_P_SCALE : 0.f;
-      vref = vmax;
+      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+      float vfix = 1.f;
+      if (vmax > 2.f * vref) {
+        vfix = vref / vmax;
+        vref = vmax;
+      }
+      const float vrel = vref > 0.f ? __fdividef(dv, vref) * AT_P_SCALE : 0.f;
       uint32_t pa[MT][4][4];
 #pragma unroll
       for (int mt = 0; mt < MT; mt++) {
-        float mx = -INFINITY;
+        // the lane's 16 products share one factor to logits in powers of two
+        // (not 0: a masked product is -inf)
+        const float f = fmaxf(qs[mt] * dk, 0x1p-120f);
+        float mx = s[mt][0][0];
 #pragma unroll
         for (int j = 0; j < 8; j++) mx = fmaxf(mx, fmaxf(s[mt][j][0], s[mt][j][1]));
+        mx *= f;
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[mt], mx), ms = mn == -INFINITY ? 0.f : mn;
-        const float alpha = ex2(m[mt] - ms), fix = alpha * vfix;
-        m[mt] = mn;
-        l[mt] *= alpha;
+        float fix = vfix;
+        if (mx > m[mt] + AT_LAZY || (m[mt] == -INFINITY && mx > m[mt])) {
+          const float alpha = ex2(m[mt] - mx);
+          fix *= alpha;
+          l[mt] *= alpha;
+          m[mt] = mx;
+        }
         if (__any_sync(0xffffffffu, fix != 1.f)) {
 #pragma unroll
           for (int n2 = 0; n2 < NV; n2++) {
             o[mt][n2][0] *= fix, o[mt][n2][1] *= fix, o[mt][n2][2] *= fix, o[mt][n2][3] *= fix;
           }
         }
+        const float ms = m[mt] == -INFINITY ? 0.f : m[mt];
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-          const float a = ex2(s[mt][j][0] - ms), b = ex2(s[mt][j][1] - ms);
+          const float a = ex2(fmaf(s[mt][j][0], f, -ms)), b = ex2(fmaf(s[mt][j][1], f, -ms));
           sum += a + b;
           split_f16(a * vrel, b * vrel, pa[mt][j >> 1][2 * (j & 1)], pa[mt][j >> 1][2 * (j & 1) + 1]);
         }
         l[mt] += sum;
       }
       // O += P V: k-step kk holds tokens 16 c + 4 kk .. + 3
-      const uint32_t vrow = rec + KV_HEADER + P * D + r * P + (16 * c) % P;
+      const uint8_t* vrow = rec + KV_HEADER + P * D + r * P + (16 * c) % P;
 #pragma unroll
       for (int n2 = 0; n2 < NV; n2++) {
-        const uint4 vw = lds128(vrow + n2 * 8 * P);
+        const uint4 vw = *reinterpret_cast<const uint4*>(vrow + n2 * 8 * P);
         const uint32_t w[4] = {vw.x, vw.y, vw.z, vw.w};
 #pragma unroll
         for (int kk = 0; kk < 4; kk++) {
@@ -482,7 +550,10 @@ __global__ void __launch_bounds__((at_warps(D) + 1) * 32, 1) kv_attend_kernel(co
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (lane == 0) mbar_arrive(&plan_done[(n >> 5) & 1]);
+      if (n + S < units) fill(n + S, st);
+      st += st_step;
+      if (st >= S) st -= S;
     }
 
     // ---- the warps' results of the segment, merged in warp order
@@ -555,6 +626,13 @@ __global__ void __launch_bounds__((at_warps(D) + 1) * 32, 1) kv_attend_kernel(co
     named_sync(1, W * 32);  // the merge area may be written again
     u += seg;
   }
+  // After a wait that ran out, copies that nobody waits for may be in flight:
+  // the CTA keeps its shared memory a while longer than any copy takes.
+  if (*const_cast<volatile int*>(&stop)) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 1 << 24) {
+    }
+  }
 }
 
 // Joins the partial results of the item that begins in CTA c's share and ends
@@ -598,11 +676,11 @@ size_t kv_attend_ws_bytes(int D) {
   return (size_t)AT_MAX_CTAS * (sizeof(AttendJoin) + 2 * at_slot_floats(D, AT_MAX_MT) * sizeof(float));
 }
 
-template <int D, int MT>
+template <int D, int P, int MT>
 static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
   const size_t fixed = at_merge_floats(D, MT) * sizeof(float) + (size_t)(p.kv.n_seq + 1) * sizeof(long long) +
-                       (size_t)p.kv.n_seq * sizeof(KvSeq) + 256;
-  const size_t per_stage = at_stage_bytes(D, p.kv.P) + 16 + 2 * sizeof(uint64_t);
+                       (size_t)p.kv.n_seq * sizeof(KvSeq) + AT_PLANS * (sizeof(AttendPlan) + sizeof(uint64_t)) + 256;
+  const size_t per_stage = at_stage_bytes(D, P);
   int stages = (int)(((size_t)device_smem_optin() - 1024 - fixed) / per_stage);
   if (stages > AT_MAX_STAGES) stages = AT_MAX_STAGES;
   if (stages < 2) return cudaErrorInvalidConfiguration;
@@ -613,7 +691,7 @@ static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(configured.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(kv_attend_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(kv_attend_kernel<D, P, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              device_smem_optin() - 1024);
     if (e != cudaSuccess) return e;
     configured.fetch_or(1ull << dev);
@@ -621,11 +699,20 @@ static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
   const int sms = device_sm_count(), grid = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  make_config(cfg, attr, dim3(grid), dim3((at_warps(D) + 1) * 32), smem, stream, true);
-  e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<D, MT>, p);
+  make_config(cfg, attr, dim3(grid), dim3((AT_WARPS + 1) * 32), smem, stream, true);
+  e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<D, P, MT>, p);
   if (e != cudaSuccess) return e;
   make_config(cfg, attr, dim3(grid, 8 * MT), dim3(D / 4), 0, stream, true);
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, MT>, p);
+}
+
+template <int D>
+static cudaError_t launch_attend_d(AttendParams& p, cudaStream_t stream) {
+  switch (p.kv.P) {
+    case 16: return launch_attend<D, 16, 1>(p, stream);
+    case 32: return launch_attend<D, 32, 1>(p, stream);
+    default: return launch_attend<D, 64, 1>(p, stream);
+  }
 }
 
 cudaError_t launch_kv_attend(const KvParams& kv, int D, const AttendArgs& a, cudaStream_t stream) {
@@ -648,10 +735,10 @@ cudaError_t launch_kv_attend(const KvParams& kv, int D, const AttendArgs& a, cud
                  p.out_len = output_extent((long long)kv.n_tok * a.n_heads * D);
                  p.sel_len = a.sel ? (long long)kv.n_tok * kv.H * a.n_sel : 0;)
   switch (D) {
-    case 64: return launch_attend<64, 1>(p, stream);
-    case 128: return launch_attend<128, 1>(p, stream);
-    case 192: return launch_attend<192, 1>(p, stream);
-    default: return launch_attend<256, 1>(p, stream);
+    case 64: return launch_attend_d<64>(p, stream);
+    case 128: return launch_attend_d<128>(p, stream);
+    case 192: return launch_attend_d<192>(p, stream);
+    default: return launch_attend_d<256>(p, stream);
   }
 }
 

@@ -291,3 +291,31 @@ def test_pages_listed_by_the_caller(lib):
     far[0, 0, 0] = 10_000_000  # no page of the table
     api.kv_attend(pair.dev, q, dev32(table), dev32(lens), pages=dev32(far))
     assert api.get_device_error() == api.DEVERR_PAGE
+
+
+@pytest.mark.parametrize("D,P,H,n_seq,length", [(128, 64, 4, 40, 9000), (64, 16, 8, 40, 6000), (256, 32, 2, 24, 6000)])
+def test_shares_of_many_tiles(lib, D, P, H, n_seq, length):
+    # a hundred tiles and more per SM: every stage, plan and barrier is used again and again
+    g = torch.Generator().manual_seed(D)
+    rng = np.random.default_rng(D)
+    lens = [int(v) for v in rng.integers(length // 2, length, n_seq)]
+    pages = [-(-n // P) for n in lens]
+    cache = api.kv_cache(H, D, P, sum(pages))
+    table = tables(rng, lens, P, sum(pages))
+    td, ld = dev32(table), dev32(lens)
+    for s in range(n_seq):
+        k, v = (torch.randn(lens[s], H, D, generator=g).cuda() for _ in range(2))
+        api.kv_append(cache, k, v, td[s:s + 1].clone(), dev32(lens[s:s + 1]), dev32([0, lens[s]]))
+    q = torch.randn(n_seq, 4 * H, D, generator=g).cuda()
+    first = api.kv_attend(cache, q, td, ld)
+    for _ in range(10):
+        assert torch.equal(first, api.kv_attend(cache, q, td, ld))
+    for s in range(0, n_seq, 7):
+        k, v = (t.double() for t in api.kv_read(cache, td[s:s + 1].clone(), dev32(lens[s:s + 1]), dev32([0, lens[s]]), lens[s]))
+        for h in range(H):
+            x = q[s, 4 * h:4 * h + 4].double()
+            p = torch.softmax(x @ k[:, h].T / D ** 0.5, -1)
+            want, mag = p @ v[:, h], p @ v[:, h].abs()
+            arg = (x.abs().amax(1) * k[:, h].abs().sum(1).max() / D ** 0.5)[:, None]
+            assert ((first[s, 4 * h:4 * h + 4] - want).abs() <= (2.0 ** -17 * arg + 2.0 ** -16) * mag).all()
+    assert api.get_device_error() == 0
