@@ -167,9 +167,17 @@ def _check(rc: int, what: str):
         raise QmvError(rc, what)
 
 
+# The current stream's handle without building a Stream object (3 us a call on
+# the Grace host, as long as the kernel launch itself).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _ptr(t: torch.Tensor | None):
@@ -418,7 +426,9 @@ def _dtype(t: torch.Tensor) -> int:
 
 
 def _ints(t: torch.Tensor | None):
-    if t is not None and t.dtype != torch.int32:
+    if t is None:
+        return None
+    if t.dtype is not torch.int32:
         raise ValueError(f"int32 tensor wanted, got {t.dtype}")
     return _ptr(t)
 
@@ -427,9 +437,17 @@ def _typed(t: torch.Tensor | None, dtype: torch.dtype, shape, what: str):
     """The address of a contiguous CUDA tensor of this type and shape."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what}: {dtype} {tuple(shape)} wanted, got {t.dtype} {tuple(t.shape)}")
     return _ptr(t)
+
+
+def _out(t: torch.Tensor | None, dtype: torch.dtype, shape, like: torch.Tensor, what: str) -> torch.Tensor:
+    """A given result tensor, checked, or a new one on like's device."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _typed(t, dtype, shape, what)
+    return t
 
 
 def _rows(t: torch.Tensor, what: str):
@@ -437,9 +455,10 @@ def _rows(t: torch.Tensor, what: str):
     if not t.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
     n, h, d = t.shape
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+    st, sh, sd = t.stride()
+    if sd != 1 or (h > 1 and sh != d):
         raise ValueError(f"{what}: the heads and dimensions of a token must be contiguous")
-    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+    return t.data_ptr(), st if n > 1 else h * d
 
 
 def rms_norm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, r: torch.Tensor | None = None, want: str = "float",
@@ -452,28 +471,32 @@ def rms_norm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, r: torch.Tenso
     outputs, res also as r itself."""
     if want not in ("float", "q8", "both"):
         raise ValueError(f"want is 'float', 'q8' or 'both', got {want!r}")
-    n, K = x.shape
-    dt, dev = _dtype(x), x.device
+    n, K = shape = x.shape
+    dt, t = _dtype(x), x.dtype
     if not x.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
-    if K > 1 and x.stride(1) != 1:
+    ld, one = x.stride()
+    if K > 1 and one != 1:
         raise ValueError("x: the values of a row must be contiguous")
-    if y is None and want != "q8":
-        y = torch.empty((n, K), dtype=x.dtype, device=dev)
-    if q8 is None and want != "float":
-        if K % 256:
-            raise QmvError(-2, "qmv_rms_norm")
-        q8 = (torch.empty((n, K), dtype=torch.int8, device=dev),
-              torch.empty((n, K // 32), dtype=torch.float32, device=dev),
-              torch.empty((n, K // 32), dtype=torch.int32, device=dev))
-    if res is None and r is not None:
-        res = torch.empty((n, K), dtype=x.dtype, device=dev)
-    q, d, s = q8 if q8 is not None else (None, None, None)
-    _check(load().qmv_rms_norm(dt, x.data_ptr(), x.stride(0) if n > 1 else K, _typed(r, x.dtype, (n, K), "r"),
-                               _typed(w, torch.float32, (K,), "w"), eps, n, K, _typed(res, x.dtype, (n, K), "res"),
-                               _typed(y, x.dtype, (n, K), "y"), _typed(q, torch.int8, (n, K), "q8"),
-                               _typed(d, torch.float32, (n, K // 32), "q8"),
-                               _typed(s, torch.int32, (n, K // 32), "q8"), _stream(stream)), "qmv_rms_norm")
+    if y is not None or want != "q8":
+        y = _out(y, t, shape, x, "y")
+    qp = dp = sp = None
+    if q8 is not None or want != "float":
+        if q8 is None:
+            if K % 256:
+                raise QmvError(-2, "qmv_rms_norm")
+            dev = x.device
+            q8 = (torch.empty(shape, dtype=torch.int8, device=dev),
+                  torch.empty((n, K // 32), dtype=torch.float32, device=dev),
+                  torch.empty((n, K // 32), dtype=torch.int32, device=dev))
+        q, d, s = q8
+        qp = _typed(q, torch.int8, shape, "q8")
+        dp, sp = _typed(d, torch.float32, (n, K // 32), "q8"), _typed(s, torch.int32, (n, K // 32), "q8")
+    if res is not None or r is not None:
+        res = _out(res, t, shape, x, "res")
+    _check(load().qmv_rms_norm(dt, x.data_ptr(), ld if n > 1 else K, _typed(r, t, shape, "r"),
+                               _typed(w, torch.float32, (K,), "w"), eps, n, K, _ptr(res), _ptr(y), qp, dp, sp,
+                               _stream(stream)), "qmv_rms_norm")
     return y, q8, res
 
 
@@ -525,13 +548,13 @@ def kv_cache(n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int, pag
 
 def _batch(table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor | None, n_tok: int) -> KvBatch:
     n_seq, max_pages = table.shape
-    if lens.numel() != n_seq or (starts is not None and starts.numel() != n_seq + 1):
+    if lens.shape != (n_seq,) or (starts is not None and starts.shape != (n_seq + 1,)):
         raise ValueError(f"lens [{n_seq}] and starts [{n_seq + 1}] wanted for a table of {n_seq} sequences")
     return KvBatch(_ints(table), _ints(lens), _ints(starts), n_seq, max_pages, n_tok, 0)
 
 
 def _kv_shape(cache: KvCache, t: torch.Tensor, heads: int, what: str):
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or t.shape[1] != heads:
+    if t.dim() != 3 or t.shape[1:] != (heads, cache.head_dim):
         raise ValueError(f"{what}: [n_tok][{heads}][{cache.head_dim}] wanted, got {tuple(t.shape)}")
 
 
@@ -583,21 +606,20 @@ def kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, lens: torch.
     """Attention of the last tokens of each sequence over the cache (qmv_kv_attend).
     q [n_tok][n_heads][D] (tokens may be strided), scale 1 / sqrt(D) if None, pages int32
     [n_tok][n_kv_heads][n_sel] (kv_select's) or None for all.  Returns out like q."""
-    n, heads, D = q.shape
+    n, heads, D = shape = q.shape
     _kv_shape(cache, q, heads, "q")
-    if out is None:
-        out = torch.empty((n, heads, D), dtype=q.dtype, device=q.device)
+    out = _out(out, q.dtype, shape, q, "out")
     if ws is None:
         ws = torch.empty(max(16, kv_attend_workspace_bytes(cache, heads)), dtype=torch.uint8, device=q.device)
     n_sel = 0
     if pages is not None:
-        if pages.dim() != 3 or tuple(pages.shape[:2]) != (n, cache.n_kv_heads):
+        if pages.dim() != 3 or pages.shape[:2] != (n, cache.n_kv_heads):
             raise ValueError(f"pages: [{n}][{cache.n_kv_heads}][n_sel] wanted, got {tuple(pages.shape)}")
         n_sel = pages.shape[2]
     qp, qs = _rows(q, "q")
     b = _batch(table, lens, starts, n)
     _check(load().qmv_kv_attend(ctypes.byref(cache), ctypes.byref(b), _dtype(q), qp, qs,
-                                _typed(out, q.dtype, (n, heads, D), "out"), heads,
+                                out.data_ptr(), heads,
                                 D ** -0.5 if scale is None else scale, int(causal), int(window), _ints(pages), n_sel,
                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "qmv_kv_attend")
     return out

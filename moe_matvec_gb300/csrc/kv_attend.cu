@@ -40,11 +40,15 @@
 
 namespace qmv {
 
+#ifndef AT_W
+#define AT_W(D, MT) ((D) > 192 ? 6 : 7)
+#define AT_SP(D, MT) ((D) > 192 ? 2 : 1)
+#endif
 constexpr int AT_TILE = 64;        // tokens of a unit
 constexpr int AT_MAX_STAGES = 32;  // the planner stays 32 to 64 tiles ahead
 constexpr int AT_PLANS = 64;       // ring of plans, in two halves
 constexpr int AT_MAX_CTAS = 320;
-constexpr int AT_MAX_MT = 1;
+constexpr int AT_MAX_MT = 2;
 // Softmax weights enter f16 times 2^6 and may exceed 1 by 2^8 (a running
 // maximum is only followed when it is left behind by more than that) and, by
 // the reference scale, by 2: below 2^15, and 22 bits down to 2^-9 of the
@@ -52,19 +56,18 @@ constexpr int AT_MAX_MT = 1;
 constexpr float AT_P_SCALE = 64.f;
 constexpr float AT_LAZY = 8.f;
 
-// Consumer warps beside the planner warp.  The quarters of an SM hold whole
-// warps: 8 of up to 255 registers a thread, or 12 of up to 168.  Eight: their
-// registers let the two products' loads, conversions and MMAs of a warp
-// overlap, and the stages outnumber the warps (32 x 8192 tokens of head_dim
-// 128: 75 us, against 86 with eleven consumers, which held every stage).
-constexpr int AT_WARPS = 7;
+// Consumer warps beside the planner warp, and how many of them share a tile
+// (each takes 64 / at_split of its tokens).  The quarters of an SM hold whole
+// warps: 8 of up to 255 registers a thread, 12 of up to 168 or 16 of up to 128.
+__host__ __device__ constexpr int at_warps(int D, int MT) { return AT_W(D, MT); }
+__host__ __device__ constexpr int at_split(int D, int MT) { return AT_SP(D, MT); }
 // shared-memory bytes from one page record to the next: a lane's V piece of
 // page c / (P / 16) must fall into another bank group than its neighbours'
 __host__ __device__ constexpr int at_rec_stride(int D, int P) {
   return kv_page_bytes(D, P) + (P == 16 ? 16 : P == 32 ? 48 : 0);
 }
 __host__ __device__ constexpr int at_stage_bytes(int D, int P) { return AT_TILE / P * at_rec_stride(D, P); }
-__host__ __device__ constexpr int at_merge_floats(int D, int MT) { return AT_WARPS * 8 * MT * (D + 8 + 2); }
+__host__ __device__ constexpr int at_merge_floats(int D, int MT) { return at_warps(D, MT) * 8 * MT * (D + 8 + 2); }
 
 // A partial result in the workspace: m and l of each row, then the rows.
 __host__ __device__ constexpr int at_slot_floats(int D, int MT) { return 8 * MT * (D + 2); }
@@ -92,7 +95,7 @@ struct AttendParams {
 
 struct AttendItem {
   int s, tbase, nrows, row0, head;  // rows row0 .. of the item's row space; row r: token tbase + r / G
-  int n, len;                       // of the sequence
+  int len;                          // of the sequence
   int tile0, tiles;                 // first tile, units
   int k;                            // the unit asked for
 };
@@ -142,14 +145,36 @@ __device__ __forceinline__ AttendItem locate(const AttendParams& p, const long l
     it.tbase = q.t0;
   }
   it.s = lo;
-  it.n = seqs[lo].n;
   it.len = seqs[lo].len;
   return it;
 }
 
-// What a tile is made of: for each of its pages the record's index in the
-// cache (page * H + head, below 2^41) or -1, and the page's index in the
-// sequence or -1.
+// The item after `it`, from its first unit.
+template <int MT>
+__device__ __forceinline__ void next_item(const AttendParams& p, const KvSeq* seqs, AttendItem& it) {
+  it.k = 0;
+  it.row0 += 8 * MT;
+  if (it.row0 < it.nrows) return;
+  it.row0 = 0;
+  if (++it.head < p.kv.H) return;
+  it.head = 0;
+  if (p.sel) {
+    it.tbase++;
+    while (it.s + 1 < p.kv.n_seq && seqs[it.s + 1].t0 <= it.tbase) it.s++;
+  } else {
+    do {
+      if (++it.s >= p.kv.n_seq) return;  // there is none: the caller is at its last unit
+    } while (seqs[it.s].n == 0);
+    const KvSeq q = seqs[it.s];
+    seq_tiles(p, q, it.tile0, it.tiles);
+    it.nrows = q.n * p.G;
+    it.tbase = q.t0;
+  }
+  it.len = seqs[it.s].len;
+}
+
+// What a tile is made of: for each of its pages the record's byte offset in
+// the cache or -1, and the page's index in the sequence or -1.
 struct AttendPlan {
   long long rec[4];
   int idx[4];
@@ -176,6 +201,19 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& a, uint32_t& 
   const __half2 hy = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
   a = *reinterpret_cast<const uint32_t*>(&hx);
   b = *reinterpret_cast<const uint32_t*>(&hy);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 // (x, y) as two f16 pairs, hi + lo
@@ -215,8 +253,9 @@ __device__ __forceinline__ void store4(void* base, long long at, int dt, const f
 }
 
 template <int D, int P, int MT>
-__global__ void __launch_bounds__((AT_WARPS + 1) * 32, 1) kv_attend_kernel(const AttendParams p) {
-  constexpr int W = AT_WARPS, R = 8 * MT, KS = D / 16, NV = D / 8, MSTRIDE = D + 8;
+__global__ void __launch_bounds__((at_warps(D, MT) + 1) * 32, 1) kv_attend_kernel(const AttendParams p) {
+  constexpr int W = at_warps(D, MT), SP = at_split(D, MT), NG = W / SP, NJ = 8 / SP;
+  constexpr int R = 8 * MT, KS = D / 16, NV = D / 8, MSTRIDE = D + 8;
   constexpr int ppt = AT_TILE / P, rec_stride = at_rec_stride(D, P), stage_bytes = ppt * rec_stride;
   extern __shared__ __align__(128) uint8_t smem[];
   const int S = p.stages, n_seq = p.kv.n_seq;
@@ -322,7 +361,7 @@ __global__ void __launch_bounds__((AT_WARPS + 1) * 32, 1) kv_attend_kernel(const
           if (pg < 0 || pos >= vis1 || pos >= it.len || pos + P <= vis0) continue;
           const int id = kv_page(p.kv, it.s, pg);
           if (id < 0) continue;
-          plan.rec[i] = (long long)id * p.kv.H + it.head;
+          plan.rec[i] = ((long long)id * p.kv.H + it.head) * kv_page_bytes(D, P);
           plan.idx[i] = pg;
           plan.bytes += kv_page_bytes(D, P);
         }
@@ -346,8 +385,13 @@ __global__ void __launch_bounds__((AT_WARPS + 1) * 32, 1) kv_attend_kernel(const
   // is posted, every unit of the half's former content has been consumed, unit
   // m - 64 among them; and the halves are posted in order, a warp that works on
   // one having seen the one before.
+  int posted = -1;  // the last half (of 32 units) known to be posted
   auto planned = [&](int m) {
-    if (mbar_wait(&plan_full[(m >> 5) & 1], (m >> 6) & 1, p.kv.err)) return true;
+    if (m >> 5 <= posted) return true;
+    if (mbar_wait(&plan_full[(m >> 5) & 1], (m >> 6) & 1, p.kv.err)) {
+      posted = m >> 5;
+      return true;
+    }
     dead = true;
     stop = 1;
     return false;
@@ -363,8 +407,8 @@ __global__ void __launch_bounds__((AT_WARPS + 1) * 32, 1) kv_attend_kernel(const
       constexpr uint32_t rb = kv_page_bytes(D, P);
 #pragma unroll
       for (int k = 0; k < ppt; k++) {
-        if (plan.rec[k] < 0) continue;
-        const long long at = plan.rec[k] * rb;
+        const long long at = plan.rec[k];
+        if (at < 0) continue;
         uint8_t* dst = smem + t * stage_bytes + k * rec_stride;
         if (QMV_CHECK(in_range(at, rb, p.kv.pages_len, p.kv.err)) && QMV_CHECK(smem_in_range(dst, rb, p.kv.err)))
           bulk_copy_g2s_hint(dst, p.kv.pages + at, rb, bar, policy);
@@ -373,12 +417,15 @@ __global__ void __launch_bounds__((AT_WARPS + 1) * 32, 1) kv_attend_kernel(const
       }
     }
   };
-  for (int m = warp; m < min(S, units) && !dead; m += W) fill(m, m);
+  // SP warps form a group that works on one tile at a time
+  const int group = warp / SP, part = warp % SP;
+  if (part == 0)
+    for (int m = group; m < min(S, units) && !dead; m += NG) fill(m, m);
   long long u = u0;
-  int n = warp, st = warp % S;  // the warp's next unit of the share and its stage
-  const int st_step = W % S;
-  while (u < u1) {
-    const AttendItem it = locate<MT>(p, base, seqs, u);
+  int n = group, st = group % S;  // the group's next unit of the share and its stage
+  const int st_step = NG % S;
+  AttendItem it = locate<MT>(p, base, seqs, u);
+  for (; u < u1; next_item<MT>(p, seqs, it)) {
     const KvSeq sq = seqs[it.s];
     const int seg = (int)min((long long)(it.tiles - it.k), u1 - u);  // units of this item in the share
     // q of the lane's rows as A fragments
@@ -427,131 +474,137 @@ __global__ void __launch_bounds__((AT_WARPS + 1) * 32, 1) kv_attend_kernel(const
     }
 
     const int seg_end = (int)(u - u0) + seg;
-    for (; n < seg_end && !dead; n += W) {
-      if (!planned(n)) break;
-      if (!mbar_wait(&full[n % AT_PLANS], (n / AT_PLANS) & 1, p.kv.err)) {
+    for (; n < seg_end; n += NG) {
+      if (!dead && planned(n) && !mbar_wait(&full[n % AT_PLANS], (n / AT_PLANS) & 1, p.kv.err)) {
         dead = true;
         stop = 1;
-        break;
       }
-      const uint8_t* stage = smem + st * stage_bytes;
-      // the lane's 16 tokens: a piece of one page
-      const int sub = 16 * c / P, idx = plans[n % AT_PLANS].idx[sub];
-      const uint8_t* rec = stage + sub * rec_stride;
-      float dk = 0.f, dv = 0.f;
-      if (idx >= 0) {
-        const float2 sc = *reinterpret_cast<const float2*>(rec);
-        dk = sc.x;
-        dv = sc.y;
-      }
-      const int pos0 = idx < 0 ? INT_MAX - 64 : idx * P + (16 * c) % P;
+      // a warp whose wait ran out computes nothing more, but keeps meeting the
+      // others at the barriers
+      if (!dead) {
+        const uint8_t* stage = smem + st * stage_bytes;
+        // the lane's 16 tokens: a piece of one page
+        const int sub = 16 * c / P, idx = plans[n % AT_PLANS].idx[sub];
+        const uint8_t* rec = stage + sub * rec_stride;
+        float dk = 0.f, dv = 0.f;
+        if (idx >= 0) {
+          const float2 sc = *reinterpret_cast<const float2*>(rec);
+          dk = sc.x;
+          dv = sc.y;
+        }
+        // (of them the warp's: 2 NJ from 16 c + 2 NJ part on)
+        const int pos0 = idx < 0 ? INT_MAX - 64 : idx * P + (16 * c) % P + 2 * NJ * part;
 
-      // S = q K^T, group j: tokens 16 c + 2 j, + 1 of row r
-      float s[MT][8][2];
-      {
-        const int ksub = 16 * (r >> 1) / P, kt = (16 * (r >> 1)) % P + (r & 1);
-        const uint8_t* krow = stage + ksub * rec_stride + KV_HEADER + kt * 64 + 16 * c;
+        // S = q K^T, group j: tokens 2 j, 2 j + 1 of the lane's, row r
+        float s[MT][NJ][2];
+        {
+          const int ksub = 16 * (r >> 1) / P, kt = (16 * (r >> 1)) % P + (r & 1);
+          const uint8_t* krow = stage + ksub * rec_stride + KV_HEADER + kt * 64 + 16 * c + 128 * NJ * part;
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          float acc[MT][4];
+          for (int j = 0; j < NJ; j++) {
+            float acc[MT][4];
 #pragma unroll
-          for (int h = 0; h < D / 64; h++) {
-            const uint4 kw = *reinterpret_cast<const uint4*>(krow + h * P * 64 + j * 128);
-            const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+            for (int h = 0; h < D / 64; h++) {
+              const uint4 kw = *reinterpret_cast<const uint4*>(krow + h * P * 64 + j * 128);
+              const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-              uint32_t b0, b1;
-              codes_to_f16(w[k], b0, b1);
+              for (int k = 0; k < 4; k++) {
+                uint32_t b0, b1;
+                codes_to_f16(w[k], b0, b1);
 #pragma unroll
-              for (int mt = 0; mt < MT; mt++) {
-                if (h == 0 && k == 0) mma16816_first(acc[mt], qa[mt][0], b0, b1);
-                else mma16816(acc[mt], qa[mt][4 * h + k], b0, b1);
+                for (int mt = 0; mt < MT; mt++) {
+                  if (h == 0 && k == 0) mma16816_first(acc[mt], qa[mt][0], b0, b1);
+                  else mma16816(acc[mt], qa[mt][4 * h + k], b0, b1);
+                }
               }
             }
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) {
+              s[mt][j][0] = acc[mt][0] + acc[mt][2];
+              s[mt][j][1] = acc[mt][1] + acc[mt][3];
+            }
           }
+        }
+        // tiles at an end of some row's range: products out of it become -inf
+        bool inside = true;
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) inside = inside && pos0 >= low[mt] && pos0 + 2 * NJ <= lim[mt];
+        if (!__all_sync(0xffffffffu, inside)) {
 #pragma unroll
           for (int mt = 0; mt < MT; mt++) {
-            s[mt][j][0] = acc[mt][0] + acc[mt][2];
-            s[mt][j][1] = acc[mt][1] + acc[mt][3];
+#pragma unroll
+            for (int j = 0; j < NJ; j++) {
+#pragma unroll
+              for (int e = 0; e < 2; e++)
+                if (pos0 + 2 * j + e >= lim[mt] || pos0 + 2 * j + e < low[mt]) s[mt][j][e] = -INFINITY;
+            }
           }
         }
-      }
-      // tiles at an end of some row's range: products out of it become -inf
-      bool inside = true;
-#pragma unroll
-      for (int mt = 0; mt < MT; mt++) inside = inside && pos0 >= low[mt] && pos0 + 16 <= lim[mt];
-      if (!__all_sync(0xffffffffu, inside)) {
+        // values share one reference scale per warp: raised when a page's is over twice it
+        float vmax = fmaxf(dv, __shfl_xor_sync(0xffffffffu, dv, 1));
+        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+        float vfix = 1.f;
+        if (vmax > 2.f * vref) {
+          vfix = vref / vmax;
+          vref = vmax;
+        }
+        const float vrel = vref > 0.f ? __fdividef(dv, vref) * AT_P_SCALE : 0.f;
+        uint32_t pa[MT][NJ / 2][4];
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
+          // the lane's 16 products share one factor to logits in powers of two
+          // (not 0: a masked product is -inf)
+          const float f = fmaxf(qs[mt] * dk, 0x1p-120f);
+          float mx = s[mt][0][0];
 #pragma unroll
-          for (int j = 0; j < 8; j++) {
+          for (int j = 0; j < NJ; j++) mx = fmaxf(mx, fmaxf(s[mt][j][0], s[mt][j][1]));
+          mx *= f;
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          float fix = vfix;
+          if (mx > m[mt] + AT_LAZY || (m[mt] == -INFINITY && mx > m[mt])) {
+            const float alpha = ex2(m[mt] - mx);
+            fix *= alpha;
+            l[mt] *= alpha;
+            m[mt] = mx;
+          }
+          if (__any_sync(0xffffffffu, fix != 1.f)) {
 #pragma unroll
-            for (int e = 0; e < 2; e++)
-              if (pos0 + 2 * j + e >= lim[mt] || pos0 + 2 * j + e < low[mt]) s[mt][j][e] = -INFINITY;
+            for (int n2 = 0; n2 < NV; n2++) {
+              o[mt][n2][0] *= fix, o[mt][n2][1] *= fix, o[mt][n2][2] *= fix, o[mt][n2][3] *= fix;
+            }
+          }
+          const float ms = m[mt] == -INFINITY ? 0.f : m[mt];
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < NJ; j++) {
+            const float a = ex2(fmaf(s[mt][j][0], f, -ms)), b = ex2(fmaf(s[mt][j][1], f, -ms));
+            sum += a + b;
+            split_f16(a * vrel, b * vrel, pa[mt][j >> 1][2 * (j & 1)], pa[mt][j >> 1][2 * (j & 1) + 1]);
+          }
+          l[mt] += sum;
+        }
+        // O += P V: k-step kk holds the lane's tokens 4 kk .. + 3
+        const uint8_t* vrow = rec + KV_HEADER + P * D + r * P + (16 * c) % P + 2 * NJ * part;
+#pragma unroll
+        for (int n2 = 0; n2 < NV; n2++) {
+          uint32_t w[NJ / 2];
+          load_words<NJ / 2>(vrow + n2 * 8 * P, w);
+#pragma unroll
+          for (int kk = 0; kk < NJ / 2; kk++) {
+            uint32_t b0, b1;
+            codes_to_f16(w[kk], b0, b1);
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) mma16816(o[mt][n2], pa[mt][kk], b0, b1);
           }
         }
       }
-      // values share one reference scale per warp: raised when a page's is over twice it
-      float vmax = fmaxf(dv, __shfl_xor_sync(0xffffffffu, dv, 1));
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-      float vfix = 1.f;
-      if (vmax > 2.f * vref) {
-        vfix = vref / vmax;
-        vref = vmax;
+      if constexpr (SP > 1) named_sync(2 + group, SP * 32);  // the group has read the tile
+      else __syncwarp();
+      if (part == 0) {
+        if (lane == 0) mbar_arrive(&plan_done[(n >> 5) & 1]);
+        if (!dead && n + S < units) fill(n + S, st);
       }
-      const float vrel = vref > 0.f ? __fdividef(dv, vref) * AT_P_SCALE : 0.f;
-      uint32_t pa[MT][4][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; mt++) {
-        // the lane's 16 products share one factor to logits in powers of two
-        // (not 0: a masked product is -inf)
-        const float f = fmaxf(qs[mt] * dk, 0x1p-120f);
-        float mx = s[mt][0][0];
-#pragma unroll
-        for (int j = 0; j < 8; j++) mx = fmaxf(mx, fmaxf(s[mt][j][0], s[mt][j][1]));
-        mx *= f;
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        float fix = vfix;
-        if (mx > m[mt] + AT_LAZY || (m[mt] == -INFINITY && mx > m[mt])) {
-          const float alpha = ex2(m[mt] - mx);
-          fix *= alpha;
-          l[mt] *= alpha;
-          m[mt] = mx;
-        }
-        if (__any_sync(0xffffffffu, fix != 1.f)) {
-#pragma unroll
-          for (int n2 = 0; n2 < NV; n2++) {
-            o[mt][n2][0] *= fix, o[mt][n2][1] *= fix, o[mt][n2][2] *= fix, o[mt][n2][3] *= fix;
-          }
-        }
-        const float ms = m[mt] == -INFINITY ? 0.f : m[mt];
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-          const float a = ex2(fmaf(s[mt][j][0], f, -ms)), b = ex2(fmaf(s[mt][j][1], f, -ms));
-          sum += a + b;
-          split_f16(a * vrel, b * vrel, pa[mt][j >> 1][2 * (j & 1)], pa[mt][j >> 1][2 * (j & 1) + 1]);
-        }
-        l[mt] += sum;
-      }
-      // O += P V: k-step kk holds tokens 16 c + 4 kk .. + 3
-      const uint8_t* vrow = rec + KV_HEADER + P * D + r * P + (16 * c) % P;
-#pragma unroll
-      for (int n2 = 0; n2 < NV; n2++) {
-        const uint4 vw = *reinterpret_cast<const uint4*>(vrow + n2 * 8 * P);
-        const uint32_t w[4] = {vw.x, vw.y, vw.z, vw.w};
-#pragma unroll
-        for (int kk = 0; kk < 4; kk++) {
-          uint32_t b0, b1;
-          codes_to_f16(w[kk], b0, b1);
-#pragma unroll
-          for (int mt = 0; mt < MT; mt++) mma16816(o[mt][n2], pa[mt][kk], b0, b1);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&plan_done[(n >> 5) & 1]);
-      if (n + S < units) fill(n + S, st);
       st += st_step;
       if (st >= S) st -= S;
     }
@@ -699,20 +752,29 @@ static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
   const int sms = device_sm_count(), grid = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  make_config(cfg, attr, dim3(grid), dim3((AT_WARPS + 1) * 32), smem, stream, true);
+  make_config(cfg, attr, dim3(grid), dim3((at_warps(D, MT) + 1) * 32), smem, stream, true);
   e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<D, P, MT>, p);
   if (e != cudaSuccess) return e;
   make_config(cfg, attr, dim3(grid, 8 * MT), dim3(D / 4), 0, stream, true);
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, MT>, p);
 }
 
+template <int D, int MT>
+static cudaError_t launch_attend_p(AttendParams& p, cudaStream_t stream) {
+  switch (p.kv.P) {
+    case 16: return launch_attend<D, 16, MT>(p, stream);
+    case 32: return launch_attend<D, 32, MT>(p, stream);
+    default: return launch_attend<D, 64, MT>(p, stream);
+  }
+}
 template <int D>
 static cudaError_t launch_attend_d(AttendParams& p, cudaStream_t stream) {
-  switch (p.kv.P) {
-    case 16: return launch_attend<D, 16, 1>(p, stream);
-    case 32: return launch_attend<D, 32, 1>(p, stream);
-    default: return launch_attend<D, 64, 1>(p, stream);
+  if constexpr (D <= 128) {
+    // rows that share a kv head, on average (with a page list a token's own)
+    const long long rows = p.sel ? p.G : ((long long)p.kv.n_tok * p.G + p.kv.n_seq - 1) / p.kv.n_seq;
+    if (rows > 8) return launch_attend_p<D, 2>(p, stream);
   }
+  return launch_attend_p<D, 1>(p, stream);
 }
 
 cudaError_t launch_kv_attend(const KvParams& kv, int D, const AttendArgs& a, cudaStream_t stream) {
