@@ -97,9 +97,11 @@ __device__ __forceinline__ void set_error(unsigned* err, unsigned bits) {
 #ifdef QMV_DEBUG
 #define QMV_DEBUG_ONLY(...) __VA_ARGS__
 #define QMV_CHECK(...) (__VA_ARGS__)
+#define QMV_EXTENT(...) (__VA_ARGS__)
 #else
 #define QMV_DEBUG_ONLY(...)
 #define QMV_CHECK(...) true
+#define QMV_EXTENT(...) 0 /* an extent handed on to a checked access */
 #endif
 
 // elements [i, i + n) of a buffer of len elements

@@ -51,6 +51,7 @@ static KvParams params(const qmv_kv_cache* c, const qmv_kv_batch* b) {
   p.starts = b->starts;
   p.H = c->n_kv_heads;
   p.P = c->page_tokens;
+  p.log_p = c->page_tokens == 16 ? 4 : c->page_tokens == 32 ? 5 : 6;
   p.n_pages = c->n_pages;
   p.n_seq = b->n_seq;
   p.max_pages = b->max_pages;
@@ -94,6 +95,7 @@ int qmv_rms_norm(int dtype, const void* x, int64_t ldx, const void* r, const flo
   p.rows = rows;
   p.K = (int)K;
   p.eps = eps;
+  p.inv_k = 1.0f / (float)K;
   QMV_DEBUG_ONLY(p.err = device_error_word(); p.x_len = (rows - 1) * ldx + K; p.n = rows * K;
                  p.out_len = output_extent(rows * K);)
   return status(launch_rms_norm(dtype, p, vec, stream, true));

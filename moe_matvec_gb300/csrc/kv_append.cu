@@ -1,4 +1,6 @@
 // Writing tokens into the paged 8-bit cache, and reading them back.
+#include <type_traits>
+
 #include "float_io.cuh"
 #include "kv_cache.cuh"
 #include "kv_launch.h"
@@ -6,76 +8,75 @@
 
 namespace qmv {
 
-constexpr int KV_THREADS = 256;
-
-// The (sequence, page) that block `item` of the grid works on: sequences take
-// as many consecutive blocks as their new tokens touch pages.  Every thread
-// returns the same answer; s = -1 past the last.
+// The (sequence, page) that an item of the grid stands for; every thread
+// returns the same answer, s = -1 for an item that stands for nothing.
+// Sequence s of the batch owns items starts[s] / P + 2 s .. starts[s+1] / P +
+// 2 (s + 1), at least as many as its new tokens can touch pages ((n - 2) / P +
+// 2 for n of them, in the worst place), so the sequence is found from starts
+// alone: a 32-ary search by each warp, one or two loads deep, where prefix sums
+// of the touched pages would need every sequence and the block's barriers.
 struct KvItem {
   int s, page;  // page: index in the sequence
   KvSeq seq;
 };
-// at least one for a sequence with tokens in the call, so that some block
-// sees to the tokens of an empty one
-__device__ __forceinline__ int touched_pages(const KvSeq& q, int P) {
-  if (q.n < 1) return 0;
-  return max(q.len - 1, 0) / P - max(q.len - q.n, 0) / P + 1;
-}
 __device__ __forceinline__ KvItem kv_item(const KvParams& p, int item) {
   KvItem r;
   if (!p.starts) {
     r.s = item;
     r.seq = kv_seq(p, item);
-    r.page = max(r.seq.len - 1, 0) / p.P;
+    r.page = max(r.seq.len - 1, 0) >> p.log_p;
     return r;
   }
-  // chunks of one sequence per thread, an exclusive scan of the page counts
-  __shared__ int wsum[KV_THREADS / 32];
-  __shared__ int found[2];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  if (tid == 0) found[0] = -1;
-  int base = 0;
-  for (int c = 0; c < p.n_seq; c += KV_THREADS) {
-    const int s = c + tid;
-    const int cnt = s < p.n_seq ? touched_pages(kv_seq(p, s), p.P) : 0;
-    int inc = cnt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) wsum[w] = inc;
-    __syncthreads();
-    int before = base, total = 0;
-#pragma unroll
-    for (int i = 0; i < KV_THREADS / 32; i++) {
-      if (i < w) before += wsum[i];
-      total += wsum[i];
-    }
-    const int lo = before + inc - cnt;
-    if (item >= lo && item < lo + cnt) {
-      found[0] = s;
-      found[1] = item - lo;
-    }
-    base += total;
-    __syncthreads();
-    if (found[0] >= 0 || item < base) break;
+  const int lane = threadIdx.x & 31;
+  auto first_item = [&](int s) { return (p.starts[s] >> p.log_p) + 2 * s; };
+  int lo = 0, n = p.n_seq;  // the sequence is one of [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, s = lo + (lane + 1) * step;  // candidates after lo
+    const bool at_or_after = (lane + 1) * step < n && first_item(s) <= item;
+    const int k = __popc(__ballot_sync(0xffffffffu, at_or_after));
+    lo += k * step;
+    n = min(n - k * step, step);
   }
-  r.s = found[0];
-  r.page = 0;
-  r.seq = KvSeq{0, 0, 0};
-  if (r.s >= 0) {
-    r.seq = kv_seq(p, r.s);
-    r.page = max(r.seq.len - r.seq.n, 0) / p.P + found[1];
-  }
+  r.s = lo;
+  r.seq = kv_seq(p, lo);
+  const int first = max(r.seq.len - r.seq.n, 0) >> p.log_p;
+  r.page = first + max(item - first_item(lo), 0);
+  // (page 0 of an empty sequence stays: some block sees to its tokens)
+  if (r.seq.n < 1 || r.page > max(r.seq.len - 1, 0) >> p.log_p) r.s = -1;
   return r;
 }
 
 // The activation rule's scale, its reciprocal and code.
-__device__ __forceinline__ float rule_inv(float d) { return d > 0.f ? __frcp_rn(d) : 0.f; }
+// (the branch-free forms where they are exact, the IEEE operations else)
+__device__ __forceinline__ float rule_scale(float amax) {
+  return amax >= 127.0f * 0x1p-126f && amax < INFINITY ? div127_rn(amax) : __fdiv_rn(amax, 127.0f);
+}
+__device__ __forceinline__ float rule_inv(float d) {
+  return d >= 0x1p-126f && d <= 0x1p126f ? rcp_rn(d) : d > 0.f ? __frcp_rn(d) : 0.f;
+}
 __device__ __forceinline__ int rule_code(float x, float inv) {
   // the conversion takes +-inf to the ends of the int range and NaN to 0
   return min(max(__float2int_rn(__fmul_rn(x, inv)), -127), 127);
+}
+
+// Four values' codes as the bytes code + 128.  Where the scale is 0 or large
+// enough that |x| / d stays below 127.5 whatever the roundings, adding 1.5 *
+// 2^23 + 128 leaves the integer, rounded half to even, in the low mantissa
+// bits; else the rule as it is written (`plain`).
+__device__ __forceinline__ bool rule_is_plain(float d) { return d > 0.f && !(d >= 0x1p-100f && d < INFINITY); }
+template <bool PLAIN>
+__device__ __forceinline__ uint32_t rule_bytes(const float (&v)[4], float inv) {
+  uint32_t q[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++)
+    q[j] = PLAIN ? (uint32_t)(rule_code(v[j], inv) + 128)
+                 : __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.0f + 128.0f));
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+}
+
+// Byte j of w (code + 128) as the float code, exactly: 2^23 + byte, less 2^23 + 128.
+__device__ __forceinline__ float byte_code(uint32_t w, int j) {
+  return __fsub_rn(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + j)), 8388608.0f + 128.0f);
 }
 
 // The codes of four packed bytes (code + 128) under a grown scale.
@@ -83,8 +84,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   uint32_t o = 0;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int c = (int)((w >> (8 * i)) & 0xFF) - 128;
-    o |= (uint32_t)((__float2int_rn(__fmul_rn((float)c, ratio)) + 128) & 0xFF) << (8 * i);
+    o |= (uint32_t)((__float2int_rn(__fmul_rn(byte_code(w, i), ratio)) + 128) & 0xFF) << (8 * i);
   }
   return o;
 }
@@ -95,66 +95,123 @@ __device__ __forceinline__ uint32_t rescale4_first(uint32_t w, float ratio, int 
   return (rescale4(w, ratio) & ~keep) | (w & keep);
 }
 
-// One CTA per (page, head) that the call's tokens touch; threads 0-127 take
-// the keys, 128-255 the values.  Pass 1 reads the page's new tokens for the
-// largest magnitude (and, for the bounds, the extremes of each dimension);
-// if an old scale has to grow, the old codes are rewritten; pass 2 reads the
-// tokens again (from L1 / L2) and stores their codes.  HBM-bound at the
-// prompt sizes, latency at single tokens: then a CTA reads 2 D values and
-// writes 2 D bytes.
-template <int DT, int D>
-__global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const KvParams p, const void* kx, const void* vx,
-                                                               long long k_stride, long long v_stride) {
+// Four vectors of four values, element (t, j) = token t, dimension j, as four
+// words of one dimension's four tokens each.
+__device__ __forceinline__ void transpose4(const uint32_t (&w)[4], uint32_t (&o)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+  const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+  o[0] = __byte_perm(a, b, 0x5410);
+  o[1] = __byte_perm(a, b, 0x7632);
+  o[2] = __byte_perm(c, d, 0x5410);
+  o[3] = __byte_perm(c, d, 0x7632);
+}
+
+// Half a CTA takes the keys of a (page, head), the other half the values; a
+// thread takes four dimensions of groups of four consecutive slots.  The
+// page's new tokens are read once into registers (T as it came); their largest
+// magnitude gives the scale; if an old scale has to grow, the old codes are
+// rewritten; then the codes are stored, the values' transposed in shared memory
+// so that they leave in 16-byte pieces.
+// NQ: groups of four slots a thread holds.  Prompts take 256 threads (512 for
+// wider heads, whose values would take too many registers): the fewer,
+// the smaller the share of finding the page and its scale.  Single tokens (ONE)
+// take 128, a group being one slot.  Bound by instructions and HBM alike at
+// prompt sizes, by latency at single tokens.
+template <int DT, int D, bool ONE>
+struct AppendShape {
+  static constexpr int THREADS = ONE ? 128 : D * sizeof(typename Elem<DT>::type) > 256 ? 512 : 256, HALF = THREADS / 2, COLS = D / 4, TG = HALF / COLS;
+  static constexpr int SLOTS = ONE ? 1 : 4;                      // of a group
+  static constexpr int NQ = ONE ? 1 : (64 / SLOTS + TG - 1) / TG;  // groups a thread
+};
+
+template <int DT, int D, bool ONE>
+__global__ void __launch_bounds__(AppendShape<DT, D, ONE>::THREADS, ONE ? 1 : 768 / AppendShape<DT, D, ONE>::THREADS)
+    kv_append_kernel(const KvParams p, const void* kx, const void* vx, long long k_stride, long long v_stride) {
   using T = typename Elem<DT>::type;
+  using Shape = AppendShape<DT, D, ONE>;
+  constexpr int HALF = Shape::HALF, COLS = Shape::COLS, TG = Shape::TG, NQ = Shape::NQ, SLOTS = Shape::SLOTS;
+  static_assert(COLS <= HALF, "a thread takes four dimensions");
+  using Raw = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;  // four values
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int HALF = KV_THREADS / 2, COLS = D / 4, TG = HALF / COLS;
-  static_assert(COLS <= HALF, "a thread takes four dimensions");
-  __shared__ float red[KV_THREADS / 32];
+  constexpr int VROW = ONE ? 4 : 64 + 16;  // bytes of a dimension's slots in shared memory
+  __shared__ float red[Shape::THREADS / 32];
   __shared__ float lo_s[TG][D], hi_s[TG][D];
-  const KvItem it = kv_item(p, blockIdx.x);
+  __shared__ __align__(16) uint8_t vt[ONE ? 16 : D * VROW];
+  const KvItem it = kv_item(p, (int)(blockIdx.x / (unsigned)p.H));
   if (it.s < 0) return;
-  const int head = blockIdx.y, P = p.P;
+  const int head = (int)(blockIdx.x % (unsigned)p.H), P = p.P;  // a token's heads side by side
   const int pos0 = it.seq.len - it.seq.n, page0 = it.page * P;
   const int lo = max(max(pos0, 0) - page0, 0), hi = min(it.seq.len - page0, P);  // the new slots
   if (pos0 < 0 && it.seq.len > 0 && threadIdx.x == 0) set_error(p.err, QMV_DEVERR_BATCH);  // tokens before the first
   if (hi <= lo) return;  // an empty sequence
-  const int phys = kv_page(p, it.s, it.page);
-  if (phys < 0) return;
-  const long long tok0 = (long long)it.seq.t0 + page0 - pos0;                    // call's token of slot 0
+  const long long tok0 = (long long)it.seq.t0 + page0 - pos0;  // call's token of slot 0
   const int part = threadIdx.x / HALF, u = threadIdx.x % HALF;
   const int col = u % COLS, tg = u / COLS;
   const long long stride = part ? v_stride : k_stride;
-  const T* x = static_cast<const T*>(part ? vx : kx) + (long long)head * D;
+  const T* x = static_cast<const T*>(part ? vx : kx) + (long long)head * D + 4 * col;
+  // slots of the thread's group q: first_slot(q) .. + SLOTS - 1
+  auto first_slot = [&](int q) { return ONE ? lo : 4 * (tg + q * TG); };
+  Raw raw[NQ][SLOTS];
+#pragma unroll
+  for (int q = 0; q < NQ; q++) {
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) {
+      const int t = first_slot(q) + i;
+      raw[q][i] = Raw{};
+      if (tg < TG && (!ONE || tg == 0) && t >= lo && t < hi && QMV_CHECK(in_range(tok0 + t, 1, p.n_tok, p.err)))
+        raw[q][i] = *reinterpret_cast<const Raw*>(x + (tok0 + t) * stride);
+    }
+  }
+  const int phys = kv_page(p, it.s, it.page);
+  if (phys < 0) return;
   const int rec_bytes = kv_page_bytes(D, P);
   const long long rec_at = ((long long)phys * p.H + head) * rec_bytes;
   if (!QMV_CHECK(in_range(rec_at, rec_bytes, p.pages_len, p.err))) return;
   uint8_t* rec = p.pages + rec_at;
   float* scales = reinterpret_cast<float*>(rec);
   const float d_old = lo > 0 ? scales[part] : 0.f;
+  auto values = [&](const Raw& r, float (&v)[4]) {
+    const T* e = reinterpret_cast<const T*>(&r);
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = to_float(e[j]);
+  };
 
-  float amax = 0.f, mn[4], mx[4];
+  float amax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; j++) mn[j] = INFINITY, mx[j] = -INFINITY;
-  if (tg < TG) {
-#pragma unroll 4
-    for (int t = lo + tg; t < hi; t += TG) {
+  for (int q = 0; q < NQ; q++) {
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) {
       float v[4];
-      if (!QMV_CHECK(in_range(tok0 + t, 1, p.n_tok, p.err))) continue;
-      load_vec<4>(x + (tok0 + t) * stride + 4 * col, v);
+      values(raw[q][i], v);
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        amax = fmaxf(amax, fabsf(v[j]));
-        mn[j] = fminf(mn[j], v[j]);
-        mx[j] = fmaxf(mx[j], v[j]);
+      for (int j = 0; j < 4; j++) amax = fmaxf(amax, fabsf(v[j]));
+    }
+  }
+  if (p.bounds && part == 0 && tg < TG) {
+    float mn[4], mx[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) mn[j] = INFINITY, mx[j] = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < NQ; q++) {
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) {
+        const int t = first_slot(q) + i;
+        float v[4];
+        values(raw[q][i], v);
+        if (t >= lo && t < hi && (!ONE || tg == 0)) {
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            mn[j] = fminf(mn[j], v[j]);
+            mx[j] = fmaxf(mx[j], v[j]);
+          }
+        }
       }
     }
-    if (p.bounds && part == 0) {
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        lo_s[tg][4 * col + j] = mn[j];
-        hi_s[tg][4 * col + j] = mx[j];
-      }
+    for (int j = 0; j < 4; j++) {
+      lo_s[tg][4 * col + j] = mn[j];
+      hi_s[tg][4 * col + j] = mx[j];
     }
   }
 #pragma unroll
@@ -163,12 +220,12 @@ __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const KvParams p,
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < HALF / 32; i++) amax = fmaxf(amax, red[part * (HALF / 32) + i]);
-  const float d = fmaxf(d_old, __fdiv_rn(amax, 127.0f));
+  const float d = fmaxf(d_old, rule_scale(amax));
   const float inv = rule_inv(d);
   uint8_t* codes = rec + KV_HEADER + part * P * D;
 
   const bool grown = lo > 0 && d > d_old;
-  const float ratio = d > 0.f ? __fdiv_rn(d_old, d) : 0.f;
+  const float ratio = lo > 0 && d > 0.f ? __fdiv_rn(d_old, d) : 0.f;
   if (grown) {
     if (part == 0) {  // slots [0, lo) of each group of 64 dimensions: contiguous
       for (int i = u; i < (D / 64) * lo * 4; i += HALF) {
@@ -189,19 +246,44 @@ __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const KvParams p,
       }
     }
   }
-  __syncthreads();  // old codes rewritten (values: chunks shared with new slots), both scales read
+  // the codes of each slot's four dimensions, code + 128 in each byte
+  uint32_t packed[NQ][SLOTS];
+  auto pack = [&](auto plain) {
+#pragma unroll
+    for (int q = 0; q < NQ; q++) {
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) {
+        float v[4];
+        values(raw[q][i], v);
+        packed[q][i] = rule_bytes<decltype(plain)::value>(v, inv);
+      }
+    }
+  };
+  if (rule_is_plain(d)) pack(std::true_type{});
+  else pack(std::false_type{});
+  if constexpr (!ONE) {
+    if (part == 1 && tg < TG) {
+#pragma unroll
+      for (int q = 0; q < NQ; q++) {
+        const int t = first_slot(q);
+        if (t >= P) continue;
+        uint32_t o[4];
+        transpose4(packed[q], o);
+#pragma unroll
+        for (int j = 0; j < 4; j++) *reinterpret_cast<uint32_t*>(vt + (4 * col + j) * VROW + t) = o[j];
+      }
+    }
+  }
+  __syncthreads();  // old codes rewritten (values: pieces shared with new slots), both scales read
   if (u == 0) scales[part] = d;
   if (part == 0) {
-    if (tg < TG) {
-#pragma unroll 4
-      for (int t = lo + tg; t < hi; t += TG) {
-        float v[4];
-        if (!QMV_CHECK(in_range(tok0 + t, 1, p.n_tok, p.err))) continue;
-        load_vec<4>(x + (tok0 + t) * stride + 4 * col, v);
-        uint32_t w = 0;
 #pragma unroll
-        for (int j = 0; j < 4; j++) w |= (uint32_t)(rule_code(v[j], inv) + 128) << (8 * j);
-        *reinterpret_cast<uint32_t*>(codes + ((size_t)(4 * col / 64) * P + t) * 64 + 4 * col % 64) = w;
+    for (int q = 0; q < NQ; q++) {
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) {
+        const int t = first_slot(q) + i;
+        if (tg < TG && (!ONE || tg == 0) && t >= lo && t < hi)
+          *reinterpret_cast<uint32_t*>(codes + ((size_t)(4 * col / 64) * P + t) * 64 + 4 * col % 64) = packed[q][i];
       }
     }
     if (p.bounds) {
@@ -229,35 +311,31 @@ __global__ void __launch_bounds__(KV_THREADS) kv_append_kernel(const KvParams p,
         }
       }
     }
+  } else if constexpr (ONE) {
+    if (tg == 0) {
+      const uint32_t w = packed[0][0];
+#pragma unroll
+      for (int j = 0; j < 4; j++) codes[(4 * col + j) * P + lo] = (uint8_t)(w >> (8 * j));
+    }
   } else {
-    // a thread takes one dimension of 16 slots: 16-byte stores where all are new
+    // 16 slots of a dimension a thread; single bytes where some are not new
     const int c0 = lo / 16, nc = (hi - 1) / 16 - c0 + 1;
     for (int i = u; i < D * nc; i += HALF) {
-      const int dd = i % D, c = c0 + i / D;
+      const int dd = i / nc, c = c0 + i % nc;
       const int a = max(lo, 16 * c), z = min(hi, 16 * c + 16);
-      if (!QMV_CHECK(in_range(tok0 + a, z - a, p.n_tok, p.err))) continue;
-      if (z - a == 16) {
-        uint32_t w[4];
-        float v[16];
-#pragma unroll
-        for (int k = 0; k < 16; k++) v[k] = to_float(x[(tok0 + 16 * c + k) * stride + dd]);
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-          w[k] = 0;
-#pragma unroll
-          for (int j = 0; j < 4; j++) w[k] |= (uint32_t)(rule_code(v[4 * k + j], inv) + 128) << (8 * j);
-        }
-        reinterpret_cast<uint4*>(codes + dd * P)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        for (int t = a; t < z; t++)
-          codes[dd * P + t] = (uint8_t)(rule_code(to_float(x[(tok0 + t) * stride + dd]), inv) + 128);
-      }
+      if (z - a == 16)
+        *reinterpret_cast<uint4*>(codes + dd * P + 16 * c) = *reinterpret_cast<const uint4*>(vt + dd * VROW + 16 * c);
+      else
+        for (int t = a; t < z; t++) codes[dd * P + t] = vt[dd * VROW + t];
     }
   }
 }
 
-// The values of the call's tokens: one CTA per (page, head); a thread takes
-// 16 dimensions of a token (keys) or 16 slots of a dimension (values).
+// The values of the call's tokens: one CTA per (page, head).  A thread takes
+// the codes of one 16-byte store of a token (keys), or, in pairs of
+// dimensions, 16 slots (values: 16-byte loads, the stores of a warp side by
+// side).
+constexpr int KV_THREADS = 256;
 template <int DT, int D>
 __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvParams p, typename Elem<DT>::type* ko,
                                                              typename Elem<DT>::type* vo
@@ -265,9 +343,9 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvParams p, t
   using T = typename Elem<DT>::type;
   pdl_launch_dependents();
   pdl_wait();
-  const KvItem it = kv_item(p, blockIdx.x);
+  const KvItem it = kv_item(p, (int)(blockIdx.x / (unsigned)p.H));
   if (it.s < 0) return;
-  const int head = blockIdx.y, P = p.P;
+  const int head = (int)(blockIdx.x % (unsigned)p.H), P = p.P;  // a token's heads side by side
   const int pos0 = it.seq.len - it.seq.n, page0 = it.page * P;
   const int lo = max(max(pos0, 0) - page0, 0), hi = min(it.seq.len - page0, P);
   const long long tok0 = (long long)it.seq.t0 + page0 - pos0;
@@ -291,37 +369,51 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvParams p, t
   const float dv = phys < 0 ? 0.f : reinterpret_cast<const float*>(rec)[1];
   const uint8_t* kc = rec + KV_HEADER;
   const uint8_t* vc = kc + P * D;
-  for (int i = threadIdx.x; i < (hi - lo) * (D / 16); i += KV_THREADS) {
-    const int t = lo + i / (D / 16), c = i % (D / 16);
-    const uint4 q = *reinterpret_cast<const uint4*>(kc + ((size_t)(c / 4) * P + t) * 64 + 16 * (c % 4));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    float v[16];
+  constexpr int N = 16 / sizeof(T), PIECES = D / N;
+  for (int i = threadIdx.x; i < (hi - lo) * PIECES; i += KV_THREADS) {
+    const int t = lo + i / PIECES, e = i % PIECES * N;
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(kc + ((size_t)(e / 64) * P + t) * 64 + e % 64);
+    float v[N];
 #pragma unroll
-    for (int k = 0; k < 16; k++) v[k] = dk * (float)((int)((w[k >> 2] >> (8 * (k & 3))) & 0xFF) - 128);
-    const long long at = (tok0 + t) * row + (long long)head * D + 16 * c;
-    if (QMV_CHECK(in_range(at, 16, out_len, p.err))) store_vec<16, T>(ko + at, v);
+    for (int k = 0; k < N / 4; k++) {
+      const uint32_t w = c[k];
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[4 * k + j] = dk * byte_code(w, j);
+    }
+    const long long at = (tok0 + t) * row + (long long)head * D + e;
+    if (QMV_CHECK(in_range(at, N, out_len, p.err))) store_vec<N, T>(ko + at, v);
   }
   const int c0 = lo / 16, nc = (hi - 1) / 16 - c0 + 1;
-  for (int i = threadIdx.x; i < D * nc; i += KV_THREADS) {
-    const int dd = i % D, c = c0 + i / D;
-    const uint4 q = reinterpret_cast<const uint4*>(vc + dd * P)[c];
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  for (int i = threadIdx.x; i < D / 2 * nc; i += KV_THREADS) {
+    const int dd = 2 * (i % (D / 2)), c = c0 + i / (D / 2);
+    const uint4 a = *reinterpret_cast<const uint4*>(vc + dd * P + 16 * c);
+    const uint4 b = *reinterpret_cast<const uint4*>(vc + (dd + 1) * P + 16 * c);
+    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+    const long long at = (tok0 + 16 * c) * row + (long long)head * D + dd;
+    T* const out = vo + at;
+    auto store = [&](int k) {
+      T pair[2];
+      from_float(dv * byte_code(wa[k >> 2], k & 3), pair[0]);
+      from_float(dv * byte_code(wb[k >> 2], k & 3), pair[1]);
+      if (!QMV_CHECK(in_range(at + k * row, 2, out_len, p.err))) return;
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(out + k * row) = make_float2(pair[0], pair[1]);
+      else *reinterpret_cast<uint32_t*>(out + k * row) = *reinterpret_cast<const uint32_t*>(pair);
+    };
+    if (16 * c >= lo && 16 * c + 16 <= hi) {
 #pragma unroll
-    for (int k = 0; k < 16; k++) {
-      const int t = 16 * c + k;
-      const long long at = (tok0 + t) * row + (long long)head * D + dd;
-      if (t >= lo && t < hi && QMV_CHECK(in_range(at, 1, out_len, p.err)))
-        from_float(dv * (float)((int)((w[k >> 2] >> (8 * (k & 3))) & 0xFF) - 128), vo[at]);
+      for (int k = 0; k < 16; k++) store(k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; k++)
+        if (16 * c + k >= lo && 16 * c + k < hi) store(k);
     }
   }
 }
 
-// Blocks that the batch's touched pages take at most: a sequence of n new
-// tokens touches at most (n + P - 2) / P + 1 pages, and never more than n.
-static unsigned item_bound(const KvParams& p) {
-  if (!p.starts) return (unsigned)p.n_seq;
-  const long long a = (long long)p.n_tok / p.P + 2ll * p.n_seq, b = p.n_tok;
-  return (unsigned)(a < b ? a : b);
+// Blocks of a call: items (see kv_item) times heads.
+static unsigned grid_of(const KvParams& p) {
+  const long long items = p.starts ? (long long)p.n_tok / p.P + 2ll * p.n_seq : p.n_seq;
+  return (unsigned)(items * p.H);
 }
 
 template <int DT, int D>
@@ -329,15 +421,18 @@ static cudaError_t append_as(const KvParams& p, const void* k, long long ks, con
                              cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  make_config(cfg, attr, dim3(item_bound(p), p.H), dim3(KV_THREADS), 0, stream, true);
-  return cudaLaunchKernelEx(&cfg, kv_append_kernel<DT, D>, p, k, v, ks, vs);
+  const bool one = !p.starts;
+  make_config(cfg, attr, dim3(grid_of(p)), dim3(one ? AppendShape<DT, D, true>::THREADS : AppendShape<DT, D, false>::THREADS),
+              0, stream, true);
+  return one ? cudaLaunchKernelEx(&cfg, kv_append_kernel<DT, D, true>, p, k, v, ks, vs)
+             : cudaLaunchKernelEx(&cfg, kv_append_kernel<DT, D, false>, p, k, v, ks, vs);
 }
 template <int DT, int D>
 static cudaError_t read_as(const KvParams& p, void* k, void* v, cudaStream_t stream) {
   using T = typename Elem<DT>::type;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  make_config(cfg, attr, dim3(item_bound(p), p.H), dim3(KV_THREADS), 0, stream, true);
+  make_config(cfg, attr, dim3(grid_of(p)), dim3(KV_THREADS), 0, stream, true);
   return cudaLaunchKernelEx(&cfg, kv_read_kernel<DT, D>, p, static_cast<T*>(k), static_cast<T*>(v)
                             QMV_DEBUG_ONLY(, output_extent((long long)p.n_tok * p.H * D)));
 }

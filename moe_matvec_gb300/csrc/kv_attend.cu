@@ -43,6 +43,7 @@ namespace qmv {
 #ifndef AT_W
 #define AT_W(D, MT) ((D) > 192 ? 6 : 7)
 #define AT_SP(D, MT) ((D) > 192 ? 2 : 1)
+#define AT_IL(D, MT) 4
 #endif
 constexpr int AT_TILE = 64;        // tokens of a unit
 constexpr int AT_MAX_STAGES = 32;  // the planner stays 32 to 64 tiles ahead
@@ -255,6 +256,9 @@ __device__ __forceinline__ void store4(void* base, long long at, int dt, const f
 template <int D, int P, int MT>
 __global__ void __launch_bounds__((at_warps(D, MT) + 1) * 32, 1) kv_attend_kernel(const AttendParams p) {
   constexpr int W = at_warps(D, MT), SP = at_split(D, MT), NG = W / SP, NJ = 8 / SP;
+  // independent products in flight: a chain of MMAs into one accumulator waits
+  // for each of them
+  constexpr int IL = AT_IL(D, MT);
   constexpr int R = 8 * MT, KS = D / 16, NV = D / 8, MSTRIDE = D + 8;
   constexpr int ppt = AT_TILE / P, rec_stride = at_rec_stride(D, P), stage_bytes = ppt * rec_stride;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -501,27 +505,34 @@ __global__ void __launch_bounds__((at_warps(D, MT) + 1) * 32, 1) kv_attend_kerne
           const int ksub = 16 * (r >> 1) / P, kt = (16 * (r >> 1)) % P + (r & 1);
           const uint8_t* krow = stage + ksub * rec_stride + KV_HEADER + kt * 64 + 16 * c + 128 * NJ * part;
 #pragma unroll
-          for (int j = 0; j < NJ; j++) {
-            float acc[MT][4];
+          for (int jg = 0; jg < NJ; jg += IL) {
+            float acc[MT][IL][4];
 #pragma unroll
             for (int h = 0; h < D / 64; h++) {
-              const uint4 kw = *reinterpret_cast<const uint4*>(krow + h * P * 64 + j * 128);
-              const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+              uint32_t w[IL][4];
+#pragma unroll
+              for (int i = 0; i < IL; i++) load_words<4>(krow + h * P * 64 + (jg + i) * 128, w[i]);
 #pragma unroll
               for (int k = 0; k < 4; k++) {
-                uint32_t b0, b1;
-                codes_to_f16(w[k], b0, b1);
 #pragma unroll
-                for (int mt = 0; mt < MT; mt++) {
-                  if (h == 0 && k == 0) mma16816_first(acc[mt], qa[mt][0], b0, b1);
-                  else mma16816(acc[mt], qa[mt][4 * h + k], b0, b1);
+                for (int i = 0; i < IL; i++) {
+                  uint32_t b0, b1;
+                  codes_to_f16(w[i][k], b0, b1);
+#pragma unroll
+                  for (int mt = 0; mt < MT; mt++) {
+                    if (h == 0 && k == 0) mma16816_first(acc[mt][i], qa[mt][0], b0, b1);
+                    else mma16816(acc[mt][i], qa[mt][4 * h + k], b0, b1);
+                  }
                 }
               }
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++) {
-              s[mt][j][0] = acc[mt][0] + acc[mt][2];
-              s[mt][j][1] = acc[mt][1] + acc[mt][3];
+            for (int i = 0; i < IL; i++) {
+#pragma unroll
+              for (int mt = 0; mt < MT; mt++) {
+                s[mt][jg + i][0] = acc[mt][i][0] + acc[mt][i][2];
+                s[mt][jg + i][1] = acc[mt][i][1] + acc[mt][i][3];
+              }
             }
           }
         }
@@ -587,15 +598,19 @@ __global__ void __launch_bounds__((at_warps(D, MT) + 1) * 32, 1) kv_attend_kerne
         // O += P V: k-step kk holds the lane's tokens 4 kk .. + 3
         const uint8_t* vrow = rec + KV_HEADER + P * D + r * P + (16 * c) % P + 2 * NJ * part;
 #pragma unroll
-        for (int n2 = 0; n2 < NV; n2++) {
-          uint32_t w[NJ / 2];
-          load_words<NJ / 2>(vrow + n2 * 8 * P, w);
+        for (int ng = 0; ng < NV; ng += IL) {
+          uint32_t w[IL][NJ / 2];
+#pragma unroll
+          for (int i = 0; i < IL; i++) load_words<NJ / 2>(vrow + (ng + i) * 8 * P, w[i]);
 #pragma unroll
           for (int kk = 0; kk < NJ / 2; kk++) {
-            uint32_t b0, b1;
-            codes_to_f16(w[kk], b0, b1);
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++) mma16816(o[mt][n2], pa[mt][kk], b0, b1);
+            for (int i = 0; i < IL; i++) {
+              uint32_t b0, b1;
+              codes_to_f16(w[i][kk], b0, b1);
+#pragma unroll
+              for (int mt = 0; mt < MT; mt++) mma16816(o[mt][ng + i], pa[mt][kk], b0, b1);
+            }
           }
         }
       }
@@ -701,22 +716,39 @@ __global__ void __launch_bounds__(D / 4) kv_join_kernel(const AttendParams p) {
   const int rr = j.row0 + row;
   if (j.last <= c || rr >= j.nrows) return;
   const int parts = j.last - c + 1, col = 4 * threadIdx.x;
-  auto part = [&](int i) { return p.slots + (size_t)(2 * (c + i) + (i == 0 ? 1 : 0)) * SLOT; };
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < parts; i++) M = fmaxf(M, part(i)[2 * row]);
-  float acc[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < parts; i++) {
-    const float* s = part(i);
-    const float m = s[2 * row], l = s[2 * row + 1];
-    const float4 x = *reinterpret_cast<const float4*>(s + 2 * R + row * D + col);
-    const float f = m == -INFINITY ? 0.f : ex2(m - M);
-    L = fmaf(l, f, L);
-    acc[0] = fmaf(x.x, f, acc[0]);
-    acc[1] = fmaf(x.y, f, acc[1]);
-    acc[2] = fmaf(x.z, f, acc[2]);
-    acc[3] = fmaf(x.w, f, acc[3]);
+  float M = -INFINITY, acc[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
+  // CHUNK parts at a time, all on their way together (8 kv heads of one
+  // sequence share 152 SMs in 19 parts each)
+  constexpr int CHUNK = 20;
+  for (int i0 = 0; i0 < parts; i0 += CHUNK) {
+    float2 st[CHUNK];
+    float4 xs[CHUNK];
+#pragma unroll
+    for (int i = 0; i < CHUNK; i++) {
+      const int k = min(i0 + i, parts - 1);
+      const float* s = p.slots + (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * SLOT;
+      st[i] = *reinterpret_cast<const float2*>(s + 2 * row);
+      xs[i] = *reinterpret_cast<const float4*>(s + 2 * R + row * D + col);
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < CHUNK; i++)
+      if (i0 + i < parts) top = fmaxf(top, st[i].x);
+    const float back = M == -INFINITY ? 0.f : ex2(M - top);
+    M = top;
+    L *= back;
+#pragma unroll
+    for (int e = 0; e < 4; e++) acc[e] *= back;
+#pragma unroll
+    for (int i = 0; i < CHUNK; i++) {
+      if (i0 + i >= parts) continue;
+      const float f = st[i].x == -INFINITY ? 0.f : ex2(st[i].x - M);
+      L = fmaf(st[i].y, f, L);
+      acc[0] = fmaf(xs[i].x, f, acc[0]);
+      acc[1] = fmaf(xs[i].y, f, acc[1]);
+      acc[2] = fmaf(xs[i].z, f, acc[2]);
+      acc[3] = fmaf(xs[i].w, f, acc[3]);
+    }
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll

@@ -16,7 +16,7 @@ struct KvParams {
   const int32_t* table;
   const int32_t* lens;
   const int32_t* starts;  // or nullptr: one token per sequence
-  int H, P, n_pages, n_seq, max_pages, n_tok;
+  int H, P, log_p, n_pages, n_seq, max_pages, n_tok;
   unsigned* err;
 #ifdef QMV_DEBUG
   long long pages_len, bounds_len, table_len;

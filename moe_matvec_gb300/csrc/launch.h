@@ -83,7 +83,7 @@ cudaError_t launch_check_rounding(unsigned long long* bad, cudaStream_t stream);
 
 // Norm (norm.cu): the arguments of qmv_rms_norm; vec: eight values a thread
 // (K and ldx multiples of 8).
-constexpr int NORM_MAX_STEPS = QMV_MAX_NORM / 8 / 1024;
+constexpr int NORM_MAX_STEPS = QMV_MAX_NORM / 8 / 512;
 struct NormParams {
   const void* x;
   const void* r;
@@ -95,7 +95,7 @@ struct NormParams {
   int32_t* s;
   long long ldx, rows;
   int K;
-  float eps;
+  float eps, inv_k;
 #ifdef QMV_DEBUG
   unsigned* err;
   long long x_len, n, out_len;
