@@ -544,8 +544,8 @@ int qmv_kv_read(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, void* k
  * shares over the whole batch whatever its lengths, in a grid that does not
  * depend on them (a captured graph stays valid as lens grow), and joined in a
  * fixed order: results are bitwise reproducible.
- * ws: qmv_kv_attend_workspace_bytes(c, n_heads) bytes, any content. */
-size_t qmv_kv_attend_workspace_bytes(const qmv_kv_cache* c, int n_heads);
+ * ws: qmv_kv_attend_workspace_bytes(c, n_heads, n_tok, n_seq) bytes, any content. */
+size_t qmv_kv_attend_workspace_bytes(const qmv_kv_cache* c, int n_heads, int n_tok, int n_seq);
 int qmv_kv_attend(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const void* q, int64_t q_stride,
                   void* out, int n_heads, float scale, int causal, int window, const int32_t* pages, int n_sel,
                   void* ws, size_t ws_bytes, cudaStream_t stream);

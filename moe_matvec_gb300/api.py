@@ -84,7 +84,7 @@ _SIGS = {
     "qmv_kv_bounds_bytes": (_i64, [_int]),
     "qmv_kv_append": (_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), _int, _vp, _i64, _vp, _i64, _vp]),
     "qmv_kv_read": (_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), _int, _vp, _vp, _vp]),
-    "qmv_kv_attend_workspace_bytes": (_sz, [ctypes.POINTER(KvCache), _int]),
+    "qmv_kv_attend_workspace_bytes": (_sz, [ctypes.POINTER(KvCache), _int, _int, _int]),
     "qmv_kv_attend": (_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), _int, _vp, _i64, _vp, _int,
                              ctypes.c_float, _int, _int, _vp, _int, _vp, _sz, _vp]),
     "qmv_kv_select_workspace_bytes": (_sz, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch)]),
@@ -595,8 +595,8 @@ def kv_read(cache: KvCache, table: torch.Tensor, lens: torch.Tensor, starts: tor
     return k, v
 
 
-def kv_attend_workspace_bytes(cache: KvCache, n_heads: int) -> int:
-    return int(load().qmv_kv_attend_workspace_bytes(ctypes.byref(cache), int(n_heads)))
+def kv_attend_workspace_bytes(cache: KvCache, n_heads: int, n_tok: int, n_seq: int) -> int:
+    return int(load().qmv_kv_attend_workspace_bytes(ctypes.byref(cache), int(n_heads), int(n_tok), int(n_seq)))
 
 
 def kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -610,7 +610,8 @@ def kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, lens: torch.
     _kv_shape(cache, q, heads, "q")
     out = _out(out, q.dtype, shape, q, "out")
     if ws is None:
-        ws = torch.empty(max(16, kv_attend_workspace_bytes(cache, heads)), dtype=torch.uint8, device=q.device)
+        ws = torch.empty(max(16, kv_attend_workspace_bytes(cache, heads, n, lens.numel())), dtype=torch.uint8,
+                         device=q.device)
     n_sel = 0
     if pages is not None:
         if pages.dim() != 3 or pages.shape[:2] != (n, cache.n_kv_heads):

@@ -144,9 +144,9 @@ int qmv_kv_read(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, void* k
   return status(launch_kv_read(params(c, b), dtype, c->head_dim, k, v, stream));
 }
 
-size_t qmv_kv_attend_workspace_bytes(const qmv_kv_cache* c, int n_heads) {
-  if (check_cache(c) || n_heads < 1 || n_heads % c->n_kv_heads) return 0;
-  return kv_attend_ws_bytes(c->head_dim);
+size_t qmv_kv_attend_workspace_bytes(const qmv_kv_cache* c, int n_heads, int n_tok, int n_seq) {
+  if (check_cache(c) || n_heads < 1 || n_heads % c->n_kv_heads || n_tok < 1 || n_seq < 1) return 0;
+  return kv_attend_ws_bytes(c->head_dim, c->n_kv_heads, n_heads / c->n_kv_heads, n_tok, n_seq);
 }
 
 int qmv_kv_attend(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const void* q, int64_t q_stride, void* out,
@@ -161,7 +161,7 @@ int qmv_kv_attend(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const
   if ((rc = check_rows(dtype, q, (long long)n_heads * c->head_dim, q_stride))) return rc;
   if (!out || !ws) return QMV_ERR_NULL;
   if (!al16(out) || !al16(ws) || !al16(pages)) return QMV_ERR_ALIGN;
-  if (ws_bytes < kv_attend_ws_bytes(c->head_dim)) return QMV_ERR_WORKSPACE;
+  if (ws_bytes < qmv_kv_attend_workspace_bytes(c, n_heads, b->n_tok, b->n_seq)) return QMV_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
   AttendArgs a{dtype, q, q_stride, out, n_heads, scale, causal, window, pages, n_sel, ws};
   return status(launch_kv_attend(params(c, b), c->head_dim, a, stream));

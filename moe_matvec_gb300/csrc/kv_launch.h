@@ -25,7 +25,7 @@ struct AttendArgs {
   int n_sel;
   void* ws;
 };
-size_t kv_attend_ws_bytes(int D);
+size_t kv_attend_ws_bytes(int D, int H, int G, int n_tok, int n_seq);
 cudaError_t launch_kv_attend(const KvParams& p, int D, const AttendArgs& a, cudaStream_t stream);
 
 struct SelectArgs {

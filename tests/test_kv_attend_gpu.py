@@ -141,7 +141,7 @@ def test_strided_queries_and_given_buffers(lib):
     pair, table = filled(rng, 2, 128, 32, lens)
     fused = randn(rng, 2, 12, 128)
     q = fused[:, 2:10]
-    ws = torch.full((api.kv_attend_workspace_bytes(pair.dev, 8),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((api.kv_attend_workspace_bytes(pair.dev, 8, 2, 2),), 0xFF, dtype=torch.uint8, device="cuda")
     out = torch.full((2, 8, 128), float("nan"), device="cuda")
     r = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), ws=ws, out=out)
     assert r is out
@@ -186,7 +186,7 @@ def test_graph_replays_as_lengths_grow(lib):
     pair.append(randn(rng, 230, H, D), randn(rng, 230, H, D), table, [100, 130], [0, 100, 230])
     k, v, q = randn(rng, 2, H, D), randn(rng, 2, H, D), randn(rng, 2, 8, D)
     td = dev32(table)
-    ws = torch.empty(api.kv_attend_workspace_bytes(pair.dev, 8), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(api.kv_attend_workspace_bytes(pair.dev, 8, 2, 2), dtype=torch.uint8, device="cuda")
     out = torch.empty(2, 8, D, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

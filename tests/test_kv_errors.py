@@ -47,8 +47,8 @@ def test_cache_shapes(L):
     for D, P in ((96, 64), (0, 64), (512, 64), (128, 8), (128, 128), (128, 0)):
         assert L.qmv_kv_page_bytes(D, P) == -2
     assert L.qmv_kv_bounds_bytes(100) == -2
-    assert L.qmv_kv_attend_workspace_bytes(R(cache()), 12) == 0              # 12 heads on 8
-    assert L.qmv_kv_attend_workspace_bytes(R(cache()), 32) > 0
+    assert L.qmv_kv_attend_workspace_bytes(R(cache()), 12, 4, 4) == 0              # 12 heads on 8
+    assert L.qmv_kv_attend_workspace_bytes(R(cache()), 32, 4, 4) > 0
     assert L.qmv_kv_select_workspace_bytes(R(cache()), R(batch())) == 4 * 8 * 16 * 4
 
 
@@ -92,7 +92,7 @@ def test_attend_and_select_reject_bad_arguments(L):
     assert attend(pages=A, n_sel=0) == -2
     assert attend(out=None) == -4 and attend(ws=None) == -4
     assert attend(out=MIS) == -5 and attend(ws=MIS) == -5 and attend(pages=MIS, n_sel=4) == -5
-    need = L.qmv_kv_attend_workspace_bytes(R(cache()), 32)
+    need = L.qmv_kv_attend_workspace_bytes(R(cache()), 32, 4, 4)
     assert attend(wsb=need - 1) == -6
 
     def select(c=None, heads=32, n_sel=4, ids=A, ws=A, wsb=1 << 30):
