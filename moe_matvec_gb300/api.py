@@ -1,7 +1,8 @@
 """Python binding of the C-ABI library libqmv.so (see include/qmv.h).
 
-Argument marshalling only: every computation runs in the library's CUDA
-kernels.  Tensors are torch CUDA tensors (PyTorch supplies device memory and
+Argument marshalling only (ctypes; for the norm, cache, attention and page
+selection calls of a decode layer a native module, csrc/binding.cpp): every
+computation runs in the library's CUDA kernels.  Tensors are torch CUDA tensors (PyTorch supplies device memory and
 the current stream); results are returned as new tensors unless `out` is
 given.  There is no CPU fallback: importing this module without a buildable
 library raises.
@@ -10,6 +11,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -101,6 +104,21 @@ _SIGS = {
 }
 
 _lib = None
+_native = None  # the native module, driving _lib
+_NATIVE_CALLS = ("qmv_rms_norm", "qmv_dequantize_act", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attend",
+                 "qmv_kv_attend_workspace_bytes", "qmv_kv_select", "qmv_kv_select_workspace_bytes")
+
+
+def _activate(lib):
+    """Make `lib` the library that every call goes to."""
+    global _lib, _native
+    if _native is None:
+        loader = importlib.machinery.ExtensionFileLoader("_binding", _build.build_binding())
+        _native = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+        loader.exec_module(_native)
+    _native.bind(QmvError, *[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS])
+    _lib = lib
+    return lib
 
 
 def _open(path: str):
@@ -118,11 +136,9 @@ def _open(path: str):
 
 def load(path: str | None = None):
     """Load (building first if needed) libqmv.so and declare its signatures."""
-    global _lib
     if _lib is not None:
         return _lib
-    _lib = _open(path or _build.build())
-    return _lib
+    return _activate(_open(path or _build.build()))
 
 
 _debug_lib = None
@@ -143,13 +159,12 @@ def load_debug():
 def using(lib):
     """Within the block, every call of this module goes to `lib` (a library
     from load() or load_debug())."""
-    global _lib
     prev = load()
-    _lib = lib
+    _activate(lib)
     try:
         yield lib
     finally:
-        _lib = prev
+        _activate(prev)
 
 
 def debug_shrink_outputs(n: int) -> None:
@@ -167,17 +182,9 @@ def _check(rc: int, what: str):
         raise QmvError(rc, what)
 
 
-# The current stream's handle without building a Stream object (3 us a call on
-# the Grace host, as long as the kernel launch itself).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream(stream=None) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    s = stream if stream is not None else torch.cuda.current_stream()
+    return s.cuda_stream
 
 
 def _ptr(t: torch.Tensor | None):
@@ -413,52 +420,20 @@ def route_run(fmt: int, Wr: torch.Tensor, x: torch.Tensor, n_experts: int, hidde
 # ---------------------------------------------------------------------------
 # The attention half of a decode layer
 # ---------------------------------------------------------------------------
-DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 MAX_SEQS = 1024
 MAX_BATCH_TOKENS = 65535
+_WANT = {"float": 1, "q8": 2, "both": 3}
 
 
-def _dtype(t: torch.Tensor) -> int:
-    dt = DTYPES.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"float32, float16 or bfloat16 tensor wanted, got {t.dtype}")
-    return dt
+def _nat():
+    """The native module (loading the library first if needed)."""
+    if _native is None:
+        load()
+    return _native
 
 
-def _ints(t: torch.Tensor | None):
-    if t is None:
-        return None
-    if t.dtype is not torch.int32:
-        raise ValueError(f"int32 tensor wanted, got {t.dtype}")
-    return _ptr(t)
-
-
-def _typed(t: torch.Tensor | None, dtype: torch.dtype, shape, what: str):
-    """The address of a contiguous CUDA tensor of this type and shape."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{what}: {dtype} {tuple(shape)} wanted, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
-
-
-def _out(t: torch.Tensor | None, dtype: torch.dtype, shape, like: torch.Tensor, what: str) -> torch.Tensor:
-    """A given result tensor, checked, or a new one on like's device."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _typed(t, dtype, shape, what)
-    return t
-
-
-def _rows(t: torch.Tensor, what: str):
-    """The address and token stride of [n_tok][heads][D], heads and dimensions contiguous."""
-    if not t.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
-    n, h, d = t.shape
-    st, sh, sd = t.stride()
-    if sd != 1 or (h > 1 and sh != d):
-        raise ValueError(f"{what}: the heads and dimensions of a token must be contiguous")
-    return t.data_ptr(), st if n > 1 else h * d
+def _on(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def rms_norm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, r: torch.Tensor | None = None, want: str = "float",
@@ -469,47 +444,16 @@ def rms_norm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, r: torch.Tenso
     activation layout, for run_q8) or "both".  Returns (y, (q, d, s), res), None for what
     was not asked for (res = s in x's type: only with r); y, q8 and res may be given as
     outputs, res also as r itself."""
-    if want not in ("float", "q8", "both"):
+    code = _WANT.get(want)
+    if code is None:
         raise ValueError(f"want is 'float', 'q8' or 'both', got {want!r}")
-    n, K = shape = x.shape
-    dt, t = _dtype(x), x.dtype
-    if not x.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
-    ld, one = x.stride()
-    if K > 1 and one != 1:
-        raise ValueError("x: the values of a row must be contiguous")
-    if y is not None or want != "q8":
-        y = _out(y, t, shape, x, "y")
-    qp = dp = sp = None
-    if q8 is not None or want != "float":
-        if q8 is None:
-            if K % 256:
-                raise QmvError(-2, "qmv_rms_norm")
-            dev = x.device
-            q8 = (torch.empty(shape, dtype=torch.int8, device=dev),
-                  torch.empty((n, K // 32), dtype=torch.float32, device=dev),
-                  torch.empty((n, K // 32), dtype=torch.int32, device=dev))
-        q, d, s = q8
-        qp = _typed(q, torch.int8, shape, "q8")
-        dp, sp = _typed(d, torch.float32, (n, K // 32), "q8"), _typed(s, torch.int32, (n, K // 32), "q8")
-    if res is not None or r is not None:
-        res = _out(res, t, shape, x, "res")
-    _check(load().qmv_rms_norm(dt, x.data_ptr(), ld if n > 1 else K, _typed(r, t, shape, "r"),
-                               _typed(w, torch.float32, (K,), "w"), eps, n, K, _ptr(res), _ptr(y), qp, dp, sp,
-                               _stream(stream)), "qmv_rms_norm")
-    return y, q8, res
+    return _nat().rms_norm(x, w, eps, r, code, y, q8, res, _on(stream))
 
 
 def dequantize_act(q: torch.Tensor, d: torch.Tensor, dtype: torch.dtype = torch.float32,
                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values [n][K] that Q8 activations (q, d of quantize_act or rms_norm) stand for."""
-    n, K = q.shape
-    if out is None:
-        out = torch.empty((n, K), dtype=dtype, device=q.device)
-    _check(load().qmv_dequantize_act(_dtype(out), _typed(q, torch.int8, (n, K), "q"),
-                                     _typed(d, torch.float32, (n, K // 32), "d"), n, K,
-                                     _typed(out, out.dtype, (n, K), "out"), _stream(stream)), "qmv_dequantize_act")
-    return out
+    return _nat().dequantize_act(q, d, dtype, out, _on(stream))
 
 
 def kv_page_bytes(head_dim: int, page_tokens: int) -> int:
@@ -522,6 +466,14 @@ def kv_bounds_bytes(head_dim: int) -> int:
     n = load().qmv_kv_bounds_bytes(int(head_dim))
     _check(n if n < 0 else 0, "qmv_kv_bounds_bytes")
     return int(n)
+
+
+def _bytes(t: torch.Tensor | None, shape, what: str):
+    if t is None:
+        return None
+    if t.dtype is not torch.uint8 or t.shape != shape:
+        raise ValueError(f"{what}: torch.uint8 {shape} wanted, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
 
 
 def kv_cache(n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int, pages: torch.Tensor | None = None,
@@ -539,23 +491,10 @@ def kv_cache(n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int, pag
         bounds = torch.empty((n_pages, n_kv_heads, kv_bounds_bytes(head_dim)), dtype=torch.uint8, device=pages.device)
     elif bounds is False:
         bounds = None
-    c = KvCache(n_kv_heads, head_dim, page_tokens, n_pages,
-                _typed(pages, torch.uint8, (n_pages, n_kv_heads, pb), "pages"),
-                _typed(bounds, torch.uint8, (n_pages, n_kv_heads, kv_bounds_bytes(head_dim)), "bounds"))
+    c = KvCache(n_kv_heads, head_dim, page_tokens, n_pages, _bytes(pages, (n_pages, n_kv_heads, pb), "pages"),
+                _bytes(bounds, (n_pages, n_kv_heads, kv_bounds_bytes(head_dim)), "bounds"))
     c.page_tensor, c.bounds_tensor = pages, bounds
     return c
-
-
-def _batch(table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor | None, n_tok: int) -> KvBatch:
-    n_seq, max_pages = table.shape
-    if lens.shape != (n_seq,) or (starts is not None and starts.shape != (n_seq + 1,)):
-        raise ValueError(f"lens [{n_seq}] and starts [{n_seq + 1}] wanted for a table of {n_seq} sequences")
-    return KvBatch(_ints(table), _ints(lens), _ints(starts), n_seq, max_pages, n_tok, 0)
-
-
-def _kv_shape(cache: KvCache, t: torch.Tensor, heads: int, what: str):
-    if t.dim() != 3 or t.shape[1:] != (heads, cache.head_dim):
-        raise ValueError(f"{what}: [n_tok][{heads}][{cache.head_dim}] wanted, got {tuple(t.shape)}")
 
 
 def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -564,15 +503,7 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.Ten
     [n_tok][n_kv_heads][D] (tokens may be strided); table int32 [n_seq][max_pages], lens
     int32 [n_seq] counting these tokens, starts int32 [n_seq + 1] (None: one token per
     sequence)."""
-    _kv_shape(cache, k, cache.n_kv_heads, "k")
-    _kv_shape(cache, v, cache.n_kv_heads, "v")
-    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
-        raise ValueError("k and v must be of one type and length")
-    kp, ks = _rows(k, "k")
-    vp, vs = _rows(v, "v")
-    b = _batch(table, lens, starts, k.shape[0])
-    _check(load().qmv_kv_append(ctypes.byref(cache), ctypes.byref(b), _dtype(k), kp, ks, vp, vs, _stream(stream)),
-           "qmv_kv_append")
+    _nat().kv_append(ctypes.addressof(cache), k, v, table, lens, starts, _on(stream))
 
 
 def kv_read(cache: KvCache, table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor | None = None,
@@ -580,19 +511,7 @@ def kv_read(cache: KvCache, table: torch.Tensor, lens: torch.Tensor, starts: tor
             v: torch.Tensor | None = None, stream=None):
     """The last tokens of each sequence as values (qmv_kv_read): (k, v), each
     [n_tok][n_kv_heads][D].  n_tok is starts[-1] (a host number; None with starts None)."""
-    if n_tok is None:
-        if starts is not None:
-            raise ValueError("n_tok is needed with starts")
-        n_tok = lens.numel()
-    shape = (n_tok, cache.n_kv_heads, cache.head_dim)
-    if k is None:
-        k = torch.empty(shape, dtype=dtype, device=table.device)
-    if v is None:
-        v = torch.empty(shape, dtype=k.dtype, device=table.device)
-    b = _batch(table, lens, starts, n_tok)
-    _check(load().qmv_kv_read(ctypes.byref(cache), ctypes.byref(b), _dtype(k), _typed(k, k.dtype, shape, "k"),
-                              _typed(v, k.dtype, shape, "v"), _stream(stream)), "qmv_kv_read")
-    return k, v
+    return _nat().kv_read(ctypes.addressof(cache), table, lens, starts, n_tok, dtype, k, v, _on(stream))
 
 
 def kv_attend_workspace_bytes(cache: KvCache, n_heads: int, n_tok: int, n_seq: int) -> int:
@@ -606,24 +525,8 @@ def kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, lens: torch.
     """Attention of the last tokens of each sequence over the cache (qmv_kv_attend).
     q [n_tok][n_heads][D] (tokens may be strided), scale 1 / sqrt(D) if None, pages int32
     [n_tok][n_kv_heads][n_sel] (kv_select's) or None for all.  Returns out like q."""
-    n, heads, D = shape = q.shape
-    _kv_shape(cache, q, heads, "q")
-    out = _out(out, q.dtype, shape, q, "out")
-    if ws is None:
-        ws = torch.empty(max(16, kv_attend_workspace_bytes(cache, heads, n, lens.numel())), dtype=torch.uint8,
-                         device=q.device)
-    n_sel = 0
-    if pages is not None:
-        if pages.dim() != 3 or pages.shape[:2] != (n, cache.n_kv_heads):
-            raise ValueError(f"pages: [{n}][{cache.n_kv_heads}][n_sel] wanted, got {tuple(pages.shape)}")
-        n_sel = pages.shape[2]
-    qp, qs = _rows(q, "q")
-    b = _batch(table, lens, starts, n)
-    _check(load().qmv_kv_attend(ctypes.byref(cache), ctypes.byref(b), _dtype(q), qp, qs,
-                                out.data_ptr(), heads,
-                                D ** -0.5 if scale is None else scale, int(causal), int(window), _ints(pages), n_sel,
-                                _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "qmv_kv_attend")
-    return out
+    return _nat().kv_attend(ctypes.addressof(cache), q, table, lens, starts, scale, causal, window, pages, ws, out,
+                            _on(stream))
 
 
 def kv_select_workspace_bytes(cache: KvCache, n_tok: int, max_pages: int) -> int:
@@ -637,18 +540,7 @@ def kv_select(cache: KvCache, q: torch.Tensor, table: torch.Tensor, lens: torch.
     """The n_sel pages worth attending to for each token and kv head (qmv_kv_select): ids
     int32 [n_tok][n_kv_heads][n_sel], ascending, -1 after the last; for kv_attend's pages.
     The cache must have bounds."""
-    n, heads, _ = q.shape
-    _kv_shape(cache, q, heads, "q")
-    if ids is None:
-        ids = torch.empty((n, cache.n_kv_heads, n_sel), dtype=torch.int32, device=q.device)
-    qp, qs = _rows(q, "q")
-    b = _batch(table, lens, starts, n)
-    if ws is None:
-        ws = torch.empty(max(16, kv_select_workspace_bytes(cache, n, b.max_pages)), dtype=torch.uint8, device=q.device)
-    _check(load().qmv_kv_select(ctypes.byref(cache), ctypes.byref(b), _dtype(q), qp, qs, heads,
-                                _typed(ids, torch.int32, (n, cache.n_kv_heads, n_sel), "ids"), n_sel, _ptr(ws),
-                                ws.numel() * ws.element_size(), _stream(stream)), "qmv_kv_select")
-    return ids
+    return _nat().kv_select(ctypes.addressof(cache), q, table, lens, starts, n_sel, ws, ids, _on(stream))
 
 
 def check_rounding(stream=None):

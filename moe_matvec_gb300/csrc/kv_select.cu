@@ -11,9 +11,10 @@
 
 namespace qmv {
 
-constexpr int SEL_THREADS = 256;
+constexpr int SEL_THREADS = 512;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
-constexpr int SEL_UNROLL = 4;     // pages a lane works on at once
+constexpr int SEL_UNROLL = 2;     // pages a lane works on at once
+constexpr int SEL_TABLE = 2048;   // page indices brought into shared memory at a time
 constexpr int SEL_MAX_CLUSTER = 8;
 constexpr int SEL_MAX_GROUP = 256;  // query heads per kv head
 constexpr int SEL_CACHED = 8192;  // keys kept in shared memory while picking
@@ -94,10 +95,11 @@ __device__ __forceinline__ int block_scan(int v, int& total, int (&buf)[SEL_WARP
 // keys differ, done as soon as a whole bin is picked; then every thread counts
 // in a contiguous run of pages and writes at its place.
 template <int D>
-__global__ void __launch_bounds__(SEL_THREADS) kv_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(SEL_THREADS, 2) kv_select_kernel(const SelectParams p) {
   constexpr int LP = D == 64 ? 4 : D == 128 ? 8 : 16, LIVE = D / 16, PPW = 32 / LP, W4 = D / 4, E = D / 32;
   extern __shared__ __align__(16) uint32_t sq[];  // [G][2][D / 4] codes, then [G] scales
   __shared__ uint32_t keys[SEL_CACHED];
+  __shared__ int table[SEL_TABLE];
   __shared__ int hist[256], buf[SEL_WARPS], s_bin, s_left, s_done;
   __shared__ uint32_t s_lo[SEL_WARPS], s_hi[SEL_WARPS];
   pdl_launch_dependents();
@@ -133,29 +135,12 @@ __global__ void __launch_bounds__(SEL_THREADS) kv_select_kernel(const SelectPara
   const int sub = lane / LP, li = lane % LP;
   constexpr int STEP = SEL_WARPS * PPW;  // pages between a lane's pages
   const int bb = kv_bounds_bytes(D);
-  uint4 lo[SEL_UNROLL], hi[SEL_UNROLL];
-  float dk[SEL_UNROLL];
-  auto fetch = [&](int pb) {  // the lane's pages pb, pb + STEP, ..
-    int id[SEL_UNROLL];
-#pragma unroll
-    for (int i = 0; i < SEL_UNROLL; i++) id[i] = pb + i * STEP < pg1 ? kv_page(p.kv, s, pb + i * STEP) : -1;
-#pragma unroll
-    for (int i = 0; i < SEL_UNROLL; i++) {
-      lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-      dk[i] = 0.f;
-      const long long at = ((long long)max(id[i], 0) * p.kv.H + head) * bb;
-      if (id[i] >= 0 && QMV_CHECK(in_range(at, bb, p.kv.bounds_len, p.kv.err))) {
-        const uint8_t* b = p.kv.bounds + at;
-        dk[i] = *reinterpret_cast<const float*>(b);
-        if (li < LIVE) {
-          lo[i] = *reinterpret_cast<const uint4*>(b + KV_HEADER + 16 * li);
-          hi[i] = *reinterpret_cast<const uint4*>(b + KV_HEADER + D + 16 * li);
-        }
-      }
-    }
+  // The cache's indices of up to SEL_TABLE pages from `from` on: one load for
+  // the block, and the bounds' addresses then hang on shared memory alone.
+  auto load_table = [&](int from) {
+    for (int i = tid; i < min(SEL_TABLE, pg1 - from); i += SEL_THREADS) table[i] = kv_page(p.kv, s, from + i);
   };
-  int pb = pg0 + warp * PPW + sub;
-  fetch(pb);  // on their way while q is quantized
+  load_table(pg0);
   float* dq = reinterpret_cast<float*>(sq + p.G * 2 * W4);
   for (int g = warp; g < p.G; g += SEL_WARPS) {
     const long long at = t * p.q_stride + (long long)(head * p.G + g) * D;
@@ -179,40 +164,62 @@ __global__ void __launch_bounds__(SEL_THREADS) kv_select_kernel(const SelectPara
     if (lane == 0) dq[g] = d;
   }
   __syncthreads();
-  for (; pb - sub < pg1; pb += STEP * SEL_UNROLL) {
-    float best[SEL_UNROLL];
-#pragma unroll
-    for (int i = 0; i < SEL_UNROLL; i++) best[i] = -INFINITY;
-    for (int g = 0; g < p.G; g++) {
-      uint4 a = make_uint4(0, 0, 0, 0), b = a;
-      if (li < LIVE) {
-        a = *reinterpret_cast<const uint4*>(sq + g * 2 * W4 + 4 * li);
-        b = *reinterpret_cast<const uint4*>(sq + g * 2 * W4 + W4 + 4 * li);
-      }
-      const float d = dq[g];
+  for (int from = pg0; from < pg1; from += SEL_TABLE) {
+    if (from > pg0) {
+      __syncthreads();
+      load_table(from);
+      __syncthreads();
+    }
+    const int upto = min(from + SEL_TABLE, pg1);
+    // warps go their own ways: their loads and products overlap
+    for (int pb = from + warp * PPW + sub; pb - sub < upto; pb += STEP * SEL_UNROLL) {
+      uint4 lo[SEL_UNROLL], hi[SEL_UNROLL];
+      float dk[SEL_UNROLL];
 #pragma unroll
       for (int i = 0; i < SEL_UNROLL; i++) {
-        int u = __dp4a((int)a.x, (int)hi[i].x, 0);
-        u = __dp4a((int)a.y, (int)hi[i].y, u);
-        u = __dp4a((int)a.z, (int)hi[i].z, u);
-        u = __dp4a((int)a.w, (int)hi[i].w, u);
-        u = __dp4a((int)b.x, (int)lo[i].x, u);
-        u = __dp4a((int)b.y, (int)lo[i].y, u);
-        u = __dp4a((int)b.z, (int)lo[i].z, u);
-        u = __dp4a((int)b.w, (int)lo[i].w, u);
-#pragma unroll
-        for (int o = LP / 2; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-        best[i] = fmaxf(best[i], __fmul_rn((float)u, d));
+        const int pg = pb + i * STEP, id = pg < upto ? table[pg - from] : -1;
+        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+        dk[i] = 0.f;
+        const long long at = ((long long)max(id, 0) * p.kv.H + head) * bb;
+        if (id >= 0 && QMV_CHECK(in_range(at, bb, p.kv.bounds_len, p.kv.err))) {
+          const uint8_t* b = p.kv.bounds + at;
+          dk[i] = *reinterpret_cast<const float*>(b);
+          if (li < LIVE) {
+            lo[i] = *reinterpret_cast<const uint4*>(b + KV_HEADER + 16 * li);
+            hi[i] = *reinterpret_cast<const uint4*>(b + KV_HEADER + D + 16 * li);
+          }
+        }
       }
-    }
-    float dnow[SEL_UNROLL];
+      float best[SEL_UNROLL];
 #pragma unroll
-    for (int i = 0; i < SEL_UNROLL; i++) dnow[i] = dk[i];
-    if (pb - sub + STEP * SEL_UNROLL < pg1) fetch(pb + STEP * SEL_UNROLL);
-    if (li == 0) {
+      for (int i = 0; i < SEL_UNROLL; i++) best[i] = -INFINITY;
+      for (int g = 0; g < p.G; g++) {
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (li < LIVE) {
+          a = *reinterpret_cast<const uint4*>(sq + g * 2 * W4 + 4 * li);
+          b = *reinterpret_cast<const uint4*>(sq + g * 2 * W4 + W4 + 4 * li);
+        }
+        const float d = dq[g];
 #pragma unroll
-      for (int i = 0; i < SEL_UNROLL; i++)
-        if (pb + i * STEP < pg1) sc[pb + i * STEP] = __fmul_rn(best[i], dnow[i]);
+        for (int i = 0; i < SEL_UNROLL; i++) {
+          int u = __dp4a((int)a.x, (int)hi[i].x, 0);
+          u = __dp4a((int)a.y, (int)hi[i].y, u);
+          u = __dp4a((int)a.z, (int)hi[i].z, u);
+          u = __dp4a((int)a.w, (int)hi[i].w, u);
+          u = __dp4a((int)b.x, (int)lo[i].x, u);
+          u = __dp4a((int)b.y, (int)lo[i].y, u);
+          u = __dp4a((int)b.z, (int)lo[i].z, u);
+          u = __dp4a((int)b.w, (int)lo[i].w, u);
+#pragma unroll
+          for (int o = LP / 2; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+          best[i] = fmaxf(best[i], __fmul_rn((float)u, d));
+        }
+      }
+      if (li == 0) {
+#pragma unroll
+        for (int i = 0; i < SEL_UNROLL; i++)
+          if (pb + i * STEP < upto) sc[pb + i * STEP] = __fmul_rn(best[i], dk[i]);
+      }
     }
   }
   // the cluster's scores are written; the first CTA goes on
@@ -321,8 +328,8 @@ static cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(1ull << dev);
   }
-  // CTAs of a cluster: one round of the lanes' pages each, while all clusters
-  // still fit the GPU at once (two CTAs an SM) and up to the portable size
+  // CTAs of a cluster: a round of the lanes' pages each or more, while all
+  // clusters still fit the GPU at once (two CTAs an SM), up to the portable size
   const int round = SEL_WARPS * (32 / (D == 64 ? 4 : D == 128 ? 8 : 16)) * SEL_UNROLL;
   int ranks = 1;
   const long long heads = (long long)p.kv.H * p.kv.n_tok;
