@@ -1,0 +1,936 @@
+// Attention over the paged 8-bit cache.
+//
+// out = softmax(scale q K^T) V for the rows (token, query head) that share a
+// kv head.  Every byte of K and V is read once per item = (sequence, kv head,
+// up to 8 or 16 MT of its rows); up to about 16 rows the kernel is bound by that
+// read.  The units of work are tiles of 64 tokens of an item; the workers (the
+// warps of all SMs, or pairs of them for head_dim above 128) take equal
+// contiguous shares of all units of the batch, so ragged lengths and single
+// long sequences fill the GPU alike.  Warps never wait for one another: a share
+// that ends inside an item leaves its running maximum, sum and accumulator in
+// the workspace, and a second kernel joins an item's parts in their order.
+// (Shares per CTA, merged in shared memory, ended unevenly: a segment's end
+// waited for its slowest warp, 2.8 us a tile; 32 x 8192 tokens 77 us.)
+//
+// A worker feeds itself: the halves of its tiles, K (with the scales) and V, go
+// through a ring of stages of its own by bulk copies (one per page and half).
+// Once a half is read, the copies of the one that comes into its stage next are
+// started, so that K and V of the next tile are on their way while this one is
+// computed and no thread waits for a stage to become free.  What the tiles are
+// made of is worked out 32 tiles at a time, a lane each.
+//
+// The arithmetic (mma.sync m16n8k16, f16 operands, fp32 sums) has codes, exact
+// in f16, in B.  With fp32 queries the rows of A are 8 query rows in two f16
+// parts, q = hi + lo, rows 0-7 hi and 8-15 lo, and so are the softmax weights:
+// one MMA gives both products, and the padding that 8 rows would leave in a
+// 16-row operand does the work of fp32 precision.  Where a kv head has more than
+// 8 rows of f16 or bfloat16 queries (HALF) A holds 16 of them: hi alone is q
+// then, exactly but for what lies 2^-25 below the row's largest; the weights
+// keep their two parts, in two MMAs.
+//
+// The order of the contraction is free, so each lane takes the 16-byte pieces
+// that the record layout puts in its reach: for S = q K^T lane (r, c) = (lane /
+// 4, lane % 4) reads dimensions 64 h + 16 c .. + 15 of token 16 (r / 2) + 2 j +
+// r % 2 of the tile (MMA column r of group j), and S then leaves lane c with
+// tokens 16 c .. 16 c + 15 of row r: exactly the slots whose V codes are 16
+// contiguous bytes of dimension 8 n + r.  No shuffle or transposition lies
+// between the two products.
+#pragma once
+#include <limits.h>
+
+#include <atomic>
+
+#include "float_io.cuh"
+#include "kv_cache.cuh"
+#include "kv_launch.h"
+#include "launch.h"
+
+namespace qmv {
+
+constexpr int AT_TILE = 64;  // tokens of a unit
+constexpr int AT_MAX_RING = 8;
+constexpr int AT_MAX_CTAS = 160;
+// Softmax weights enter f16 times 2^6 and may exceed 1 by 2^8 (a running
+// maximum is only followed when it is left behind by more than that) and, by
+// the reference scale, by 2: below 2^15, and 22 bits down to 2^-9 of the
+// largest, an error of 2^-31 of it below that.
+constexpr float AT_P_SCALE = 64.f;
+constexpr float AT_LAZY = 8.f;
+
+// Warps of a CTA: the quarters of an SM hold whole warps, 8 of up to 255
+// registers a thread or 12 of up to 168, and q and the accumulators take them.
+__host__ __device__ constexpr int at_warps(int D, int MT, bool HALF) { return D * MT <= 64 && !HALF ? 12 : 8; }
+// Warps that share a tile: from head_dim 192 on two, whose stages would not
+// fit shared memory else.
+__host__ __device__ constexpr int at_split(int D) { return D > 128 ? 2 : 1; }
+// Shared-memory bytes from one page's V to the next: a lane's piece of page c /
+// (P / 16) must fall into another bank group than its neighbours'.
+__host__ __device__ constexpr int at_v_stride(int D, int P) { return P * D + (P == 16 ? 32 : P == 32 ? 64 : 0); }
+// A stage holds either half of a tile.
+__host__ __device__ constexpr int at_stage_bytes(int D) { return AT_TILE * D + 128; }
+// A part in the workspace: m and l of each row, then the rows.  Slot 0 of a
+// warp: the item that its share begins inside of (and what it hands to its
+// partner); slot 1: the one that it ends inside of.
+// (R rows)
+__host__ __device__ constexpr int at_slot_floats(int D, int R) { return R * (D + 2); }
+// What the join needs of an item: the workers first .. last that hold its
+// parts (last < first: there is nothing to join), and its rows.
+struct AttendJoin {
+  int first, last, tbase, row0, nrows, head, pad[2];
+};
+
+struct AttendParams {
+  KvParams kv;
+  const void* q;
+  void* out;
+  long long q_stride;
+  float scale_log2;  // scale * log2(e)
+  int dtype, G, n_heads, causal, window;
+  const int32_t* sel;
+  int n_sel, ring;
+  float* slots;       // [worker][SP warps][2]
+  int* n_items;       // items of the batch
+  AttendJoin* joins;  // [item]
+  int max_items;
+#ifdef QMV_DEBUG
+  long long q_len, out_len, sel_len;
+#endif
+};
+
+struct AttendItem {
+  int s, tbase, nrows, row0, head;  // rows row0 .. of the item's row space; row r: token tbase + r / G
+  KvSeq seq;
+  int tile0, tiles;                 // first tile, units
+  int k;                            // the unit asked for
+  int id;                           // of the batch's items
+};
+
+// Tiles of a sequence that any of its tokens may see.
+__device__ __forceinline__ void seq_tiles(const AttendParams& p, const KvSeq& q, int& tile0, int& tiles) {
+  tile0 = p.window > 0 ? max(q.len - q.n - p.window + 1, 0) / AT_TILE : 0;
+  tiles = max((q.len + AT_TILE - 1) / AT_TILE - tile0, 1);
+}
+
+// Unit u of the batch (ids: the sequences' first items; base: prefix sums of the sequences' units or, when each
+// token has its own pages, their first tokens).
+template <int R>
+__device__ __forceinline__ AttendItem locate(const AttendParams& p, const long long* base, const int* ids, long long u) {
+  AttendItem it;
+  const int H = p.kv.H;
+  long long key = u;
+  if (p.sel) {
+    const int tiles = (p.n_sel * p.kv.P + AT_TILE - 1) / AT_TILE, n_rt = (p.G + R - 1) / R;
+    const long long item = u / tiles;
+    it.k = (int)(u - item * tiles);
+    it.id = (int)item;
+    it.tiles = tiles;
+    it.tile0 = 0;
+    it.row0 = (int)(item % n_rt) * R;
+    const long long th = item / n_rt;
+    it.head = (int)(th % H);
+    it.tbase = (int)(th / H);
+    it.nrows = p.G;
+    key = it.tbase;
+  }
+  int lo = 0, hi = p.kv.n_seq;  // base[lo] <= key < base[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (base[mid] <= key) lo = mid; else hi = mid;
+  }
+  it.s = lo;
+  it.seq = kv_seq(p.kv, lo);
+  if (!p.sel) {
+    seq_tiles(p, it.seq, it.tile0, it.tiles);
+    it.nrows = it.seq.n * p.G;
+    const int n_rt = (it.nrows + R - 1) / R;
+    const long long local = u - base[lo], item = local / it.tiles;
+    it.k = (int)(local - item * it.tiles);
+    it.id = ids[lo] + (int)item;
+    it.row0 = (int)(item % n_rt) * R;
+    it.head = (int)(item / n_rt);
+    it.tbase = it.seq.t0;
+  }
+  return it;
+}
+
+// The item after `it`, from its first unit.
+template <int R>
+__device__ __forceinline__ void next_item(const AttendParams& p, const long long* base, AttendItem& it) {
+  it.k = 0;
+  it.id++;
+  it.row0 += R;
+  if (it.row0 < it.nrows) return;
+  it.row0 = 0;
+  if (++it.head < p.kv.H) return;
+  it.head = 0;
+  const int n_seq = p.kv.n_seq;
+  if (p.sel) {
+    it.tbase++;
+    while (it.s + 1 < n_seq && base[it.s + 1] <= it.tbase) it.s++;
+    it.seq = kv_seq(p.kv, it.s);
+  } else {
+    do {
+      if (++it.s >= n_seq) return;  // there is none: the caller is at its last unit
+    } while (base[it.s] == base[it.s + 1]);
+    it.seq = kv_seq(p.kv, it.s);
+    seq_tiles(p, it.seq, it.tile0, it.tiles);
+    it.nrows = it.seq.n * p.G;
+    it.tbase = it.seq.t0;
+  }
+}
+
+// Position of row r's token (the row space of `it`).
+__device__ __forceinline__ int row_pos(const AttendParams& p, const AttendItem& it, int r) {
+  return it.seq.len - it.seq.n + (it.tbase - it.seq.t0) + r / p.G;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four code bytes (code + 128) as two f16 pairs, exactly: 0x6400 | b is 1024 +
+// b, less 1152 is the code.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& a, uint32_t& b) {
+  const __half2 off = __half2half2(__ushort_as_half(0x6480u));
+  const uint32_t x = __byte_perm(w, 0x64646464u, 0x4140), y = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 hx = __hsub2(*reinterpret_cast<const __half2*>(&x), off);
+  const __half2 hy = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
+  a = *reinterpret_cast<const uint32_t*>(&hx);
+  b = *reinterpret_cast<const uint32_t*>(&hy);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// (x, y) as two f16 pairs, hi + lo
+__device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the same with a zero sum to start from
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Four consecutive values of a float tensor of type dt.
+__device__ __forceinline__ void load4(const void* base, long long at, int dt, float (&v)[4]) {
+  if (dt == QMV_DT_F32) load_vec<4>(static_cast<const float*>(base) + at, v);
+  else if (dt == QMV_DT_F16) load_vec<4>(static_cast<const __half*>(base) + at, v);
+  else load_vec<4>(static_cast<const __nv_bfloat16*>(base) + at, v);
+}
+// Two consecutive values into one (at even).
+__device__ __forceinline__ void store2(void* base, long long at, int dt, float x, float y) {
+  if (dt == QMV_DT_F32)
+    *reinterpret_cast<float2*>(static_cast<float*>(base) + at) = make_float2(x, y);
+  else if (dt == QMV_DT_F16)
+    *reinterpret_cast<__half2*>(static_cast<__half*>(base) + at) = __floats2half2_rn(x, y);
+  else
+    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(base) + at) = __floats2bfloat162_rn(x, y);
+}
+
+// Rows of an item, and of a lane's A fragment (its rows r and, with HALF, r + 8).
+__host__ __device__ constexpr int at_rows(int MT, bool HALF) { return (HALF ? 16 : 8) * MT; }
+
+template <int D, int P, int MT, bool HALF>
+__global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kernel(const AttendParams p) {
+  constexpr int W = at_warps(D, MT, HALF), SP = at_split(D), NG = W / SP, NJ = 8 / SP;
+  // independent products in flight: a chain of MMAs into one accumulator waits
+  // for each of them
+  constexpr int IL = MT == 1 ? 4 : 2;
+  constexpr int R = at_rows(MT, HALF), NR = HALF ? 2 : 1, KS = D / 16, NV = D / 8, ppt = AT_TILE / P;
+  constexpr int K_STRIDE = KV_HEADER + P * D, V_STRIDE = at_v_stride(D, P), STAGE = at_stage_bytes(D);
+  static_assert(ppt * K_STRIDE <= STAGE && (ppt - 1) * V_STRIDE + P * D <= STAGE, "a stage holds either half");
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int S = p.ring, n_seq = p.kv.n_seq;
+  // stages [group][S] | barriers [group][S] | first units | first items
+  uint8_t* cur = smem + (size_t)NG * S * STAGE;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(cur);
+  cur += NG * S * sizeof(uint64_t);
+  long long* const base = reinterpret_cast<long long*>(cur);
+  int* const ids = reinterpret_cast<int*>(base + n_seq + 1);
+  __shared__ long long wtot[W];
+  __shared__ int wids[W];
+  __shared__ int stop;  // a wait ran out: no copy is started any more
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  if (tid < NG * S) mbar_init(&bars[tid], 1);
+  if (tid == 0) stop = 0;
+  fence_mbar_init();
+  pdl_wait();
+  // the sequences' first units (first tokens) and items
+  long long total = 0;
+  int items = 0;
+  for (int c = 0; c < n_seq; c += W * 32) {
+    const int s = c + tid;
+    long long units = 0;
+    int first = 0, mine = 0;
+    if (s < n_seq) {
+      const KvSeq q = kv_seq(p.kv, s);
+      int t0, tiles;
+      seq_tiles(p, q, t0, tiles);
+      mine = (q.n * p.G + R - 1) / R * p.kv.H;
+      units = (long long)mine * tiles;
+      first = q.t0;
+    }
+    long long inc = units;
+    int inc_ids = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      const int w = __shfl_up_sync(0xffffffffu, inc_ids, o);
+      if (lane >= o) inc += v, inc_ids += w;
+    }
+    if (lane == 31) wtot[warp] = inc, wids[warp] = inc_ids;
+    __syncthreads();
+    long long before = total;
+    int before_ids = items;
+#pragma unroll
+    for (int i = 0; i < W; i++) {
+      if (i < warp) before += wtot[i], before_ids += wids[i];
+      total += wtot[i], items += wids[i];
+    }
+    if (s < n_seq) {
+      base[s] = p.sel ? first : before + inc - units;
+      ids[s] = before_ids + inc_ids - mine;
+    }
+    __syncthreads();
+  }
+  if (p.sel) {
+    const int tiles = (p.n_sel * P + AT_TILE - 1) / AT_TILE;
+    items = p.kv.n_tok * p.kv.H * ((p.G + R - 1) / R);
+    total = (long long)items * tiles;
+  } else if (tid == 0) {
+    base[n_seq] = total;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && tid == 0) *p.n_items = items;
+
+  // The workers: SP warps that work on one tile at a time; neighbours in number
+  // sit on different SMs, so that a small batch spreads.
+  const int group = warp / SP, part = warp % SP;
+  const long long share = (total + (long long)NG * gridDim.x - 1) / ((long long)NG * gridDim.x);
+  const int worker = group * gridDim.x + blockIdx.x;
+  const long long u0 = min(worker * share, total), u1 = min(total, u0 + share);
+  const int units = (int)(u1 - u0);
+  if (units == 0) return;
+  const int r = lane >> 2, c = lane & 3;
+  uint8_t* const stages = smem + (size_t)group * S * STAGE;
+  uint64_t* const full = bars + group * S;
+  const uint64_t policy = policy_evict_first();
+  bool dead = false;
+
+  // ---- what the units [planned, planned + 32) of the share are made of, a lane
+  // each: for each page of the tile its index in the cache and in the sequence
+  // (or -1), and the kv head
+  int planned = 0, page[ppt], idx[ppt], head = 0;
+  auto plan = [&](int from) {
+    planned = from;
+#pragma unroll
+    for (int i = 0; i < ppt; i++) page[i] = idx[i] = -1;
+    if (from + lane >= units) return;
+    const AttendItem it = locate<R>(p, base, ids, u0 + from + lane);
+    head = it.head;
+    const int rows = min(it.row0 + R, it.nrows) - 1;
+    // positions that some row of the item may see: [vis0, vis1)
+    const int vis1 = p.causal ? row_pos(p, it, rows) + 1 : it.seq.len;
+    const int vis0 = p.window > 0 ? row_pos(p, it, it.row0) - p.window + 1 : 0;
+#pragma unroll
+    for (int i = 0; i < ppt; i++) {
+      int pg;
+      if (p.sel) {
+        const int j = it.k * ppt + i;
+        const long long at = ((long long)it.tbase * p.kv.H + it.head) * p.n_sel + j;
+        pg = j < p.n_sel && QMV_CHECK(in_range(at, 1, p.sel_len, p.kv.err)) ? p.sel[at] : -1;
+        if (pg >= p.kv.max_pages) {
+          set_error(p.kv.err, QMV_DEVERR_PAGE);
+          pg = -1;
+        }
+        // a token that no sequence covers has no pages
+        if (it.tbase < it.seq.t0 || it.tbase >= it.seq.t0 + it.seq.n) pg = -1;
+      } else {
+        pg = (it.tile0 + it.k) * ppt + i;
+      }
+      const long long pos = (long long)pg * P;
+      if (pg < 0 || pos >= vis1 || pos >= it.seq.len || pos + P <= vis0) continue;
+      page[i] = kv_page(p.kv, it.s, pg);
+      idx[i] = page[i] < 0 ? -1 : pg;
+    }
+  };
+  // Starts the copies of half h (unit h / 2 of the share: K, then V) into stage
+  // st, which nothing reads any more; by whole warps, lane 0 of the first posts
+  // the bytes and copies.  `now`: the unit that is worked on.
+  auto fill = [&](int h, int st, int now) {
+    const int t = h >> 1;
+    if (t >= units || dead) return;
+    if (t - planned >= 32) plan(now);
+    const int src = t - planned;
+    int pg[ppt];
+#pragma unroll
+    for (int i = 0; i < ppt; i++) pg[i] = __shfl_sync(0xffffffffu, page[i], src);
+    const int hd = __shfl_sync(0xffffffffu, head, src);
+    if (part != 0 || lane != 0 || *const_cast<volatile int*>(&stop)) return;
+    const bool v = h & 1;
+    const uint32_t bytes = v ? P * D : K_STRIDE;
+    uint32_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < ppt; i++) sum += pg[i] < 0 ? 0u : bytes;
+    mbar_arrive_expect_tx(&full[st], sum);
+#pragma unroll
+    for (int i = 0; i < ppt; i++) {
+      if (pg[i] < 0) continue;
+      const long long at = ((long long)pg[i] * p.kv.H + hd) * kv_page_bytes(D, P) + (v ? K_STRIDE : 0);
+      uint8_t* dst = stages + st * STAGE + i * (v ? V_STRIDE : K_STRIDE);
+      if (QMV_CHECK(in_range(at, bytes, p.kv.pages_len, p.kv.err)) && QMV_CHECK(smem_in_range(dst, bytes, p.kv.err)))
+        bulk_copy_g2s_hint(dst, p.kv.pages + at, bytes, &full[st], policy);
+      else
+        mbar_complete_tx(&full[st], bytes);
+    }
+  };
+  // The worker has read stage st: half h + S may come into it.
+  auto release = [&](int h, int st, int now) {
+    if constexpr (SP > 1) named_sync(2 + group, SP * 32);
+    else __syncwarp();
+    fill(h + S, st, now);
+  };
+  // A wait that runs out ends the warp's arithmetic, not its steps: it goes on
+  // meeting its partner at the barriers.
+  auto landed = [&](int st, int phase) {
+    if (dead) return;
+    if (__all_sync(0xffffffffu, mbar_wait(&full[st], phase, p.kv.err))) return;
+    dead = true;
+    stop = 1;
+  };
+  plan(0);
+  for (int h = 0; h < S; h++) fill(h, h, 0);
+  int tile = 0, st = 0, phase = 0;  // the next unit of the share; stage and phase of its next half
+  auto next_stage = [&] {
+    if (++st == S) {
+      st = 0;
+      phase ^= 1;
+    }
+  };
+
+  long long u = u0;
+  AttendItem it = locate<R>(p, base, ids, u);
+  for (; u < u1; next_item<R>(p, base, it)) {
+    const int seg = (int)min((long long)(it.tiles - it.k), u1 - u);  // units of this item in the share
+    // q of the lane's rows as A fragments
+    uint32_t qa[MT][KS][4];
+    float qs[MT][NR];
+    int lim[MT][NR], low[MT][NR];
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+      for (int nr = 0; nr < NR; nr++) {
+        const int row = it.row0 + (mt * NR + nr) * 8 + r;
+        const bool live = row < it.nrows;
+        const int pos = live ? row_pos(p, it, row) : -1;
+        lim[mt][nr] = live ? (p.causal ? min(pos + 1, it.seq.len) : it.seq.len) : 0;
+        low[mt][nr] = p.window > 0 ? pos - p.window + 1 : INT_MIN;
+        const long long at = (long long)(it.tbase + row / p.G) * p.q_stride + (long long)(it.head * p.G + row % p.G) * D;
+        float v[KS][4], amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+          const int d0 = 64 * (k >> 2) + 16 * c + 4 * (k & 3);
+          v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.f;
+          if (live && QMV_CHECK(in_range(at + d0, 4, p.q_len, p.kv.err))) load4(p.q, at + d0, p.dtype, v[k]);
+#pragma unroll
+          for (int e = 0; e < 4; e++) amax = fmaxf(amax, fabsf(v[k][e]));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // the row over a power of two near its largest magnitude (exact), so that
+        // two f16 parts hold 22 bits of it
+        const int e = min(max((int)(__float_as_uint(amax) >> 23), 1), 253);
+        const float down = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
+        // (the sign of the scale goes into q: a larger product is then a larger logit)
+        const float down1 = p.scale_log2 < 0.f ? -down : down;
+        qs[mt][nr] = __uint_as_float((uint32_t)e << 23) * fabsf(p.scale_log2);
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+          if constexpr (HALF) {
+            qa[mt][k][nr] = pack_f16(v[k][0] * down1, v[k][1] * down1);
+            qa[mt][k][2 + nr] = pack_f16(v[k][2] * down1, v[k][3] * down1);
+          } else {
+            split_f16(v[k][0] * down1, v[k][1] * down1, qa[mt][k][0], qa[mt][k][1]);
+            split_f16(v[k][2] * down1, v[k][3] * down1, qa[mt][k][2], qa[mt][k][3]);
+          }
+        }
+      }
+    }
+    float o[MT][NV][4], m[MT][NR], l[MT][NR], vref = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+      for (int nr = 0; nr < NR; nr++) {
+        m[mt][nr] = -INFINITY;
+        l[mt][nr] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < NV; n++) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
+    }
+
+    for (const int end = tile + seg; tile < end; tile++) {
+      // the lane's 16 tokens are a piece of one page (of them the warp's: 2 NJ
+      // from 16 c + 2 NJ part on)
+      const int sub = 16 * c / P;
+      int pidx = -1;
+#pragma unroll
+      for (int i = 0; i < ppt; i++) {
+        const int v = __shfl_sync(0xffffffffu, idx[i], tile - planned);
+        if (sub == i) pidx = v;
+      }
+      const int pos0 = pidx < 0 ? INT_MAX - 64 : pidx * P + (16 * c) % P + 2 * NJ * part;
+      float dk = 0.f, dv = 0.f;
+      float s[MT][NR][NJ][2];
+      landed(st, phase);
+      if (!dead) {
+        const uint8_t* stage = stages + st * STAGE;
+        if (pidx >= 0) {
+          const float2 sc = *reinterpret_cast<const float2*>(stage + sub * K_STRIDE);
+          dk = sc.x;
+          dv = sc.y;
+        }
+        // S = q K^T, group j: tokens 2 j, 2 j + 1 of the lane's, row r
+        const int ksub = 16 * (r >> 1) / P, kt = (16 * (r >> 1)) % P + (r & 1);
+        const uint8_t* krow = stage + ksub * K_STRIDE + KV_HEADER + kt * 64 + 16 * c + 128 * NJ * part;
+#pragma unroll
+        for (int jg = 0; jg < NJ; jg += IL) {
+          float acc[MT][IL][4];
+#pragma unroll
+          for (int h = 0; h < D / 64; h++) {
+            uint32_t w[IL][4];
+#pragma unroll
+            for (int i = 0; i < IL; i++) load_words<4>(krow + h * P * 64 + (jg + i) * 128, w[i]);
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+#pragma unroll
+              for (int i = 0; i < IL; i++) {
+                uint32_t b0, b1;
+                codes_to_f16(w[i][k], b0, b1);
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++) {
+                  if (h == 0 && k == 0) mma16816_first(acc[mt][i], qa[mt][0], b0, b1);
+                  else mma16816(acc[mt][i], qa[mt][4 * h + k], b0, b1);
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < IL; i++) {
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+              for (int e = 0; e < 2; e++) {
+                if constexpr (HALF) s[mt][0][jg + i][e] = acc[mt][i][e], s[mt][NR - 1][jg + i][e] = acc[mt][i][2 + e];
+                else s[mt][0][jg + i][e] = acc[mt][i][e] + acc[mt][i][2 + e];
+              }
+            }
+          }
+        }
+      }
+      release(2 * tile, st, tile);
+      next_stage();
+      uint32_t pa[MT][NJ / 2][4], pb[HALF ? MT : 1][NJ / 2][4];
+      if (!dead) {
+        // tiles at an end of some row's range: products out of it become -inf
+        bool inside = true;
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+          for (int nr = 0; nr < NR; nr++) inside = inside && pos0 >= low[mt][nr] && pos0 + 2 * NJ <= lim[mt][nr];
+        }
+        if (!__all_sync(0xffffffffu, inside)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+            for (int nr = 0; nr < NR; nr++) {
+#pragma unroll
+              for (int j = 0; j < NJ; j++) {
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                  if (pos0 + 2 * j + e >= lim[mt][nr] || pos0 + 2 * j + e < low[mt][nr]) s[mt][nr][j][e] = -INFINITY;
+              }
+            }
+          }
+        }
+        // values share one reference scale per warp: raised when a page's is over twice it
+        float vmax = fmaxf(dv, __shfl_xor_sync(0xffffffffu, dv, 1));
+        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+        float vfix = 1.f;
+        if (vmax > 2.f * vref) {
+          vfix = vref / vmax;
+          vref = vmax;
+        }
+        const float vrel = vref > 0.f ? __fdividef(dv, vref) * AT_P_SCALE : 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+          float fix[NR];
+#pragma unroll
+          for (int nr = 0; nr < NR; nr++) {
+            // the lane's products share one factor to logits in powers of two
+            // (not 0: a masked product is -inf)
+            const float f = fmaxf(qs[mt][nr] * dk, 0x1p-120f);
+            float mx = s[mt][nr][0][0];
+#pragma unroll
+            for (int j = 0; j < NJ; j++) mx = fmaxf(mx, fmaxf(s[mt][nr][j][0], s[mt][nr][j][1]));
+            mx *= f;
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            fix[nr] = vfix;
+            if (mx > m[mt][nr] + AT_LAZY || (m[mt][nr] == -INFINITY && mx > m[mt][nr])) {
+              const float alpha = ex2(m[mt][nr] - mx);
+              fix[nr] *= alpha;
+              l[mt][nr] *= alpha;
+              m[mt][nr] = mx;
+            }
+            const float ms = m[mt][nr] == -INFINITY ? 0.f : m[mt][nr];
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < NJ; j++) {
+              const float a = ex2(fmaf(s[mt][nr][j][0], f, -ms)), b = ex2(fmaf(s[mt][nr][j][1], f, -ms));
+              sum += a + b;
+              // HALF: high parts in A's rows of pa, low parts in those of pb
+              if constexpr (HALF)
+                split_f16(a * vrel, b * vrel, pa[mt][j >> 1][2 * (j & 1) + nr], pb[mt][j >> 1][2 * (j & 1) + nr]);
+              else
+                split_f16(a * vrel, b * vrel, pa[mt][j >> 1][2 * (j & 1)], pa[mt][j >> 1][2 * (j & 1) + 1]);
+            }
+            l[mt][nr] += sum;
+          }
+          if (__any_sync(0xffffffffu, fix[0] != 1.f || fix[NR - 1] != 1.f)) {
+#pragma unroll
+            for (int n2 = 0; n2 < NV; n2++) {
+              o[mt][n2][0] *= fix[0], o[mt][n2][1] *= fix[0];
+              o[mt][n2][2] *= fix[NR - 1], o[mt][n2][3] *= fix[NR - 1];
+            }
+          }
+        }
+      }
+      landed(st, phase);
+      if (!dead) {
+        // O += P V: k-step kk holds the lane's tokens 4 kk .. + 3
+        const uint8_t* vrow = stages + st * STAGE + sub * V_STRIDE + r * P + (16 * c) % P + 2 * NJ * part;
+#pragma unroll
+        for (int ng = 0; ng < NV; ng += IL) {
+          uint32_t w[IL][NJ / 2];
+#pragma unroll
+          for (int i = 0; i < IL; i++) load_words<NJ / 2>(vrow + (ng + i) * 8 * P, w[i]);
+#pragma unroll
+          for (int kk = 0; kk < NJ / 2; kk++) {
+#pragma unroll
+            for (int i = 0; i < IL; i++) {
+              uint32_t b0, b1;
+              codes_to_f16(w[i][kk], b0, b1);
+#pragma unroll
+              for (int mt = 0; mt < MT; mt++) {
+                mma16816(o[mt][ng + i], pa[mt][kk], b0, b1);
+                if constexpr (HALF) mma16816(o[mt][ng + i], pb[mt][kk], b0, b1);
+              }
+            }
+          }
+        }
+      }
+      release(2 * tile + 1, st, tile);
+      next_stage();
+    }
+
+    // ---- the item's rows, or the share's part of them
+    const bool begins = it.k == 0, ends = it.k + seg == it.tiles, whole = begins && ends;
+    // (with page lists a token may lie in no sequence: its row is not written)
+    const bool covered = it.tbase >= it.seq.t0 && it.tbase < it.seq.t0 + it.seq.n;
+    float back = vref * (1.f / AT_P_SCALE);
+    // column pair n2 of the lane's row: o in fp32, without the reference scale
+    auto pair = [&](int mt, int nr, int n2, float f) {
+      const float(&x)[4] = o[mt][n2];
+      return HALF ? make_float2(x[2 * nr] * f, x[2 * nr + 1] * f) : make_float2((x[0] + x[2]) * f, (x[1] + x[3]) * f);
+    };
+    auto write_slot = [&](float* slot, int mt, int nr) {
+      const int row = (mt * NR + nr) * 8 + r;
+      if (c == 0) {
+        // (the maximum of a row that is no number ignores that)
+        slot[2 * row] = l[mt][nr] != l[mt][nr] ? NAN : m[mt][nr];
+        slot[2 * row + 1] = l[mt][nr];
+      }
+      float* dst = slot + 2 * R + row * D + 2 * c;
+#pragma unroll
+      for (int n2 = 0; n2 < NV; n2++) *reinterpret_cast<float2*>(dst + 8 * n2) = pair(mt, nr, n2, back);
+    };
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+      for (int nr = 0; nr < NR; nr++) {
+        l[mt][nr] += __shfl_xor_sync(0xffffffffu, l[mt][nr], 1);
+        l[mt][nr] += __shfl_xor_sync(0xffffffffu, l[mt][nr], 2);
+      }
+    }
+    float* const slots = p.slots + (size_t)(worker * SP) * 2 * at_slot_floats(D, R);
+    if constexpr (SP > 1) {
+      // the partner's half of the tokens comes over its slot 0
+      float* const other = slots + 2 * at_slot_floats(D, R);
+      if (part == 1) {
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+          for (int nr = 0; nr < NR; nr++) write_slot(other, mt, nr);
+        }
+      }
+      named_sync(2 + group, SP * 32);
+      if (part == 0) {
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+          for (int nr = 0; nr < NR; nr++) {
+            const int row = (mt * NR + nr) * 8 + r;
+            const float2 st2 = __ldcg(reinterpret_cast<const float2*>(other + 2 * row));
+            const float M = fmaxf(m[mt][nr], st2.x);
+            const float f0 = m[mt][nr] == -INFINITY ? 0.f : ex2(m[mt][nr] - M) * back;
+            const float f1 = st2.x == -INFINITY ? 0.f : ex2(st2.x - M);
+            const float* src = other + 2 * R + row * D + 2 * c;
+#pragma unroll
+            for (int n2 = 0; n2 < NV; n2++) {
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(src + 8 * n2));
+              const float2 y = pair(mt, nr, n2, f0);
+              o[mt][n2][2 * nr] = fmaf(x.x, f1, y.x);
+              o[mt][n2][2 * nr + 1] = fmaf(x.y, f1, y.y);
+              if constexpr (!HALF) o[mt][n2][2] = o[mt][n2][3] = 0.f;
+            }
+            l[mt][nr] = (m[mt][nr] == -INFINITY ? l[mt][nr] : l[mt][nr] * ex2(m[mt][nr] - M)) + st2.y * (st2.x == -INFINITY ? 1.f : f1);
+            m[mt][nr] = M;
+          }
+        }
+        back = 1.f;
+      }
+    }
+    if (part == 0) {
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+        for (int nr = 0; nr < NR; nr++) {
+          const int rr = it.row0 + (mt * NR + nr) * 8 + r;
+          if (!whole) {
+            write_slot(slots + (begins ? at_slot_floats(D, R) : 0), mt, nr);
+          } else if (covered && rr < it.nrows) {
+            // (a row that is no number stays one)
+            const float f = l[mt][nr] > 0.f ? back / l[mt][nr] : l[mt][nr] != l[mt][nr] ? NAN : 0.f;
+            const long long at = ((long long)(it.tbase + rr / p.G) * p.n_heads + it.head * p.G + rr % p.G) * D + 2 * c;
+#pragma unroll
+            for (int n2 = 0; n2 < NV; n2++) {
+              const float2 x = pair(mt, nr, n2, f);
+              if (QMV_CHECK(in_range(at + 8 * n2, 2, p.out_len, p.kv.err))) store2(p.out, at + 8 * n2, p.dtype, x.x, x.y);
+            }
+          }
+        }
+      }
+    }
+    if (begins && part == 0 && lane == 0) {
+      AttendJoin j{};
+      j.first = worker;
+      j.last = whole || !covered ? worker - 1 : (int)((u + it.tiles - 1) / share);
+      j.tbase = it.tbase;
+      j.row0 = it.row0;
+      j.nrows = it.nrows;
+      j.head = it.head;
+      if (it.id < p.max_items) p.joins[it.id] = j;
+    }
+    u += seg;
+  }
+  // After a wait that ran out, copies that nobody waits for may be in flight:
+  // the CTA keeps its shared memory a while longer than any copy takes.
+  if (*const_cast<volatile int*>(&stop)) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 1 << 24) {
+    }
+  }
+}
+
+// Joins the parts of an item: slot 1 of its first worker, slot 0 of the others,
+// in that order (whatever the timing: the result is reproducible).  A
+// row is the work of JW warps: each goes over every JW-th part with its lanes
+// over the columns, AHEAD parts on their way at a time, and the JW results are
+// added in order.  One warp a row, eight rows a block, where there are many
+// items (of few parts each); 16 warps, one row a block, where the blocks of a
+// few items leave SMs to spare (one sequence of 131072 tokens and 8 kv heads:
+// 147 parts an item).
+__host__ __device__ constexpr int join_rows(int JW) { return JW == 1 ? 8 : 1; }
+template <int D, int R, int JW>
+__global__ void __launch_bounds__(join_rows(JW) * JW * 32, JW == 1 ? 1 : 2) kv_join_kernel(const AttendParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int SLOT = at_slot_floats(D, R), SP = at_split(D), ROWS = join_rows(JW), AHEAD = JW == 1 ? 8 : 4;
+  __shared__ float sm[ROWS][JW][2];
+  __shared__ float sx[ROWS][JW][JW > 1 ? D : 1];
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % JW, rb = threadIdx.x / (32 * JW);
+  const int n_items = *p.n_items;
+  const AttendJoin j = p.joins[blockIdx.x];
+  if ((int)blockIdx.x >= n_items || j.last < j.first) return;
+  const int row = blockIdx.y * ROWS + rb, rr = j.row0 + row, parts = j.last - j.first + 1;
+  float M = -INFINITY, L = 0.f, acc[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; i++) acc[i] = 0.f;
+  for (int k0 = w; k0 < parts; k0 += JW * AHEAD) {
+    float2 st[AHEAD];
+    float xs[AHEAD][D / 32];
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++) {
+      const int k = min(k0 + i * JW, parts - 1);
+      const float* s = p.slots + ((size_t)(j.first + k) * SP * 2 + (k == 0 ? 1 : 0)) * SLOT;
+      st[i] = *reinterpret_cast<const float2*>(s + 2 * row);
+#pragma unroll
+      for (int q = 0; q < D / 64; q++) {
+        const float2 v = *reinterpret_cast<const float2*>(s + 2 * R + row * D + 64 * q + 2 * lane);
+        xs[i][2 * q] = v.x;
+        xs[i][2 * q + 1] = v.y;
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++)
+      if (k0 + i * JW < parts) top = fmaxf(top, st[i].x);
+    const float back = M == -INFINITY ? 0.f : ex2(M - top);
+    M = top;
+    L *= back;
+#pragma unroll
+    for (int e = 0; e < D / 32; e++) acc[e] *= back;
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++) {
+      if (k0 + i * JW >= parts) continue;
+      const float f = st[i].x == -INFINITY ? 0.f : ex2(st[i].x - M);
+      L = fmaf(st[i].y, f, L);
+#pragma unroll
+      for (int e = 0; e < D / 32; e++) acc[e] = fmaf(xs[i][e], f, acc[e]);
+    }
+  }
+  if constexpr (JW > 1) {
+    if (lane == 0) {
+      sm[rb][w][0] = M;
+      sm[rb][w][1] = L;
+    }
+#pragma unroll
+    for (int e = 0; e < D / 32; e++) sx[rb][w][64 * (e >> 1) + 2 * lane + (e & 1)] = acc[e];
+    __syncthreads();
+    if (w != 0) return;
+    M = -INFINITY;
+    for (int i = 0; i < JW; i++) M = fmaxf(M, sm[rb][i][0]);
+    L = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; e++) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < JW; i++) {
+      const float m = sm[rb][i][0], l = sm[rb][i][1], f = m == -INFINITY && l == l ? 0.f : ex2(m - M);
+      L = fmaf(l, f, L);
+#pragma unroll
+      for (int e = 0; e < D / 32; e++) acc[e] = fmaf(sx[rb][i][64 * (e >> 1) + 2 * lane + (e & 1)], f, acc[e]);
+    }
+  }
+  if (rr >= j.nrows) return;
+  const float inv = L > 0.f ? 1.f / L : L != L ? NAN : 0.f;
+  const long long at = ((long long)(j.tbase + rr / p.G) * p.n_heads + j.head * p.G + rr % p.G) * D + 2 * lane;
+#pragma unroll
+  for (int q = 0; q < D / 64; q++)
+    if (QMV_CHECK(in_range(at + 64 * q, 2, p.out_len, p.kv.err)))
+      store2(p.out, at + 64 * q, p.dtype, acc[2 * q] * inv, acc[2 * q + 1] * inv);
+}
+
+template <int D, int P, int MT, bool HALF>
+static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
+  constexpr int groups = at_warps(D, MT, HALF) / at_split(D);
+  const size_t fixed = (size_t)(p.kv.n_seq + 1) * (sizeof(long long) + sizeof(int)) + 256;
+  const size_t per_step = groups * (at_stage_bytes(D) + sizeof(uint64_t));
+  int ring = (int)(((size_t)device_smem_optin() - 1024 - fixed) / per_step);
+  if (ring > AT_MAX_RING) ring = AT_MAX_RING;
+  if (ring < 2) return cudaErrorInvalidConfiguration;
+  p.ring = ring;
+  const size_t smem = fixed + ring * per_step;
+  static std::atomic<unsigned long long> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(configured.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(kv_attend_kernel<D, P, MT, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             device_smem_optin() - 1024);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(1ull << dev);
+  }
+  const int sms = device_sm_count(), grid = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  make_config(cfg, attr, dim3(grid), dim3(at_warps(D, MT, HALF) * 32), smem, stream, true);
+  // (exactly as many where a token is an item by itself; else at most)
+  constexpr int R = at_rows(MT, HALF);
+  const long long each = (p.G + R - 1) / R;
+  p.max_items = (int)(p.kv.H * (p.sel || !p.kv.starts
+                                    ? each * p.kv.n_tok
+                                    : ((long long)p.kv.n_tok * p.G + R - 1) / R + p.kv.n_seq));
+  e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<D, P, MT, HALF>, p);
+  if (e != cudaSuccess) return e;
+  const bool few = (long long)p.max_items * R <= (D == 256 ? 2ll : 4ll) * sms;  // the blocks of 16 warps fit at once
+  const int jw = few ? 16 : 1;
+  make_config(cfg, attr, dim3(p.max_items, R / join_rows(jw)), dim3(join_rows(jw) * jw * 32), 0, stream, true);
+  return few ? cudaLaunchKernelEx(&cfg, kv_join_kernel<D, R, 16>, p)
+             : cudaLaunchKernelEx(&cfg, kv_join_kernel<D, R, 1>, p);
+}
+
+template <int D, int MT, bool HALF>
+static cudaError_t launch_attend_p(AttendParams& p, cudaStream_t stream) {
+  switch (p.kv.P) {
+    case 16: return launch_attend<D, 16, MT, HALF>(p, stream);
+    case 32: return launch_attend<D, 32, MT, HALF>(p, stream);
+    default: return launch_attend<D, 64, MT, HALF>(p, stream);
+  }
+}
+// Rows that share a kv head, on average (with page lists a token's own).
+static long long attend_rows(const AttendParams& p) {
+  return p.sel ? p.G : ((long long)p.kv.n_tok * p.G + p.kv.n_seq - 1) / p.kv.n_seq;
+}
+
+template <int D, bool HALF>
+static cudaError_t launch_attend_d(AttendParams& p, cudaStream_t stream) {
+  if constexpr (D == 64 && !HALF)  // (else a second set of fragments and sums would not fit the registers)
+    if (attend_rows(p) > at_rows(1, HALF)) return launch_attend_p<D, 2, HALF>(p, stream);
+  return launch_attend_p<D, 1, HALF>(p, stream);
+}
+
+template <bool HALF>
+static cudaError_t launch_attend_as(AttendParams& p, int D, cudaStream_t stream) {
+  switch (D) {
+    case 64: return launch_attend_d<64, HALF>(p, stream);
+    case 128: return launch_attend_d<128, HALF>(p, stream);
+    case 192: return launch_attend_d<192, HALF>(p, stream);
+    default: return launch_attend_d<256, HALF>(p, stream);
+  }
+}
+
+}  // namespace qmv

@@ -319,3 +319,39 @@ def test_shares_of_many_tiles(lib, D, P, H, n_seq, length):
             arg = (x.abs().amax(1) * k[:, h].abs().sum(1).max() / D ** 0.5)[:, None]
             assert ((first[s, 4 * h:4 * h + 4] - want).abs() <= (2.0 ** -17 * arg + 2.0 ** -16) * mag).all()
     assert api.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("G,news", [(3, [7, 1, 20]), (8, [2, 5, 1]), (16, [1, 1, 3]), (33, [1, 2, 1])])
+def test_rows_per_kv_head(lib, dtype, D, G, news):
+    # row counts around the kernels' 8, 16 and 32 rows of an item
+    rng = np.random.default_rng(D + G)
+    lens = [90, 31, 260]
+    st = np.concatenate([[0], np.cumsum(news)])
+    pair, table = filled(rng, 2, D, 32, lens)
+    q = randn(rng, st[-1], 2 * G, D, dtype=dtype, scale=1.5)
+    for kw in ({}, {"window": 40}, {"causal": False}):
+        out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), dev32(st), **kw)
+        check(pair, q, table, lens, st, out, **kw)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_outlier_pages_in_every_type(lib, dtype):
+    # values of one page a thousand or a million times larger than its
+    # neighbours', which still count in full in the sum of the weights
+    rng = np.random.default_rng(52)
+    H, D, P = 2, 64, 16
+    for big in (1e3, 1e6):
+        pair = Pair(H, D, P, 20)
+        table = tables(rng, [250], P, 20)
+        k, v = randn(rng, 250, H, D), randn(rng, 250, H, D) * 0.01
+        v[32:48] *= big
+        pair.append(k, v, table, [250], [0, 250])
+        q = randn(rng, 1, 6, D, dtype=dtype)
+        if dtype == torch.float16 and big > 1e3:
+            q *= 0  # (the values' mean still fits f16)
+        check(pair, q, table, [250], None, api.kv_attend(pair.dev, q, dev32(table), dev32([250])))
+        # the big page under a mask: the others must be as exact as without it
+        sel = np.array([[[p for p in range(16) if p != 2]] * H], np.int32)
+        check(pair, q, table, [250], None, api.kv_attend(pair.dev, q, dev32(table), dev32([250]), pages=dev32(sel)), pages=sel)
