@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cmath>
@@ -93,6 +94,17 @@ void* typed(const at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, con
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
   return at::empty(shape, like.options().dtype(type));
+}
+
+// A tensor of its own type over part of buf's memory (which it keeps): results
+// that belong together share one allocation, which costs the host more than
+// all else of a small call.
+at::Tensor piece(const at::Tensor& buf, int64_t byte, at::IntArrayRef shape, at::ScalarType type) {
+  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(),
+                                                   c10::scalarTypeToTypeMeta(type));
+  impl->set_storage_offset(byte / (int64_t)c10::elementSize(type));
+  impl->set_sizes_contiguous(shape);
+  return at::Tensor(std::move(impl));
 }
 
 // A given result, checked, or a new one on like's device.
@@ -238,9 +250,12 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       s = result(PyTuple_GET_ITEM(a[6], 2), at::kInt, {rows_n, K / 32}, x, "q8");
     } else if (want & 2) {
       if (K % 256) check(QMV_ERR_SHAPE, "qmv_rms_norm");
-      q = fresh(x.sizes(), at::kChar, x);
-      d = fresh({rows_n, K / 32}, at::kFloat, x);
-      s = fresh({rows_n, K / 32}, at::kInt, x);
+      // (K % 256 == 0 keeps the parts 16-byte aligned)
+      const int64_t codes = rows_n * K, scales = codes / 8;
+      const at::Tensor buf = fresh({codes + 2 * scales}, at::kByte, x);
+      q = piece(buf, 0, x.sizes(), at::kChar);
+      d = piece(buf, codes, {rows_n, K / 32}, at::kFloat);
+      s = piece(buf, codes + scales, {rows_n, K / 32}, at::kInt);
     }
     if (a[7] != Py_None || rp) res = result(a[7], x.scalar_type(), x.sizes(), x, "res");
     const cudaStream_t st = stream_of(a[8]);
@@ -312,7 +327,17 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dt = dtype_code(t);
     const int64_t shape[3] = {n_tok, c->n_kv_heads, c->head_dim};
     const qmv_kv_batch b = batch_of(a[1], a[2], a[3], n_tok);
-    at::Tensor k = result(a[6], t, shape, table, "k"), v = result(a[7], t, shape, table, "v");
+    at::Tensor k, v;
+    if (a[6] == Py_None && a[7] == Py_None) {
+      on_device(table);
+      const int64_t bytes = n_tok * c->n_kv_heads * c->head_dim * (int64_t)c10::elementSize(t);
+      const at::Tensor buf = fresh({2 * bytes}, at::kByte, table);
+      k = piece(buf, 0, shape, t);
+      v = piece(buf, bytes, shape, t);
+    } else {
+      k = result(a[6], t, shape, table, "k");
+      v = result(a[7], t, shape, table, "v");
+    }
     const cudaStream_t st = stream_of(a[8]);
     check(called([&] { return abi.kv_read(c, &b, dt, k.data_ptr(), v.data_ptr(), st); }), "qmv_kv_read");
     return Py_BuildValue("(NN)", wrap(k), wrap(v));

@@ -45,7 +45,8 @@ cudaError_t launch_kv_attend(const KvParams& kv, int D, const AttendArgs& a, cud
   p.joins = reinterpret_cast<AttendJoin*>(reinterpret_cast<uint8_t*>(p.n_items) + 256);
   QMV_DEBUG_ONLY(p.q_len = (long long)(kv.n_tok - 1) * a.q_stride + (long long)a.n_heads * D;
                  p.out_len = output_extent((long long)kv.n_tok * a.n_heads * D);
-                 p.sel_len = a.sel ? (long long)kv.n_tok * kv.H * a.n_sel : 0;)
+                 p.sel_len = a.sel ? (long long)kv.n_tok * kv.H * a.n_sel : 0;
+                 p.slots_len = (long long)(slots_bytes(D) / sizeof(float));)
   return a.dtype != QMV_DT_F32 && attend_rows(p) > 8 ? launch_attend_half(p, D, stream) : launch_attend_split(p, D, stream);
 }
 

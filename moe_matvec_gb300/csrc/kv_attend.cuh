@@ -93,7 +93,7 @@ struct AttendParams {
   AttendJoin* joins;  // [item]
   int max_items;
 #ifdef QMV_DEBUG
-  long long q_len, out_len, sel_len;
+  long long q_len, out_len, sel_len, slots_len;
 #endif
 };
 
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
       float dk = 0.f, dv = 0.f;
       float s[MT][NR][NJ][2];
       landed(st, phase);
-      if (!dead) {
+      if (!dead && QMV_CHECK(smem_in_range(stages + st * STAGE, STAGE, p.kv.err))) {
         const uint8_t* stage = stages + st * STAGE;
         if (pidx >= 0) {
           const float2 sc = *reinterpret_cast<const float2*>(stage + sub * K_STRIDE);
@@ -678,6 +678,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
       return HALF ? make_float2(x[2 * nr] * f, x[2 * nr + 1] * f) : make_float2((x[0] + x[2]) * f, (x[1] + x[3]) * f);
     };
     auto write_slot = [&](float* slot, int mt, int nr) {
+      if (!QMV_CHECK(in_range(slot - p.slots, at_slot_floats(D, R), p.slots_len, p.kv.err))) return;
       const int row = (mt * NR + nr) * 8 + r;
       if (c == 0) {
         // (the maximum of a row that is no number ignores that)
@@ -807,6 +808,7 @@ __global__ void __launch_bounds__(join_rows(JW) * JW * 32, JW == 1 ? 1 : 2) kv_j
     for (int i = 0; i < AHEAD; i++) {
       const int k = min(k0 + i * JW, parts - 1);
       const float* s = p.slots + ((size_t)(j.first + k) * SP * 2 + (k == 0 ? 1 : 0)) * SLOT;
+      if (!QMV_CHECK(in_range(s - p.slots, SLOT, p.slots_len, p.kv.err))) return;
       st[i] = *reinterpret_cast<const float2*>(s + 2 * row);
 #pragma unroll
       for (int q = 0; q < D / 64; q++) {

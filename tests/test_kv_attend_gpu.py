@@ -355,3 +355,54 @@ def test_outlier_pages_in_every_type(lib, dtype):
         # the big page under a mask: the others must be as exact as without it
         sel = np.array([[[p for p in range(16) if p != 2]] * H], np.int32)
         check(pair, q, table, [250], None, api.kv_attend(pair.dev, q, dev32(table), dev32([250]), pages=dev32(sel)), pages=sel)
+
+
+def by_device(cache):
+    """A restatement cache holding what the device's holds."""
+    ref = kv_ref.Cache(cache.n_kv_heads, cache.head_dim, cache.page_tokens, cache.n_pages)
+    ref.pages[:] = cache.page_tensor.cpu().numpy()
+    ref.bounds[:] = cache.bounds_tensor.cpu().numpy()
+    return ref
+
+
+@pytest.mark.parametrize("pages_held", [2500, 12000])
+def test_picks_among_thousands_of_pages(lib, pages_held):
+    # more pages than a block brings in at once, and than it keeps keys of
+    rng = np.random.default_rng(60)
+    H, D, P, n = 1, 64, 16, pages_held * 16 - 5
+    cache = api.kv_cache(H, D, P, pages_held + 1, bounds=True)
+    table = tables(rng, [n], P, pages_held + 1)
+    for a in range(0, n, 60000):
+        b = min(n, a + 60000)
+        api.kv_append(cache, randn(rng, b - a, H, D), randn(rng, b - a, H, D), dev32(table), dev32([b]), dev32([0, b - a]))
+    ref = by_device(cache)
+    q = randn(rng, 1, 3, D)
+    for n_sel in (2, 64, 2049, pages_held - 3):
+        ids = api.kv_select(cache, q, dev32(table), dev32([n]), n_sel).cpu().numpy()
+        assert np.array_equal(ids, kv_ref.select(ref, q.cpu().numpy(), table, [n], [0, 1], n_sel))
+    assert api.get_device_error() == 0
+
+
+def test_picks_for_many_query_heads(lib):
+    rng = np.random.default_rng(61)
+    pair, table = filled(rng, 1, 256, 16, [400])
+    q = randn(rng, 1, 200, 256)
+    ids = api.kv_select(pair.dev, q, dev32(table), dev32([400]), 7).cpu().numpy()
+    assert np.array_equal(ids, kv_ref.select(pair.ref, q.cpu().numpy(), table, [400], [0, 1], 7))
+    out = api.kv_attend(pair.dev, q, dev32(table), dev32([400]), pages=dev32(ids))
+    check(pair, q, table, [400], None, out, pages=ids)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, torch.float32), (128, torch.bfloat16), (256, torch.float32)])
+def test_as_many_sequences_as_a_call_takes(lib, D, dtype):
+    rng = np.random.default_rng(62)
+    lens = [int(v) for v in rng.integers(0, 12, 1024)]
+    pair, table = filled(rng, 1, D, 16, lens)
+    q = randn(rng, 1024, 3, D, dtype=dtype)
+    check(pair, q, table, lens, None, api.kv_attend(pair.dev, q, dev32(table), dev32(lens)))
+    ids = api.kv_select(pair.dev, q, dev32(table), dev32(lens), 1).cpu().numpy()
+    assert np.array_equal(ids[:, 0, 0], [0 if n else -1 for n in lens])
+    starts = np.concatenate([[0], np.cumsum([min(n, 2) for n in lens])])
+    q = randn(rng, starts[-1], 12, D, dtype=dtype)
+    out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), dev32(starts))
+    check(pair, q, table, lens, starts, out)
