@@ -48,7 +48,11 @@
 namespace qmv {
 
 constexpr int AT_TILE = 64;  // tokens of a unit
-constexpr int AT_MAX_RING = 8;
+// Stages of a worker: K of one tile while V of the one before is read and the
+// other way round.  More bytes in flight cost HBM bandwidth (a bare copy loop:
+// 7.2 TB/s with 80 KB in flight per SM, 6.7 with 210); with three stages a
+// worker 32 x 8192 tokens of head_dim 128 took 71 us, with two 68.
+constexpr int AT_RING = 2;
 constexpr int AT_MAX_CTAS = 160;
 // Softmax weights enter f16 times 2^6 and may exceed 1 by 2^8 (a running
 // maximum is only followed when it is left behind by more than that) and, by
@@ -87,7 +91,7 @@ struct AttendParams {
   float scale_log2;  // scale * log2(e)
   int dtype, G, n_heads, causal, window;
   const int32_t* sel;
-  int n_sel, ring;
+  int n_sel;
   float* slots;       // [worker][SP warps][2]
   int* n_items;       // items of the batch
   AttendJoin* joins;  // [item]
@@ -272,7 +276,8 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
   constexpr int K_STRIDE = KV_HEADER + P * D, V_STRIDE = at_v_stride(D, P), STAGE = at_stage_bytes(D);
   static_assert(ppt * K_STRIDE <= STAGE && (ppt - 1) * V_STRIDE + P * D <= STAGE, "a stage holds either half");
   extern __shared__ __align__(128) uint8_t smem[];
-  const int S = p.ring, n_seq = p.kv.n_seq;
+  constexpr int S = AT_RING;
+  const int n_seq = p.kv.n_seq;
   // stages [group][S] | barriers [group][S] | first units | first items
   uint8_t* cur = smem + (size_t)NG * S * STAGE;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(cur);
@@ -870,12 +875,7 @@ template <int D, int P, int MT, bool HALF>
 static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
   constexpr int groups = at_warps(D, MT, HALF) / at_split(D);
   const size_t fixed = (size_t)(p.kv.n_seq + 1) * (sizeof(long long) + sizeof(int)) + 256;
-  const size_t per_step = groups * (at_stage_bytes(D) + sizeof(uint64_t));
-  int ring = (int)(((size_t)device_smem_optin() - 1024 - fixed) / per_step);
-  if (ring > AT_MAX_RING) ring = AT_MAX_RING;
-  if (ring < 2) return cudaErrorInvalidConfiguration;
-  p.ring = ring;
-  const size_t smem = fixed + ring * per_step;
+  const size_t smem = fixed + groups * AT_RING * (at_stage_bytes(D) + sizeof(uint64_t));
   static std::atomic<unsigned long long> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
