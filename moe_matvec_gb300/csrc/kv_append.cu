@@ -134,10 +134,11 @@ __global__ void __launch_bounds__(AppendShape<DT, D, ONE>::THREADS, ONE ? 1 : 76
   using Raw = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;  // four values
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int VROW = ONE ? 4 : 64 + 16;  // bytes of a dimension's slots in shared memory
   __shared__ float red[Shape::THREADS / 32];
   __shared__ float lo_s[TG][D], hi_s[TG][D];
-  __shared__ __align__(16) uint8_t vt[ONE ? 16 : D * VROW];
+  // the values' codes, 16 words of four slots per dimension: word q of dimension
+  // dd at q ^ (dd / 4 % 16), so that the lanes' stores fall into different banks
+  __shared__ __align__(16) uint32_t vt[ONE ? 4 : D * 16];
   const KvItem it = kv_item(p, (int)(blockIdx.x / (unsigned)p.H));
   if (it.s < 0) return;
   const int head = (int)(blockIdx.x % (unsigned)p.H), P = p.P;  // a token's heads side by side
@@ -152,15 +153,19 @@ __global__ void __launch_bounds__(AppendShape<DT, D, ONE>::THREADS, ONE ? 1 : 76
   const T* x = static_cast<const T*>(part ? vx : kx) + (long long)head * D + 4 * col;
   // slots of the thread's group q: first_slot(q) .. + SLOTS - 1
   auto first_slot = [&](int q) { return ONE ? lo : 4 * (tg + q * TG); };
+  const bool mine = tg < TG && (!ONE || tg == 0);  // the thread has slots
+  auto is_new = [&](int t) { return t >= lo && t < hi; };
+  // a slot that is not new takes the nearest new one's values: the extremes stay
+  // those of the new tokens
   Raw raw[NQ][SLOTS];
+  const T* const x0 = x + tok0 * stride;
 #pragma unroll
   for (int q = 0; q < NQ; q++) {
 #pragma unroll
     for (int i = 0; i < SLOTS; i++) {
-      const int t = first_slot(q) + i;
+      const int t = min(max(first_slot(q) + i, lo), hi - 1);
       raw[q][i] = Raw{};
-      if (tg < TG && (!ONE || tg == 0) && t >= lo && t < hi && QMV_CHECK(in_range(tok0 + t, 1, p.n_tok, p.err)))
-        raw[q][i] = *reinterpret_cast<const Raw*>(x + (tok0 + t) * stride);
+      if (mine && QMV_CHECK(in_range(tok0 + t, 1, p.n_tok, p.err))) raw[q][i] = *reinterpret_cast<const Raw*>(x0 + t * stride);
     }
   }
   const int phys = kv_page(p, it.s, it.page);
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(AppendShape<DT, D, ONE>::THREADS, ONE ? 1 : 76
       for (int j = 0; j < 4; j++) amax = fmaxf(amax, fabsf(v[j]));
     }
   }
-  if (p.bounds && part == 0 && tg < TG) {
+  if (p.bounds && part == 0 && tg < TG) {  // (ONE: a thread of another group has none)
     float mn[4], mx[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) mn[j] = INFINITY, mx[j] = -INFINITY;
@@ -196,10 +201,9 @@ __global__ void __launch_bounds__(AppendShape<DT, D, ONE>::THREADS, ONE ? 1 : 76
     for (int q = 0; q < NQ; q++) {
 #pragma unroll
       for (int i = 0; i < SLOTS; i++) {
-        const int t = first_slot(q) + i;
         float v[4];
         values(raw[q][i], v);
-        if (t >= lo && t < hi && (!ONE || tg == 0)) {
+        if (mine) {
 #pragma unroll
           for (int j = 0; j < 4; j++) {
             mn[j] = fminf(mn[j], v[j]);
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(AppendShape<DT, D, ONE>::THREADS, ONE ? 1 : 76
         uint32_t o[4];
         transpose4(packed[q], o);
 #pragma unroll
-        for (int j = 0; j < 4; j++) *reinterpret_cast<uint32_t*>(vt + (4 * col + j) * VROW + t) = o[j];
+        for (int j = 0; j < 4; j++) vt[(4 * col + j) * 16 + ((t >> 2) ^ (col & 15))] = o[j];
       }
     }
   }
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(AppendShape<DT, D, ONE>::THREADS, ONE ? 1 : 76
 #pragma unroll
       for (int i = 0; i < SLOTS; i++) {
         const int t = first_slot(q) + i;
-        if (tg < TG && (!ONE || tg == 0) && t >= lo && t < hi)
+        if (mine && is_new(t))
           *reinterpret_cast<uint32_t*>(codes + ((size_t)(4 * col / 64) * P + t) * 64 + 4 * col % 64) = packed[q][i];
       }
     }
@@ -320,13 +324,22 @@ __global__ void __launch_bounds__(AppendShape<DT, D, ONE>::THREADS, ONE ? 1 : 76
   } else {
     // 16 slots of a dimension a thread; single bytes where some are not new
     const int c0 = lo / 16, nc = (hi - 1) / 16 - c0 + 1;
-    for (int i = u; i < D * nc; i += HALF) {
-      const int dd = i / nc, c = c0 + i % nc;
+    for (int i = u; i < D * 4; i += HALF) {
+      const int dd = i / 4, c = i % 4, k = dd / 4 % 16;
+      if (c < c0 || c >= c0 + nc) continue;
+      uint4 w = *reinterpret_cast<const uint4*>(vt + dd * 16 + 4 * (c ^ (k >> 2)));
+      if (k & 1) w = make_uint4(w.y, w.x, w.w, w.z);
+      if (k & 2) w = make_uint4(w.z, w.w, w.x, w.y);
       const int a = max(lo, 16 * c), z = min(hi, 16 * c + 16);
-      if (z - a == 16)
-        *reinterpret_cast<uint4*>(codes + dd * P + 16 * c) = *reinterpret_cast<const uint4*>(vt + dd * VROW + 16 * c);
-      else
-        for (int t = a; t < z; t++) codes[dd * P + t] = vt[dd * VROW + t];
+      uint8_t* const dst = codes + dd * P + 16 * c;
+      if (z - a == 16) {
+        *reinterpret_cast<uint4*>(dst) = w;
+      } else {
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 16; j++)
+          if (16 * c + j >= a && 16 * c + j < z) dst[j] = (uint8_t)(ws[j >> 2] >> (8 * (j & 3)));
+      }
     }
   }
 }
