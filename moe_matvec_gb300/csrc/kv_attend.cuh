@@ -13,7 +13,7 @@
 // waited for its slowest warp, 2.8 us a tile; 32 x 8192 tokens 77 us.)
 //
 // A worker feeds itself: the halves of its tiles, K (with the scales) and V, go
-// through a ring of stages of its own by bulk copies (one per page and half).
+// through two stages of its own by bulk copies (one per page and half).
 // Once a half is read, the copies of the one that comes into its stage next are
 // started, so that K and V of the next tile are on their way while this one is
 // computed and no thread waits for a stage to become free.  What the tiles are
@@ -67,11 +67,25 @@ __host__ __device__ constexpr int at_warps(int D, int MT, bool HALF) { return D 
 // Warps that share a tile: from head_dim 192 on two, whose stages would not
 // fit shared memory else.
 __host__ __device__ constexpr int at_split(int D) { return D > 128 ? 2 : 1; }
-// Shared-memory bytes from one page's V to the next: a lane's piece of page c /
-// (P / 16) must fall into another bank group than its neighbours'.
-__host__ __device__ constexpr int at_v_stride(int D, int P) { return P * D + (P == 16 ? 32 : P == 32 ? 64 : 0); }
-// A stage holds either half of a tile.
-__host__ __device__ constexpr int at_stage_bytes(int D) { return AT_TILE * D + 128; }
+// A stage holds half a tile, K with the scales or V.  For head_dim 64 and pages
+// under a tile it holds a whole one: a bulk copy takes an SM about 46 ns however
+// small, and two for every page would take longer than the 8 KB of a tile from
+// HBM (8 draft tokens on 4000 of head_dim 64 in pages of 16: 22 us, now 20
+// with one copy a page; 32 sequences of 8192: 86 us, now 70).
+__host__ __device__ constexpr bool at_whole(int D, int P) { return D == 64 && P < AT_TILE; }
+// Shared-memory bytes from one page to the next, of K (or the whole record) and
+// of V: a lane's V piece of page c / (P / 16) must fall into another bank group
+// than its neighbours'.
+__host__ __device__ constexpr int at_k_stride(int D, int P) {
+  return at_whole(D, P) ? kv_page_bytes(D, P) + (P == 16 ? 16 : 48) : KV_HEADER + P * D;
+}
+__host__ __device__ constexpr int at_v_stride(int D, int P) {
+  return at_whole(D, P) ? at_k_stride(D, P) : P * D + (P == 16 ? 32 : P == 32 ? 64 : 0);
+}
+__host__ __device__ constexpr int at_stage_bytes(int D, int P) {
+  return at_whole(D, P) ? AT_TILE / P * at_k_stride(D, P) : AT_TILE * D + 128;
+}
+
 // A part in the workspace: m and l of each row, then the rows.  Slot 0 of a
 // warp: the item that its share begins inside of (and what it hands to its
 // partner); slot 1: the one that it ends inside of.
@@ -273,8 +287,10 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
   // for each of them
   constexpr int IL = MT == 1 ? 4 : 2;
   constexpr int R = at_rows(MT, HALF), NR = HALF ? 2 : 1, KS = D / 16, NV = D / 8, ppt = AT_TILE / P;
-  constexpr int K_STRIDE = KV_HEADER + P * D, V_STRIDE = at_v_stride(D, P), STAGE = at_stage_bytes(D);
-  static_assert(ppt * K_STRIDE <= STAGE && (ppt - 1) * V_STRIDE + P * D <= STAGE, "a stage holds either half");
+  constexpr bool WHOLE = at_whole(D, P);
+  constexpr int K_STRIDE = at_k_stride(D, P), V_STRIDE = at_v_stride(D, P), STAGE = at_stage_bytes(D, P);
+  constexpr int K_BYTES = KV_HEADER + P * D, V_BYTES = P * D;
+  static_assert(ppt * K_STRIDE <= STAGE && (ppt - 1) * V_STRIDE + V_BYTES <= STAGE, "a stage holds either half");
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int S = AT_RING;
   const int n_seq = p.kv.n_seq;
@@ -393,11 +409,11 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
       idx[i] = page[i] < 0 ? -1 : pg;
     }
   };
-  // Starts the copies of half h (unit h / 2 of the share: K, then V) into stage
-  // st, which nothing reads any more; by whole warps, lane 0 of the first posts
-  // the bytes and copies.  `now`: the unit that is worked on.
+  // Starts the copies of half h (unit h / 2 of the share: K, then V; WHOLE: of
+  // unit h) into stage st, which nothing reads any more; by whole warps, lane 0
+  // of the first posts the bytes and copies.  `now`: the unit that is worked on.
   auto fill = [&](int h, int st, int now) {
-    const int t = h >> 1;
+    const int t = WHOLE ? h : h >> 1;
     if (t >= units || dead) return;
     if (t - planned >= 32) plan(now);
     const int src = t - planned;
@@ -406,8 +422,8 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
     for (int i = 0; i < ppt; i++) pg[i] = __shfl_sync(0xffffffffu, page[i], src);
     const int hd = __shfl_sync(0xffffffffu, head, src);
     if (part != 0 || lane != 0 || *const_cast<volatile int*>(&stop)) return;
-    const bool v = h & 1;
-    const uint32_t bytes = v ? P * D : K_STRIDE;
+    const bool v = !WHOLE && (h & 1);
+    const uint32_t bytes = WHOLE ? K_BYTES + V_BYTES : v ? V_BYTES : K_BYTES;
     uint32_t sum = 0;
 #pragma unroll
     for (int i = 0; i < ppt; i++) sum += pg[i] < 0 ? 0u : bytes;
@@ -415,7 +431,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
 #pragma unroll
     for (int i = 0; i < ppt; i++) {
       if (pg[i] < 0) continue;
-      const long long at = ((long long)pg[i] * p.kv.H + hd) * kv_page_bytes(D, P) + (v ? K_STRIDE : 0);
+      const long long at = ((long long)pg[i] * p.kv.H + hd) * kv_page_bytes(D, P) + (v ? K_BYTES : 0);
       uint8_t* dst = stages + st * STAGE + i * (v ? V_STRIDE : K_STRIDE);
       if (QMV_CHECK(in_range(at, bytes, p.kv.pages_len, p.kv.err)) && QMV_CHECK(smem_in_range(dst, bytes, p.kv.err)))
         bulk_copy_g2s_hint(dst, p.kv.pages + at, bytes, &full[st], policy);
@@ -566,8 +582,10 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
           }
         }
       }
-      release(2 * tile, st, tile);
-      next_stage();
+      if constexpr (!WHOLE) {
+        release(2 * tile, st, tile);
+        next_stage();
+      }
       uint32_t pa[MT][NJ / 2][4], pb[HALF ? MT : 1][NJ / 2][4];
       if (!dead) {
         // tiles at an end of some row's range: products out of it become -inf
@@ -644,10 +662,10 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
           }
         }
       }
-      landed(st, phase);
+      if constexpr (!WHOLE) landed(st, phase);
       if (!dead) {
         // O += P V: k-step kk holds the lane's tokens 4 kk .. + 3
-        const uint8_t* vrow = stages + st * STAGE + sub * V_STRIDE + r * P + (16 * c) % P + 2 * NJ * part;
+        const uint8_t* vrow = stages + st * STAGE + (WHOLE ? K_BYTES : 0) + sub * V_STRIDE + r * P + (16 * c) % P + 2 * NJ * part;
 #pragma unroll
         for (int ng = 0; ng < NV; ng += IL) {
           uint32_t w[IL][NJ / 2];
@@ -668,7 +686,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
           }
         }
       }
-      release(2 * tile + 1, st, tile);
+      release(WHOLE ? tile : 2 * tile + 1, st, tile);
       next_stage();
     }
 
@@ -875,7 +893,7 @@ template <int D, int P, int MT, bool HALF>
 static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
   constexpr int groups = at_warps(D, MT, HALF) / at_split(D);
   const size_t fixed = (size_t)(p.kv.n_seq + 1) * (sizeof(long long) + sizeof(int)) + 256;
-  const size_t smem = fixed + groups * AT_RING * (at_stage_bytes(D) + sizeof(uint64_t));
+  const size_t smem = fixed + groups * AT_RING * (at_stage_bytes(D, P) + sizeof(uint64_t));
   static std::atomic<unsigned long long> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
