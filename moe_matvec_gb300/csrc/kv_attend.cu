@@ -16,7 +16,7 @@ static size_t slots_bytes(int D) {
   for (int i = 0; i < (D == 64 ? 4 : 2); i++) {
     const int mt = 1 + i / 2;
     const bool half = i % 2;
-    const size_t b = (size_t)AT_MAX_CTAS * at_warps(D, mt, half) * 2 * at_slot_floats(D, at_rows(mt, half)) * sizeof(float);
+    const size_t b = (size_t)AT_MAX_CTAS * at_warps(D, mt, half) / at_split(D) * 2 * at_slot_floats(D, at_rows(mt, half)) * sizeof(float);
     if (b > most) most = b;
   }
   return most;

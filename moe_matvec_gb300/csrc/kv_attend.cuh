@@ -64,9 +64,20 @@ constexpr float AT_LAZY = 8.f;
 // Warps of a CTA: the quarters of an SM hold whole warps, 8 of up to 255
 // registers a thread or 12 of up to 168, and q and the accumulators take them.
 __host__ __device__ constexpr int at_warps(int D, int MT, bool HALF) { return D * MT <= 64 && !HALF ? 12 : 8; }
-// Warps that share a tile: from head_dim 192 on two, whose stages would not
-// fit shared memory else.
+// Warps that share a tile: from head_dim 192 on two, each for half the
+// dimensions of K and of V (q and the accumulators of all would not fit a
+// thread's registers; two warps with half the tokens each spilled, 16 x 8192
+// tokens of head_dim 256: 47 us, now 39).  They add their products of q and
+// K through shared memory and do the softmax each.
 __host__ __device__ constexpr int at_split(int D) { return D > 128 ? 2 : 1; }
+__host__ __device__ constexpr int at_exchange_bytes(int NR) { return NR * AT_TILE * 8 * (int)sizeof(float); }
+// First dimension of k-step k of a warp (less the lane's 16 c): 64 dimensions a
+// four steps, of which two warps share the middle ones of 192.
+template <int D>
+__device__ __forceinline__ int at_kdim(int part, int k) {
+  if (D == 192 && k >= 4) return 64 + 8 * part + 4 * (k - 4);
+  return 64 * ((D > 128 ? 2 * part : 0) + (k >> 2)) + 4 * (k & 3);
+}
 // A stage holds half a tile, K with the scales or V.  For head_dim 64 and pages
 // under a tile it holds a whole one: a bulk copy takes an SM about 46 ns however
 // small, and two for every page would take longer than the 8 KB of a tile from
@@ -86,10 +97,9 @@ __host__ __device__ constexpr int at_stage_bytes(int D, int P) {
   return at_whole(D, P) ? AT_TILE / P * at_k_stride(D, P) : AT_TILE * D + 128;
 }
 
-// A part in the workspace: m and l of each row, then the rows.  Slot 0 of a
-// warp: the item that its share begins inside of (and what it hands to its
-// partner); slot 1: the one that it ends inside of.
-// (R rows)
+// A part in the workspace: m and l of each of the R rows, then the rows.  Slot 0
+// of a worker: the item that its share begins inside of; slot 1: the one that it
+// ends inside of.
 __host__ __device__ constexpr int at_slot_floats(int D, int R) { return R * (D + 2); }
 // What the join needs of an item: the workers first .. last that hold its
 // parts (last < first: there is nothing to join), and its rows.
@@ -106,7 +116,7 @@ struct AttendParams {
   int dtype, G, n_heads, causal, window;
   const int32_t* sel;
   int n_sel;
-  float* slots;       // [worker][SP warps][2]
+  float* slots;       // [worker][2]
   int* n_items;       // items of the batch
   AttendJoin* joins;  // [item]
   int max_items;
@@ -282,11 +292,12 @@ __host__ __device__ constexpr int at_rows(int MT, bool HALF) { return (HALF ? 16
 
 template <int D, int P, int MT, bool HALF>
 __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kernel(const AttendParams p) {
-  constexpr int W = at_warps(D, MT, HALF), SP = at_split(D), NG = W / SP, NJ = 8 / SP;
+  constexpr int W = at_warps(D, MT, HALF), SP = at_split(D), NG = W / SP, NJ = 8;
   // independent products in flight: a chain of MMAs into one accumulator waits
   // for each of them
   constexpr int IL = MT == 1 ? 4 : 2;
-  constexpr int R = at_rows(MT, HALF), NR = HALF ? 2 : 1, KS = D / 16, NV = D / 8, ppt = AT_TILE / P;
+  constexpr int R = at_rows(MT, HALF), NR = HALF ? 2 : 1, ppt = AT_TILE / P;
+  constexpr int DW = D / SP, KS = DW / 16, NV = DW / 8;  // dimensions of a warp, of K and of V
   constexpr bool WHOLE = at_whole(D, P);
   constexpr int K_STRIDE = at_k_stride(D, P), V_STRIDE = at_v_stride(D, P), STAGE = at_stage_bytes(D, P);
   constexpr int K_BYTES = KV_HEADER + P * D, V_BYTES = P * D;
@@ -294,8 +305,9 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int S = AT_RING;
   const int n_seq = p.kv.n_seq;
-  // stages [group][S] | barriers [group][S] | first units | first items
-  uint8_t* cur = smem + (size_t)NG * S * STAGE;
+  // stages [group][S] | products [group][SP] (SP > 1) | barriers [group][S] | first units | first items
+  constexpr int XCH = SP > 1 ? at_exchange_bytes(NR) : 0;
+  uint8_t* cur = smem + (size_t)NG * S * STAGE + NG * SP * XCH;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(cur);
   cur += NG * S * sizeof(uint64_t);
   long long* const base = reinterpret_cast<long long*>(cur);
@@ -484,11 +496,21 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
         float v[KS][4], amax = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; k++) {
-          const int d0 = 64 * (k >> 2) + 16 * c + 4 * (k & 3);
+          const int d0 = at_kdim<D>(part, k) + 16 * c;
           v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.f;
           if (live && QMV_CHECK(in_range(at + d0, 4, p.q_len, p.kv.err))) load4(p.q, at + d0, p.dtype, v[k]);
 #pragma unroll
           for (int e = 0; e < 4; e++) amax = fmaxf(amax, fabsf(v[k][e]));
+        }
+        if constexpr (SP > 1) {  // one scale for the row: the partner's dimensions count too
+#pragma unroll
+          for (int k = 0; k < KS; k++) {
+            const int d0 = at_kdim<D>(1 - part, k) + 16 * c;
+            float x[4] = {};
+            if (live && QMV_CHECK(in_range(at + d0, 4, p.q_len, p.kv.err))) load4(p.q, at + d0, p.dtype, x);
+#pragma unroll
+            for (int e = 0; e < 4; e++) amax = fmaxf(amax, fabsf(x[e]));
+          }
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -524,8 +546,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
     }
 
     for (const int end = tile + seg; tile < end; tile++) {
-      // the lane's 16 tokens are a piece of one page (of them the warp's: 2 NJ
-      // from 16 c + 2 NJ part on)
+      // the lane's 16 tokens are a piece of one page
       const int sub = 16 * c / P;
       int pidx = -1;
 #pragma unroll
@@ -533,7 +554,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
         const int v = __shfl_sync(0xffffffffu, idx[i], tile - planned);
         if (sub == i) pidx = v;
       }
-      const int pos0 = pidx < 0 ? INT_MAX - 64 : pidx * P + (16 * c) % P + 2 * NJ * part;
+      const int pos0 = pidx < 0 ? INT_MAX - 64 : pidx * P + (16 * c) % P;
       float dk = 0.f, dv = 0.f;
       float s[MT][NR][NJ][2];
       landed(st, phase);
@@ -546,17 +567,29 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
         }
         // S = q K^T, group j: tokens 2 j, 2 j + 1 of the lane's, row r
         const int ksub = 16 * (r >> 1) / P, kt = (16 * (r >> 1)) % P + (r & 1);
-        const uint8_t* krow = stage + ksub * K_STRIDE + KV_HEADER + kt * 64 + 16 * c + 128 * NJ * part;
+        const uint8_t* krow = stage + ksub * K_STRIDE + KV_HEADER + kt * 64 + 16 * c;
 #pragma unroll
         for (int jg = 0; jg < NJ; jg += IL) {
           float acc[MT][IL][4];
 #pragma unroll
-          for (int h = 0; h < D / 64; h++) {
+          for (int h = 0; h < (KS + 3) / 4; h++) {
+            constexpr int LAST = KS % 4 ? KS % 4 : 4;  // k-steps of the last 64 dimensions
+            const int at = at_kdim<D>(part, 4 * h), here = at / 64 * P * 64 + at % 64;
             uint32_t w[IL][4];
 #pragma unroll
-            for (int i = 0; i < IL; i++) load_words<4>(krow + h * P * 64 + (jg + i) * 128, w[i]);
+            for (int i = 0; i < IL; i++) {
+              const uint8_t* from = krow + here + (jg + i) * 128;
+              if (h == (KS + 3) / 4 - 1) {
+                uint32_t x[LAST];
+                load_words<LAST>(from, x);
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
+                for (int k = 0; k < LAST; k++) w[i][k] = x[k];
+              } else {
+                load_words<4>(from, w[i]);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4 && 4 * h + k < KS; k++) {
 #pragma unroll
               for (int i = 0; i < IL; i++) {
                 uint32_t b0, b1;
@@ -582,9 +615,29 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
           }
         }
       }
+      float4* const xch = reinterpret_cast<float4*>(smem + (size_t)NG * S * STAGE + (group * SP + part) * XCH) + lane;
+      if constexpr (SP > 1) {
+#pragma unroll
+        for (int nr = 0; nr < NR; nr++) {
+#pragma unroll
+          for (int j = 0; j < NJ; j += 2)
+            xch[(nr * NJ + j) * 16] = make_float4(s[0][nr][j][0], s[0][nr][j][1], s[0][nr][j + 1][0], s[0][nr][j + 1][1]);
+        }
+      }
       if constexpr (!WHOLE) {
         release(2 * tile, st, tile);
         next_stage();
+      }
+      if constexpr (SP > 1) {  // (both warps add the same two: their softmax is the same bit for bit)
+        const float4* const other = xch + (part ? -1 : 1) * (XCH / 16);
+#pragma unroll
+        for (int nr = 0; nr < NR; nr++) {
+#pragma unroll
+          for (int j = 0; j < NJ; j += 2) {
+            const float4 x = other[(nr * NJ + j) * 16];
+            s[0][nr][j][0] += x.x, s[0][nr][j][1] += x.y, s[0][nr][j + 1][0] += x.z, s[0][nr][j + 1][1] += x.w;
+          }
+        }
       }
       uint32_t pa[MT][NJ / 2][4], pb[HALF ? MT : 1][NJ / 2][4];
       if (!dead) {
@@ -665,7 +718,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
       if constexpr (!WHOLE) landed(st, phase);
       if (!dead) {
         // O += P V: k-step kk holds the lane's tokens 4 kk .. + 3
-        const uint8_t* vrow = stages + st * STAGE + (WHOLE ? K_BYTES : 0) + sub * V_STRIDE + r * P + (16 * c) % P + 2 * NJ * part;
+        const uint8_t* vrow = stages + st * STAGE + (WHOLE ? K_BYTES : 0) + sub * V_STRIDE + (DW * part + r) * P + (16 * c) % P;
 #pragma unroll
         for (int ng = 0; ng < NV; ng += IL) {
           uint32_t w[IL][NJ / 2];
@@ -694,7 +747,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
     const bool begins = it.k == 0, ends = it.k + seg == it.tiles, whole = begins && ends;
     // (with page lists a token may lie in no sequence: its row is not written)
     const bool covered = it.tbase >= it.seq.t0 && it.tbase < it.seq.t0 + it.seq.n;
-    float back = vref * (1.f / AT_P_SCALE);
+    const float back = vref * (1.f / AT_P_SCALE);
     // column pair n2 of the lane's row: o in fp32, without the reference scale
     auto pair = [&](int mt, int nr, int n2, float f) {
       const float(&x)[4] = o[mt][n2];
@@ -703,12 +756,12 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
     auto write_slot = [&](float* slot, int mt, int nr) {
       if (!QMV_CHECK(in_range(slot - p.slots, at_slot_floats(D, R), p.slots_len, p.kv.err))) return;
       const int row = (mt * NR + nr) * 8 + r;
-      if (c == 0) {
+      if (c == 0 && part == 0) {
         // (the maximum of a row that is no number ignores that)
         slot[2 * row] = l[mt][nr] != l[mt][nr] ? NAN : m[mt][nr];
         slot[2 * row + 1] = l[mt][nr];
       }
-      float* dst = slot + 2 * R + row * D + 2 * c;
+      float* dst = slot + 2 * R + row * D + DW * part + 2 * c;
 #pragma unroll
       for (int n2 = 0; n2 < NV; n2++) *reinterpret_cast<float2*>(dst + 8 * n2) = pair(mt, nr, n2, back);
     };
@@ -720,61 +773,22 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
         l[mt][nr] += __shfl_xor_sync(0xffffffffu, l[mt][nr], 2);
       }
     }
-    float* const slots = p.slots + (size_t)(worker * SP) * 2 * at_slot_floats(D, R);
-    if constexpr (SP > 1) {
-      // the partner's half of the tokens comes over its slot 0
-      float* const other = slots + 2 * at_slot_floats(D, R);
-      if (part == 1) {
+    float* const slots = p.slots + (size_t)worker * 2 * at_slot_floats(D, R);
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++) {
+    for (int mt = 0; mt < MT; mt++) {
 #pragma unroll
-          for (int nr = 0; nr < NR; nr++) write_slot(other, mt, nr);
-        }
-      }
-      named_sync(2 + group, SP * 32);
-      if (part == 0) {
+      for (int nr = 0; nr < NR; nr++) {
+        const int rr = it.row0 + (mt * NR + nr) * 8 + r;
+        if (!whole) {
+          write_slot(slots + (begins ? at_slot_floats(D, R) : 0), mt, nr);
+        } else if (covered && rr < it.nrows) {
+          // (a row that is no number stays one)
+          const float f = l[mt][nr] > 0.f ? back / l[mt][nr] : l[mt][nr] != l[mt][nr] ? NAN : 0.f;
+          const long long at = ((long long)(it.tbase + rr / p.G) * p.n_heads + it.head * p.G + rr % p.G) * D + DW * part + 2 * c;
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++) {
-#pragma unroll
-          for (int nr = 0; nr < NR; nr++) {
-            const int row = (mt * NR + nr) * 8 + r;
-            const float2 st2 = __ldcg(reinterpret_cast<const float2*>(other + 2 * row));
-            const float M = fmaxf(m[mt][nr], st2.x);
-            const float f0 = m[mt][nr] == -INFINITY ? 0.f : ex2(m[mt][nr] - M) * back;
-            const float f1 = st2.x == -INFINITY ? 0.f : ex2(st2.x - M);
-            const float* src = other + 2 * R + row * D + 2 * c;
-#pragma unroll
-            for (int n2 = 0; n2 < NV; n2++) {
-              const float2 x = __ldcg(reinterpret_cast<const float2*>(src + 8 * n2));
-              const float2 y = pair(mt, nr, n2, f0);
-              o[mt][n2][2 * nr] = fmaf(x.x, f1, y.x);
-              o[mt][n2][2 * nr + 1] = fmaf(x.y, f1, y.y);
-              if constexpr (!HALF) o[mt][n2][2] = o[mt][n2][3] = 0.f;
-            }
-            l[mt][nr] = (m[mt][nr] == -INFINITY ? l[mt][nr] : l[mt][nr] * ex2(m[mt][nr] - M)) + st2.y * (st2.x == -INFINITY ? 1.f : f1);
-            m[mt][nr] = M;
-          }
-        }
-        back = 1.f;
-      }
-    }
-    if (part == 0) {
-#pragma unroll
-      for (int mt = 0; mt < MT; mt++) {
-#pragma unroll
-        for (int nr = 0; nr < NR; nr++) {
-          const int rr = it.row0 + (mt * NR + nr) * 8 + r;
-          if (!whole) {
-            write_slot(slots + (begins ? at_slot_floats(D, R) : 0), mt, nr);
-          } else if (covered && rr < it.nrows) {
-            // (a row that is no number stays one)
-            const float f = l[mt][nr] > 0.f ? back / l[mt][nr] : l[mt][nr] != l[mt][nr] ? NAN : 0.f;
-            const long long at = ((long long)(it.tbase + rr / p.G) * p.n_heads + it.head * p.G + rr % p.G) * D + 2 * c;
-#pragma unroll
-            for (int n2 = 0; n2 < NV; n2++) {
-              const float2 x = pair(mt, nr, n2, f);
-              if (QMV_CHECK(in_range(at + 8 * n2, 2, p.out_len, p.kv.err))) store2(p.out, at + 8 * n2, p.dtype, x.x, x.y);
-            }
+          for (int n2 = 0; n2 < NV; n2++) {
+            const float2 x = pair(mt, nr, n2, f);
+            if (QMV_CHECK(in_range(at + 8 * n2, 2, p.out_len, p.kv.err))) store2(p.out, at + 8 * n2, p.dtype, x.x, x.y);
           }
         }
       }
@@ -813,7 +827,7 @@ template <int D, int R, int JW>
 __global__ void __launch_bounds__(join_rows(JW) * JW * 32, JW == 1 ? 1 : 2) kv_join_kernel(const AttendParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int SLOT = at_slot_floats(D, R), SP = at_split(D), ROWS = join_rows(JW), AHEAD = JW == 1 ? 8 : 4;
+  constexpr int SLOT = at_slot_floats(D, R), ROWS = join_rows(JW), AHEAD = JW == 1 ? 8 : 4;
   __shared__ float sm[ROWS][JW][2];
   __shared__ float sx[ROWS][JW][JW > 1 ? D : 1];
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % JW, rb = threadIdx.x / (32 * JW);
@@ -830,7 +844,7 @@ __global__ void __launch_bounds__(join_rows(JW) * JW * 32, JW == 1 ? 1 : 2) kv_j
 #pragma unroll
     for (int i = 0; i < AHEAD; i++) {
       const int k = min(k0 + i * JW, parts - 1);
-      const float* s = p.slots + ((size_t)(j.first + k) * SP * 2 + (k == 0 ? 1 : 0)) * SLOT;
+      const float* s = p.slots + ((size_t)(j.first + k) * 2 + (k == 0 ? 1 : 0)) * SLOT;
       if (!QMV_CHECK(in_range(s - p.slots, SLOT, p.slots_len, p.kv.err))) return;
       st[i] = *reinterpret_cast<const float2*>(s + 2 * row);
 #pragma unroll
@@ -893,7 +907,8 @@ template <int D, int P, int MT, bool HALF>
 static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
   constexpr int groups = at_warps(D, MT, HALF) / at_split(D);
   const size_t fixed = (size_t)(p.kv.n_seq + 1) * (sizeof(long long) + sizeof(int)) + 256;
-  const size_t smem = fixed + groups * AT_RING * (at_stage_bytes(D, P) + sizeof(uint64_t));
+  const size_t exchange = at_split(D) > 1 ? at_split(D) * at_exchange_bytes(HALF ? 2 : 1) : 0;
+  const size_t smem = fixed + groups * (exchange + AT_RING * (at_stage_bytes(D, P) + sizeof(uint64_t)));
   static std::atomic<unsigned long long> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
