@@ -139,6 +139,12 @@ __device__ __forceinline__ void seq_tiles(const AttendParams& p, const KvSeq& q,
   tiles = max((q.len + AT_TILE - 1) / AT_TILE - tile0, 1);
 }
 
+// a / b for a >= 0, b > 0: in 32 bits where they do (a 64-bit division is some
+// 150 cycles, and a share's first copy waits for four of them).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // Unit u of the batch (ids: the sequences' first items; base: prefix sums of the sequences' units or, when each
 // token has its own pages, their first tokens).
 template <int R>
@@ -148,15 +154,15 @@ __device__ __forceinline__ AttendItem locate(const AttendParams& p, const long l
   long long key = u;
   if (p.sel) {
     const int tiles = (p.n_sel * p.kv.P + AT_TILE - 1) / AT_TILE, n_rt = (p.G + R - 1) / R;
-    const long long item = u / tiles;
-    it.k = (int)(u - item * tiles);
-    it.id = (int)item;
+    const int item = (int)divide(u, tiles);
+    it.k = (int)(u - (long long)item * tiles);
+    it.id = item;
     it.tiles = tiles;
     it.tile0 = 0;
-    it.row0 = (int)(item % n_rt) * R;
-    const long long th = item / n_rt;
-    it.head = (int)(th % H);
-    it.tbase = (int)(th / H);
+    const int th = item / n_rt;
+    it.row0 = (item - th * n_rt) * R;
+    it.tbase = th / H;
+    it.head = th - it.tbase * H;
     it.nrows = p.G;
     key = it.tbase;
   }
@@ -171,11 +177,12 @@ __device__ __forceinline__ AttendItem locate(const AttendParams& p, const long l
     seq_tiles(p, it.seq, it.tile0, it.tiles);
     it.nrows = it.seq.n * p.G;
     const int n_rt = (it.nrows + R - 1) / R;
-    const long long local = u - base[lo], item = local / it.tiles;
-    it.k = (int)(local - item * it.tiles);
-    it.id = ids[lo] + (int)item;
-    it.row0 = (int)(item % n_rt) * R;
-    it.head = (int)(item / n_rt);
+    const long long local = u - base[lo];
+    const int item = (int)divide(local, it.tiles);
+    it.k = (int)(local - (long long)item * it.tiles);
+    it.id = ids[lo] + item;
+    it.head = item / n_rt;
+    it.row0 = (item - it.head * n_rt) * R;
     it.tbase = it.seq.t0;
   }
   return it;
@@ -373,7 +380,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
   // The workers: SP warps that work on one tile at a time; neighbours in number
   // sit on different SMs, so that a small batch spreads.
   const int group = warp / SP, part = warp % SP;
-  const long long share = (total + (long long)NG * gridDim.x - 1) / ((long long)NG * gridDim.x);
+  const long long share = divide(total + NG * gridDim.x - 1, NG * gridDim.x);
   const int worker = group * gridDim.x + blockIdx.x;
   const long long u0 = min(worker * share, total), u1 = min(total, u0 + share);
   const int units = (int)(u1 - u0);
@@ -796,7 +803,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
     if (begins && part == 0 && lane == 0) {
       AttendJoin j{};
       j.first = worker;
-      j.last = whole || !covered ? worker - 1 : (int)((u + it.tiles - 1) / share);
+      j.last = whole || !covered ? worker - 1 : (int)divide(u + it.tiles - 1, share);
       j.tbase = it.tbase;
       j.row0 = it.row0;
       j.nrows = it.nrows;
