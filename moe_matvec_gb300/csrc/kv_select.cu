@@ -130,6 +130,13 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) kv_select_kernel(const SelectP
     return;
   }
 
+  // Up to SEL_CACHED keys go straight into the first CTA's shared memory (once it
+  // is known to run), more of them by the workspace.
+  const bool cached = last <= SEL_CACHED;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  uint32_t first_keys;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(first_keys) : "r"(smem_u32(keys)));
+
   // ---- scores of pages [pg0, pg1)
   const int per = (last + ranks - 1) / ranks, pg0 = min(rank * per, last), pg1 = min(pg0 + per, last);
   const int sub = lane / LP, li = lane % LP;
@@ -163,6 +170,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) kv_select_kernel(const SelectP
     }
     if (lane == 0) dq[g] = d;
   }
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   __syncthreads();
   for (int from = pg0; from < pg1; from += SEL_TABLE) {
     if (from > pg0) {
@@ -218,7 +226,12 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) kv_select_kernel(const SelectP
       if (li == 0) {
 #pragma unroll
         for (int i = 0; i < SEL_UNROLL; i++)
-          if (pb + i * STEP < upto) sc[pb + i * STEP] = __fmul_rn(best[i], dk[i]);
+          if (pb + i * STEP < upto) {
+            const float score = __fmul_rn(best[i], dk[i]);
+            if (cached && QMV_CHECK(in_range(pb + i * STEP, 1, SEL_CACHED, p.kv.err)))
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(first_keys + 4 * (pb + i * STEP)), "r"(score_key(score)) : "memory");
+            if (!cached) sc[pb + i * STEP] = score;
+          }
       }
     }
   }
@@ -229,14 +242,12 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) kv_select_kernel(const SelectP
 
   // ---- picks
   uint32_t kmin = 0xffffffffu, kmax = 0;
-  const bool cached = last <= SEL_CACHED;
+  auto key = [&](int i) { return cached ? keys[i] : score_key(__ldcg(sc + i)); };
   for (int i = tid; i < last; i += SEL_THREADS) {
-    const uint32_t k = score_key(__ldcg(sc + i));
-    if (cached) keys[i] = k;
+    const uint32_t k = key(i);
     kmin = min(kmin, k);
     kmax = max(kmax, k);
   }
-  auto key = [&](int i) { return cached ? keys[i] : score_key(__ldcg(sc + i)); };
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   if (lane == 0) {
@@ -303,7 +314,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) kv_select_kernel(const SelectP
     n_gt += k > floor || (whole && k == floor);
     n_eq += !whole && k == floor;
   }
-  int rank_eq = block_scan(n_eq, total, buf);
+  int rank_eq = whole ? 0 : block_scan(n_eq, total, buf);
   const int take = n_gt + min(max(left - rank_eq, 0), n_eq);
   int at = block_scan(take, total, buf);
   for (int i = b0; i < b1; i++) {

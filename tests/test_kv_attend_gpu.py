@@ -240,6 +240,17 @@ def test_ties_go_to_the_lower_page(lib):
             assert np.array_equal(ids, kv_ref.select(pair.ref, q.cpu().numpy(), table, [n], [0, 1], n_sel))
 
 
+def test_more_pages_than_shared_memory_holds_scores_of(lib):
+    rng = np.random.default_rng(49)
+    H, D, P, n = 1, 64, 16, 8400 * 16 - 5
+    pair, table = filled(rng, H, D, P, [n])
+    for heads in (1, 5):
+        q = randn(rng, 1, heads, D)
+        for n_sel in (2, 300, 8400):
+            ids = api.kv_select(pair.dev, q, dev32(table), dev32([n]), n_sel).cpu().numpy()
+            assert np.array_equal(ids, kv_ref.select(pair.ref, q.cpu().numpy(), table, [n], [0, 1], n_sel))
+
+
 def test_picks_of_several_tokens(lib):
     rng = np.random.default_rng(42)
     H, D, P = 2, 128, 16
