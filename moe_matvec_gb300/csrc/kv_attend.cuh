@@ -19,6 +19,12 @@
 // computed and no thread waits for a stage to become free.  What the tiles are
 // made of is worked out 32 tiles at a time, a lane each.
 //
+// Measured: 32 sequences of up to 8192 tokens, 40 query and 8 kv heads of 128
+// (395 MB): 68 us, 5.8 TB/s, 86% of a copy's bandwidth; one sequence of 131072
+// (269 MB): 50 us; one of 1000: 10 us, of which the copies and products of its
+// one tile a worker are 3 and the rest is launches, dependent loads and the
+// join.
+//
 // The arithmetic (mma.sync m16n8k16, f16 operands, fp32 sums) has codes, exact
 // in f16, in B.  With fp32 queries the rows of A are 8 query rows in two f16
 // parts, q = hi + lo, rows 0-7 hi and 8-15 lo, and so are the softmax weights:

@@ -78,7 +78,10 @@ __device__ __forceinline__ int block_scan(int v, int& total, int (&buf)[SEL_WARP
 }
 
 // One cluster per (token, kv head): its CTAs score a share of the pages each,
-// and the first then picks.
+// and the first, in whose shared memory the scores' keys meet, then picks.
+// 16 sequences of up to 65536 tokens, 8 heads of 128, pages of 64 (26 MB of
+// bounds): 14 us, of them 6-8 the scores of the longest sequence and 5 its picks;
+// 2 sequences of 16384: 6 us, steps that wait for one another throughout.
 //
 // Scores: the group's query heads are quantized into shared memory, split by
 // sign: with q = q+ + q-,

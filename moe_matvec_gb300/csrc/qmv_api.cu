@@ -761,7 +761,7 @@ const char* qmv_strerror(int code) {
     case QMV_OK: return "success";
     case QMV_ERR_FORMAT: return "unknown weight format";
     case QMV_ERR_SHAPE: return "invalid shape (M, K, ffn, hidden or split count)";
-    case QMV_ERR_NTOK: return "n_tok outside [1, 64] or top_k outside [1, 8]";
+    case QMV_ERR_NTOK: return "n_tok, n_seq or top_k outside the call's limits";
     case QMV_ERR_NULL: return "a required pointer is NULL";
     case QMV_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case QMV_ERR_WORKSPACE: return "workspace too small";

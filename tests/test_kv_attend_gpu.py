@@ -243,7 +243,11 @@ def test_ties_go_to_the_lower_page(lib):
 def test_more_pages_than_shared_memory_holds_scores_of(lib):
     rng = np.random.default_rng(49)
     H, D, P, n = 1, 64, 16, 8400 * 16 - 5
-    pair, table = filled(rng, H, D, P, [n])
+    pair = Pair(H, D, P, 8403)
+    table = tables(rng, [n], P, 8403)
+    for at in range(0, n, 16000):
+        m = min(16000, n - at)
+        pair.append(randn(rng, m, H, D), randn(rng, m, H, D), table, [at + m], [0, m])
     for heads in (1, 5):
         q = randn(rng, 1, heads, D)
         for n_sel in (2, 300, 8400):
