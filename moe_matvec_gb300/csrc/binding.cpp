@@ -242,22 +242,31 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* wp = typed(w, at::kFloat, {K}, "w");
     void* rp = a[3] == Py_None ? nullptr : typed(tensor(a[3], "r"), x.scalar_type(), x.sizes(), "r");
     at::Tensor y, q, d, s, res;
-    if (a[5] != Py_None || (want & 1)) y = result(a[5], x.scalar_type(), x.sizes(), x, "y");
+    // New results of up to a megabyte are one allocation (y | codes, scales, sums
+    // | res); larger ones two or three, so that none keeps another's memory.
+    const bool new_y = a[5] == Py_None && (want & 1), new_q = a[6] == Py_None && (want & 2), new_res = a[7] == Py_None && rp;
+    if (new_q && K % 256) check(QMV_ERR_SHAPE, "qmv_rms_norm");
+    // (K % 256 == 0 keeps the parts 16-byte aligned)
+    const int64_t codes = rows_n * K, scales = codes / 8, floats = (codes * (int64_t)c10::elementSize(x.scalar_type()) + 255) / 256 * 256;
+    const int64_t at_q = new_y ? floats : 0, at_res = at_q + (new_q ? codes + 2 * scales : 0), all = at_res + (new_res ? floats : 0);
+    const bool one = new_y + new_q + new_res > 1 && all <= 1 << 20;
+    const at::Tensor shared = one ? fresh({all}, at::kByte, x) : at::Tensor();
+    if (one && new_y) y = piece(shared, 0, x.sizes(), x.scalar_type());
+    else if (a[5] != Py_None || new_y) y = result(a[5], x.scalar_type(), x.sizes(), x, "y");
     if (a[6] != Py_None) {
       if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 3) value_error("q8: a tuple (q, d, s) wanted");
       q = result(PyTuple_GET_ITEM(a[6], 0), at::kChar, x.sizes(), x, "q8");
       d = result(PyTuple_GET_ITEM(a[6], 1), at::kFloat, {rows_n, K / 32}, x, "q8");
       s = result(PyTuple_GET_ITEM(a[6], 2), at::kInt, {rows_n, K / 32}, x, "q8");
-    } else if (want & 2) {
-      if (K % 256) check(QMV_ERR_SHAPE, "qmv_rms_norm");
-      // (K % 256 == 0 keeps the parts 16-byte aligned)
-      const int64_t codes = rows_n * K, scales = codes / 8;
-      const at::Tensor buf = fresh({codes + 2 * scales}, at::kByte, x);
-      q = piece(buf, 0, x.sizes(), at::kChar);
-      d = piece(buf, codes, {rows_n, K / 32}, at::kFloat);
-      s = piece(buf, codes + scales, {rows_n, K / 32}, at::kInt);
+    } else if (new_q) {
+      const at::Tensor buf = one ? shared : fresh({codes + 2 * scales}, at::kByte, x);
+      const int64_t from = one ? at_q : 0;
+      q = piece(buf, from, x.sizes(), at::kChar);
+      d = piece(buf, from + codes, {rows_n, K / 32}, at::kFloat);
+      s = piece(buf, from + codes + scales, {rows_n, K / 32}, at::kInt);
     }
-    if (a[7] != Py_None || rp) res = result(a[7], x.scalar_type(), x.sizes(), x, "res");
+    if (one && new_res) res = piece(shared, at_res, x.sizes(), x.scalar_type());
+    else if (a[7] != Py_None || new_res) res = result(a[7], x.scalar_type(), x.sizes(), x, "res");
     const cudaStream_t st = stream_of(a[8]);
     const float eps = (float)real(a[2]);
     auto at_or_null = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };

@@ -13,8 +13,8 @@ namespace qmv {
 // Sequence s of the batch owns items starts[s] / P + 2 s .. starts[s+1] / P +
 // 2 (s + 1), at least as many as its new tokens can touch pages ((n - 2) / P +
 // 2 for n of them, in the worst place), so the sequence is found from starts
-// alone: a 32-ary search by each warp, one or two loads deep, where prefix sums
-// of the touched pages would need every sequence and the block's barriers.
+// alone, where prefix sums of the touched pages would need every sequence and
+// the block's barriers.
 struct KvItem {
   int s, page;  // page: index in the sequence
   KvSeq seq;
@@ -27,16 +27,8 @@ __device__ __forceinline__ KvItem kv_item(const KvParams& p, int item) {
     r.page = max(r.seq.len - 1, 0) >> p.log_p;
     return r;
   }
-  const int lane = threadIdx.x & 31;
   auto first_item = [&](int s) { return (p.starts[s] >> p.log_p) + 2 * s; };
-  int lo = 0, n = p.n_seq;  // the sequence is one of [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32, s = lo + (lane + 1) * step;  // candidates after lo
-    const bool at_or_after = (lane + 1) * step < n && first_item(s) <= item;
-    const int k = __popc(__ballot_sync(0xffffffffu, at_or_after));
-    lo += k * step;
-    n = min(n - k * step, step);
-  }
+  const int lo = last_seq_at_most(p.n_seq, item, first_item);
   r.s = lo;
   r.seq = kv_seq(p, lo);
   const int first = max(r.seq.len - r.seq.n, 0) >> p.log_p;

@@ -53,6 +53,23 @@ __device__ __forceinline__ KvSeq kv_seq(const KvParams& p, int s) {
   return q;
 }
 
+// The last sequence whose at(s) is at most x (at does not fall with s, and the
+// first is taken to be at most x): a 32-ary search by each warp of the caller,
+// one or two loads deep, the same answer in all lanes.
+template <class At>
+__device__ __forceinline__ int last_seq_at_most(int n_seq, int x, At at) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = n_seq;  // the sequence is one of [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, s = lo + (lane + 1) * step;  // candidates after lo
+    const bool at_or_after = (lane + 1) * step < n && at(s) <= x;
+    const int k = __popc(__ballot_sync(0xffffffffu, at_or_after));
+    lo += k * step;
+    n = min(n - k * step, step);
+  }
+  return lo;
+}
+
 // The page of the cache that holds page `pg` of sequence s, or -1 if the
 // table's entry is no page (QMV_DEVERR_PAGE).
 __device__ __forceinline__ int kv_page(const KvParams& p, int s, int pg) {

@@ -22,11 +22,7 @@ constexpr int SEL_CACHED = 8192;  // keys kept in shared memory while picking
 // The sequence that holds token t, or -1.
 __device__ __forceinline__ int seq_of_token(const KvParams& p, int t) {
   if (!p.starts) return t;
-  int lo = 0, hi = p.n_seq;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.starts[mid] <= t) lo = mid; else hi = mid;
-  }
+  const int lo = last_seq_at_most(p.n_seq, t, [&](int s) { return p.starts[s]; });
   const KvSeq q = kv_seq(p, lo);
   return t >= q.t0 && t < q.t0 + q.n ? lo : -1;
 }
