@@ -92,8 +92,22 @@ void* typed(const at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, con
   return ptr(t);
 }
 
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-  return at::empty(shape, like.options().dtype(type));
+// The stream of a call: the given one's handle, or torch's current one.
+cudaStream_t stream_of(PyObject* o) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
+  const unsigned long long v = PyLong_AsUnsignedLongLong(o);
+  if (PyErr_Occurred()) throw Raised{};
+  return reinterpret_cast<cudaStream_t>(v);
+}
+
+// A new tensor for work on st.  The allocator takes memory for used on the
+// current stream: it is told where that is another one, so that memory dropped
+// early (a workspace always is) goes to nobody before the work is done.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like, cudaStream_t st) {
+  at::Tensor t = at::empty(shape, like.options().dtype(type));
+  const c10::DeviceIndex dev = t.device().index();
+  if (st != c10::cuda::getCurrentCUDAStream(dev).stream()) t.record_stream(c10::cuda::getStreamFromExternal(st, dev).unwrap());
+  return t;
 }
 
 // A tensor of its own type over part of buf's memory (which it keeps): results
@@ -108,21 +122,14 @@ at::Tensor piece(const at::Tensor& buf, int64_t byte, at::IntArrayRef shape, at:
 }
 
 // A given result, checked, or a new one on like's device.
-at::Tensor result(PyObject* o, at::ScalarType type, at::IntArrayRef shape, const at::Tensor& like, const char* what) {
+at::Tensor result(PyObject* o, at::ScalarType type, at::IntArrayRef shape, const at::Tensor& like, cudaStream_t st, const char* what) {
   if (o == Py_None) {
     on_device(like);
-    return fresh(shape, type, like);
+    return fresh(shape, type, like, st);
   }
   const at::Tensor& t = tensor(o, what);
   typed(t, type, shape, what);
   return t;
-}
-
-cudaStream_t stream_of(PyObject* o) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-  const unsigned long long v = PyLong_AsUnsignedLongLong(o);
-  if (PyErr_Occurred()) throw Raised{};
-  return reinterpret_cast<cudaStream_t>(v);
 }
 
 long long integer(PyObject* o) {
@@ -241,6 +248,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int want = as_int(a[4]);
     void* wp = typed(w, at::kFloat, {K}, "w");
     void* rp = a[3] == Py_None ? nullptr : typed(tensor(a[3], "r"), x.scalar_type(), x.sizes(), "r");
+    const cudaStream_t st = stream_of(a[8]);
     at::Tensor y, q, d, s, res;
     // New results of up to a megabyte are one allocation (y | codes, scales, sums
     // | res); larger ones two or three, so that none keeps another's memory.
@@ -250,24 +258,23 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t codes = rows_n * K, scales = codes / 8, floats = (codes * (int64_t)c10::elementSize(x.scalar_type()) + 255) / 256 * 256;
     const int64_t at_q = new_y ? floats : 0, at_res = at_q + (new_q ? codes + 2 * scales : 0), all = at_res + (new_res ? floats : 0);
     const bool one = new_y + new_q + new_res > 1 && all <= 1 << 20;
-    const at::Tensor shared = one ? fresh({all}, at::kByte, x) : at::Tensor();
+    const at::Tensor shared = one ? fresh({all}, at::kByte, x, st) : at::Tensor();
     if (one && new_y) y = piece(shared, 0, x.sizes(), x.scalar_type());
-    else if (a[5] != Py_None || new_y) y = result(a[5], x.scalar_type(), x.sizes(), x, "y");
+    else if (a[5] != Py_None || new_y) y = result(a[5], x.scalar_type(), x.sizes(), x, st, "y");
     if (a[6] != Py_None) {
       if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 3) value_error("q8: a tuple (q, d, s) wanted");
-      q = result(PyTuple_GET_ITEM(a[6], 0), at::kChar, x.sizes(), x, "q8");
-      d = result(PyTuple_GET_ITEM(a[6], 1), at::kFloat, {rows_n, K / 32}, x, "q8");
-      s = result(PyTuple_GET_ITEM(a[6], 2), at::kInt, {rows_n, K / 32}, x, "q8");
+      q = result(PyTuple_GET_ITEM(a[6], 0), at::kChar, x.sizes(), x, st, "q8");
+      d = result(PyTuple_GET_ITEM(a[6], 1), at::kFloat, {rows_n, K / 32}, x, st, "q8");
+      s = result(PyTuple_GET_ITEM(a[6], 2), at::kInt, {rows_n, K / 32}, x, st, "q8");
     } else if (new_q) {
-      const at::Tensor buf = one ? shared : fresh({codes + 2 * scales}, at::kByte, x);
+      const at::Tensor buf = one ? shared : fresh({codes + 2 * scales}, at::kByte, x, st);
       const int64_t from = one ? at_q : 0;
       q = piece(buf, from, x.sizes(), at::kChar);
       d = piece(buf, from + codes, {rows_n, K / 32}, at::kFloat);
       s = piece(buf, from + codes + scales, {rows_n, K / 32}, at::kInt);
     }
     if (one && new_res) res = piece(shared, at_res, x.sizes(), x.scalar_type());
-    else if (a[7] != Py_None || new_res) res = result(a[7], x.scalar_type(), x.sizes(), x, "res");
-    const cudaStream_t st = stream_of(a[8]);
+    else if (a[7] != Py_None || new_res) res = result(a[7], x.scalar_type(), x.sizes(), x, st, "res");
     const float eps = (float)real(a[2]);
     auto at_or_null = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
     const int64_t ld = rows_n > 1 ? x.stride(0) : K;
@@ -294,8 +301,8 @@ PyObject* dequantize_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t rows_n = q.size(0), K = q.size(1);
     const void* qp = typed(q, at::kChar, q.sizes(), "q");
     const void* dp = typed(d, at::kFloat, {rows_n, K / 32}, "d");
-    at::Tensor out = result(a[3], t, q.sizes(), q, "out");
     const cudaStream_t st = stream_of(a[4]);
+    at::Tensor out = result(a[3], t, q.sizes(), q, st, "out");
     check(called([&] {
             return abi.dequantize_act(dt, static_cast<const int8_t*>(qp), static_cast<const float*>(dp), rows_n, K,
                                       out.data_ptr(), st);
@@ -336,25 +343,25 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dt = dtype_code(t);
     const int64_t shape[3] = {n_tok, c->n_kv_heads, c->head_dim};
     const qmv_kv_batch b = batch_of(a[1], a[2], a[3], n_tok);
+    const cudaStream_t st = stream_of(a[8]);
     at::Tensor k, v;
     if (a[6] == Py_None && a[7] == Py_None) {
       on_device(table);
       const int64_t bytes = n_tok * c->n_kv_heads * c->head_dim * (int64_t)c10::elementSize(t);
-      const at::Tensor buf = fresh({2 * bytes}, at::kByte, table);
+      const at::Tensor buf = fresh({2 * bytes}, at::kByte, table, st);
       k = piece(buf, 0, shape, t);
       v = piece(buf, bytes, shape, t);
     } else {
-      k = result(a[6], t, shape, table, "k");
-      v = result(a[7], t, shape, table, "v");
+      k = result(a[6], t, shape, table, st, "k");
+      v = result(a[7], t, shape, table, st, "v");
     }
-    const cudaStream_t st = stream_of(a[8]);
     check(called([&] { return abi.kv_read(c, &b, dt, k.data_ptr(), v.data_ptr(), st); }), "qmv_kv_read");
     return Py_BuildValue("(NN)", wrap(k), wrap(v));
   });
 }
 
-at::Tensor workspace(PyObject* o, size_t bytes, const at::Tensor& like) {
-  if (o == Py_None) return at::empty({(int64_t)(bytes < 16 ? 16 : bytes)}, like.options().dtype(at::kByte));
+at::Tensor workspace(PyObject* o, size_t bytes, const at::Tensor& like, cudaStream_t st) {
+  if (o == Py_None) return fresh({(int64_t)(bytes < 16 ? 16 : bytes)}, at::kByte, like, st);
   const at::Tensor& t = tensor(o, "ws");
   ptr(t);
   return t;
@@ -385,9 +392,10 @@ PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       pages = ints(t);
       n_sel = (int)t.size(2);
     }
-    at::Tensor out = result(a[10], q.scalar_type(), q.sizes(), q, "out");
-    at::Tensor ws = workspace(a[9], a[9] == Py_None ? abi.kv_attend_workspace_bytes(c, (int)heads, b.n_tok, b.n_seq) : 0, q);
     const cudaStream_t st = stream_of(a[11]);
+    at::Tensor out = result(a[10], q.scalar_type(), q.sizes(), q, st, "out");
+    at::Tensor ws =
+        workspace(a[9], a[9] == Py_None ? abi.kv_attend_workspace_bytes(c, (int)heads, b.n_tok, b.n_seq) : 0, q, st);
     check(called([&] {
             return abi.kv_attend(c, &b, dt, qp, qs, out.data_ptr(), (int)heads, scale, causal, window, pages, n_sel,
                                  ws.data_ptr(), ws.nbytes(), st);
@@ -411,9 +419,9 @@ PyObject* kv_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (q.size(1) > INT32_MAX) value_error("too many heads");
     const qmv_kv_batch b = batch_of(a[2], a[3], a[4], q.size(0));
     const int64_t shape[3] = {q.size(0), c->n_kv_heads, n_sel};
-    at::Tensor ids = result(a[7], at::kInt, shape, q, "ids");
-    at::Tensor ws = workspace(a[6], a[6] == Py_None ? abi.kv_select_workspace_bytes(c, &b) : 0, q);
     const cudaStream_t st = stream_of(a[8]);
+    at::Tensor ids = result(a[7], at::kInt, shape, q, st, "ids");
+    at::Tensor ws = workspace(a[6], a[6] == Py_None ? abi.kv_select_workspace_bytes(c, &b) : 0, q, st);
     check(called([&] {
             return abi.kv_select(c, &b, dt, qp, qs, (int)q.size(1), static_cast<int32_t*>(ids.data_ptr()), n_sel,
                                  ws.data_ptr(), ws.nbytes(), st);

@@ -209,6 +209,27 @@ def test_graph_replays_as_lengths_grow(lib):
         check(pair, q, table, now, None, out)
 
 
+def test_a_stream_that_is_not_the_current_one(lib):
+    # the workspace is dropped when the call returns: nobody may have its memory before the work is done
+    rng = np.random.default_rng(37)
+    pair, table = filled(rng, 2, 128, 64, [900, 1200])
+    q, td, lens = randn(rng, 2, 8, 128), dev32(table), dev32([900, 1200])
+    want = api.kv_attend(pair.dev, q, td, lens)
+    picks = api.kv_select(pair.dev, q, td, lens, 5)
+    size = api.kv_attend_workspace_bytes(pair.dev, 8, 2, 2)
+    small = api.kv_select_workspace_bytes(pair.dev, 2, td.shape[1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # the work below starts some 10 ms later
+    out = api.kv_attend(pair.dev, q, td, lens, stream=side)
+    ids = api.kv_select(pair.dev, q, td, lens, 5, stream=side)
+    other = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in (size, size, small, small)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(ids, picks)
+    assert not any(t.any() for t in other)
+
+
 # ---------------------------------------------------------------- selection
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("D,P,G", [(64, 16, 1), (128, 32, 4), (192, 16, 3), (256, 64, 8)])
