@@ -37,7 +37,7 @@ cudaError_t launch_kv_attend(const KvParams& kv, int D, const AttendArgs& a, cud
   p.n_heads = a.n_heads;
   p.G = a.n_heads / kv.H;
   p.causal = a.causal;
-  p.window = a.window;
+  p.window = a.window < 1 << 27 ? a.window : 1 << 27;  // (beyond any position: no sum below leaves 32 bits)
   p.sel = a.sel;
   p.n_sel = a.n_sel;
   p.slots = static_cast<float*>(a.ws);

@@ -84,6 +84,18 @@ def test_several_tokens_masks_and_windows(lib, causal, window):
         check(pair, q, table, lens, st, out, causal=causal, window=window)
 
 
+def test_the_largest_window(lib):
+    # with more tokens in the call than the sequence holds, and none at all
+    rng = np.random.default_rng(29)
+    lens, news = [1, 0, 90], [4, 3, 2]
+    st = np.concatenate([[0], np.cumsum(news)])
+    pair, table = filled(rng, 1, 64, 16, lens)
+    q = randn(rng, st[-1], 2, 64)
+    out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), dev32(st), window=2 ** 31 - 1)
+    check(pair, q, table, lens, st, out)
+    assert torch.equal(out, api.kv_attend(pair.dev, q, dev32(table), dev32(lens), dev32(st)))
+
+
 def test_a_whole_prompt(lib):
     rng = np.random.default_rng(30)
     lens = [260, 33]
