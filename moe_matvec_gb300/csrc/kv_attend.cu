@@ -6,6 +6,8 @@ namespace qmv {
 
 cudaError_t launch_attend_split(AttendParams& p, int D, cudaStream_t stream);
 cudaError_t launch_attend_half(AttendParams& p, int D, cudaStream_t stream);
+cudaError_t launch_attend_split_cluster(AttendParams& p, int D, cudaStream_t stream);
+cudaError_t launch_attend_half_cluster(AttendParams& p, int D, cudaStream_t stream);
 
 // Items of a batch at most: with page lists every token has its own.
 static long long max_items(int H, int G, int n_tok, int n_seq, int R) {
@@ -24,6 +26,34 @@ static size_t slots_bytes(int D) {
 // slots | number of items | joins
 size_t kv_attend_ws_bytes(int D, int H, int G, int n_tok, int n_seq) {
   return slots_bytes(D) + 256 + (size_t)max_items(H, G, n_tok, n_seq, 8) * sizeof(AttendJoin);
+}
+
+int attend_resident_clusters(int c);
+
+// CTAs of a cluster per item, or 0 for equal shares over the GPU and a second
+// kernel.  A cluster saves that kernel, its launch and the prefix sum of the
+// batch, about as much as CL_TILES tiles of a warp take, but its warps get as many
+// tiles as its own sequence has: with page lists a number the host knows, else at
+// most what the table can hold (against one tile for the shares: how much of the
+// table is in use is not known here).  All clusters have to be resident at once.
+// Measured, shares / clusters: one sequence of 1000 tokens 9.5 / 8.0 us, 32 of 500
+// 10.9 / 7.3, 64 listed pages of 16 sequences (8 tiles a warp, 7 in equal shares)
+// 32 / 28; where warps would get 5 tiles more than by shares (200 listed pages of 4
+// sequences, with append and selection) clusters lose, 31 / 34.
+constexpr int CL_TILES = 1;
+static int clusters_for(const AttendParams& p, int D, bool half) {
+  if (p.kv.starts && !p.sel) return 0;  // the items hang on starts
+  const int mt = attend_mt(p, D, half), R = at_rows(mt, half), workers = at_warps(D, mt, half) / at_split(D);
+  const long long items = (long long)p.kv.n_tok * p.kv.H * ((p.G + R - 1) / R);
+  const long long slots = (long long)(p.sel ? p.n_sel : p.kv.max_pages) * p.kv.P;
+  long long tiles = (slots + AT_TILE - 1) / AT_TILE;
+  if (p.window > 0 && !p.sel && (p.window + 62) / AT_TILE + 2 < tiles) tiles = (p.window + 62) / AT_TILE + 2;
+  int c = 1;
+  while (c < 8 && c * workers < tiles && items <= attend_resident_clusters(2 * c)) c *= 2;
+  if (items > attend_resident_clusters(c)) return 0;
+  const long long here = (tiles + c * workers - 1) / (c * workers);
+  const long long all = p.sel ? (items * tiles + workers * device_sm_count() - 1) / (workers * device_sm_count()) : 1;
+  return here <= all + CL_TILES ? c : 0;
 }
 
 cudaError_t launch_kv_attend(const KvParams& kv, int D, const AttendArgs& a, cudaStream_t stream) {
@@ -47,7 +77,10 @@ cudaError_t launch_kv_attend(const KvParams& kv, int D, const AttendArgs& a, cud
                  p.out_len = output_extent((long long)kv.n_tok * a.n_heads * D);
                  p.sel_len = a.sel ? (long long)kv.n_tok * kv.H * a.n_sel : 0;
                  p.slots_len = (long long)(slots_bytes(D) / sizeof(float));)
-  return a.dtype != QMV_DT_F32 && attend_rows(p) > 8 ? launch_attend_half(p, D, stream) : launch_attend_split(p, D, stream);
+  const bool half = a.dtype != QMV_DT_F32 && attend_rows(p) > 8;
+  p.cluster = clusters_for(p, D, half);
+  if (p.cluster) return half ? launch_attend_half_cluster(p, D, stream) : launch_attend_split_cluster(p, D, stream);
+  return half ? launch_attend_half(p, D, stream) : launch_attend_split(p, D, stream);
 }
 
 }  // namespace qmv

@@ -9,6 +9,8 @@
 // long sequences fill the GPU alike.  Warps never wait for one another: a share
 // that ends inside an item leaves its running maximum, sum and accumulator in
 // the workspace, and a second kernel joins an item's parts in their order.
+// (Batches of few units take a cluster per item and no second kernel instead, see
+// clusters_for in kv_attend.cu.)
 // (Shares per CTA, merged in shared memory, ended unevenly: a segment's end
 // waited for its slowest warp, 2.8 us a tile; 32 x 8192 tokens 77 us.)
 //
@@ -21,9 +23,9 @@
 //
 // Measured: 32 sequences of up to 8192 tokens, 40 query and 8 kv heads of 128
 // (395 MB): 68 us, 5.8 TB/s, 86% of a copy's bandwidth; one sequence of 131072
-// (269 MB): 50 us; one of 1000: 10 us, of which the copies and products of its
-// one tile a worker are 3 and the rest is launches, dependent loads and the
-// join.
+// (269 MB): 50 us; one of 1000 (clusters): 8 us, of which the copies and products
+// of its one tile a worker are 3 and the rest is the launch, dependent loads and
+// the join.
 //
 // The arithmetic (mma.sync m16n8k16, f16 operands, fp32 sums) has codes, exact
 // in f16, in B.  With fp32 queries the rows of A are 8 query rows in two f16
@@ -126,6 +128,7 @@ struct AttendParams {
   int* n_items;       // items of the batch
   AttendJoin* joins;  // [item]
   int max_items;
+  int cluster;  // CL: CTAs of an item
 #ifdef QMV_DEBUG
   long long q_len, out_len, sel_len, slots_len;
 #endif
@@ -300,10 +303,81 @@ __device__ __forceinline__ void store2(void* base, long long at, int dt, float x
     *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(base) + at) = __floats2bfloat162_rn(x, y);
 }
 
+// Item `id` of a batch whose items do not depend on its lengths (page lists, or
+// one token a sequence), from its first unit.  By a whole warp.
+template <int R>
+__device__ __forceinline__ AttendItem item_of(const AttendParams& p, int id) {
+  AttendItem it;
+  const int n_rt = (p.G + R - 1) / R, th = id / n_rt;
+  it.id = id;
+  it.k = 0;
+  it.row0 = (id - th * n_rt) * R;
+  it.tbase = th / p.kv.H;
+  it.head = th - it.tbase * p.kv.H;
+  it.s = p.kv.starts ? last_seq_at_most(p.kv.n_seq, it.tbase, [&](int s) { return p.kv.starts[s]; }) : it.tbase;
+  it.seq = kv_seq(p.kv, it.s);
+  it.nrows = p.sel ? p.G : it.seq.n * p.G;
+  if (p.sel) {
+    it.tile0 = 0;
+    it.tiles = (p.n_sel * p.kv.P + AT_TILE - 1) / AT_TILE;
+  } else {
+    seq_tiles(p, it.seq, it.tile0, it.tiles);
+  }
+  return it;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// p of this CTA, in CTA `rank` of the cluster.
+__device__ __forceinline__ float2 load_peer(const float* p, int rank) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
+// Adds parts of a row: M, L and the lane's columns of acc over the parts given
+// by load(i, stat, x), N at a time.
+template <int E, int N, class Load>
+__device__ __forceinline__ void join_row(int parts, Load load, float& M, float& L, float (&acc)[E]) {
+  M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; e++) acc[e] = 0.f;
+  for (int i0 = 0; i0 < parts; i0 += N) {
+    float2 st[N];
+    float x[N][E];
+#pragma unroll
+    for (int i = 0; i < N; i++) load(min(i0 + i, parts - 1), st[i], x[i]);
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < N; i++) top = fmaxf(top, st[i].x);
+    const float back = M == -INFINITY && L == L ? 0.f : ex2(M - top);
+    M = top;
+    L *= back;
+#pragma unroll
+    for (int e = 0; e < E; e++) acc[e] *= back;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      if (i0 + i >= parts) continue;
+      // (a row that is no number keeps its sum as one)
+      const float f = st[i].x == -INFINITY && st[i].y == st[i].y ? 0.f : ex2(st[i].x - M);
+      L = fmaf(st[i].y, f, L);
+#pragma unroll
+      for (int e = 0; e < E; e++) acc[e] = fmaf(x[i][e], f, acc[e]);
+    }
+  }
+}
+
 // Rows of an item, and of a lane's A fragment (its rows r and, with HALF, r + 8).
 __host__ __device__ constexpr int at_rows(int MT, bool HALF) { return (HALF ? 16 : 8) * MT; }
 
-template <int D, int P, int MT, bool HALF>
+// CL: a cluster per item, for batches of few units (see clusters_for): its
+// workers share the item's tiles, and its rows are joined through shared memory,
+// so that there is no second kernel and no prefix sum of the batch.
+template <int D, int P, int MT, bool HALF, bool CL>
 __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kernel(const AttendParams p) {
   constexpr int W = at_warps(D, MT, HALF), SP = at_split(D), NG = W / SP, NJ = 8;
   // independent products in flight: a chain of MMAs into one accumulator waits
@@ -335,62 +409,76 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
   if (tid == 0) stop = 0;
   fence_mbar_init();
   pdl_wait();
-  // the sequences' first units (first tokens) and items
-  long long total = 0;
-  int items = 0;
-  for (int c = 0; c < n_seq; c += W * 32) {
-    const int s = c + tid;
-    long long units = 0;
-    int first = 0, mine = 0;
-    if (s < n_seq) {
-      const KvSeq q = kv_seq(p.kv, s);
-      int t0, tiles;
-      seq_tiles(p, q, t0, tiles);
-      mine = (q.n * p.G + R - 1) / R * p.kv.H;
-      units = (long long)mine * tiles;
-      first = q.t0;
-    }
-    long long inc = units;
-    int inc_ids = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      const int w = __shfl_up_sync(0xffffffffu, inc_ids, o);
-      if (lane >= o) inc += v, inc_ids += w;
-    }
-    if (lane == 31) wtot[warp] = inc, wids[warp] = inc_ids;
-    __syncthreads();
-    long long before = total;
-    int before_ids = items;
-#pragma unroll
-    for (int i = 0; i < W; i++) {
-      if (i < warp) before += wtot[i], before_ids += wids[i];
-      total += wtot[i], items += wids[i];
-    }
-    if (s < n_seq) {
-      base[s] = p.sel ? first : before + inc - units;
-      ids[s] = before_ids + inc_ids - mine;
-    }
-    __syncthreads();
-  }
-  if (p.sel) {
-    const int tiles = (p.n_sel * P + AT_TILE - 1) / AT_TILE;
-    items = p.kv.n_tok * p.kv.H * ((p.G + R - 1) / R);
-    total = (long long)items * tiles;
-  } else if (tid == 0) {
-    base[n_seq] = total;
-  }
-  __syncthreads();
-  if (blockIdx.x == 0 && tid == 0) *p.n_items = items;
-
-  // The workers: SP warps that work on one tile at a time; neighbours in number
-  // sit on different SMs, so that a small batch spreads.
   const int group = warp / SP, part = warp % SP;
-  const long long share = divide(total + NG * gridDim.x - 1, NG * gridDim.x);
-  const int worker = group * gridDim.x + blockIdx.x;
-  const long long u0 = min(worker * share, total), u1 = min(total, u0 + share);
+  AttendItem it;
+  long long u0 = 0, u1 = 0, share = 1;
+  int worker = 0;
+  const int ranks = CL ? p.cluster : 1, rank = CL ? blockIdx.x % ranks : 0;
+  if constexpr (CL) {
+    it = item_of<R>(p, blockIdx.x / ranks);
+    const int each = (it.tiles + ranks * NG - 1) / (ranks * NG), w = group * ranks + rank;
+    u0 = min(w * each, it.tiles);
+    u1 = min((w + 1) * each, it.tiles);
+    it.k = (int)u0;
+    __syncthreads();  // the barriers are there
+  } else {
+    // the sequences' first units (first tokens) and items
+    long long total = 0;
+    int items = 0;
+    for (int c = 0; c < n_seq; c += W * 32) {
+      const int s = c + tid;
+      long long units = 0;
+      int first = 0, mine = 0;
+      if (s < n_seq) {
+        const KvSeq q = kv_seq(p.kv, s);
+        int t0, tiles;
+        seq_tiles(p, q, t0, tiles);
+        mine = (q.n * p.G + R - 1) / R * p.kv.H;
+        units = (long long)mine * tiles;
+        first = q.t0;
+      }
+      long long inc = units;
+      int inc_ids = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        const int w = __shfl_up_sync(0xffffffffu, inc_ids, o);
+        if (lane >= o) inc += v, inc_ids += w;
+      }
+      if (lane == 31) wtot[warp] = inc, wids[warp] = inc_ids;
+      __syncthreads();
+      long long before = total;
+      int before_ids = items;
+#pragma unroll
+      for (int i = 0; i < W; i++) {
+        if (i < warp) before += wtot[i], before_ids += wids[i];
+        total += wtot[i], items += wids[i];
+      }
+      if (s < n_seq) {
+        base[s] = p.sel ? first : before + inc - units;
+        ids[s] = before_ids + inc_ids - mine;
+      }
+      __syncthreads();
+    }
+    if (p.sel) {
+      const int tiles = (p.n_sel * P + AT_TILE - 1) / AT_TILE;
+      items = p.kv.n_tok * p.kv.H * ((p.G + R - 1) / R);
+      total = (long long)items * tiles;
+    } else if (tid == 0) {
+      base[n_seq] = total;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && tid == 0) *p.n_items = items;
+
+    // The workers: SP warps that work on one tile at a time; neighbours in number
+    // sit on different SMs, so that a small batch spreads.
+    share = divide(total + NG * gridDim.x - 1, NG * gridDim.x);
+    worker = group * gridDim.x + blockIdx.x;
+    u0 = min(worker * share, total);
+    u1 = min(total, u0 + share);
+  }
   const int units = (int)(u1 - u0);
-  if (units == 0) return;
+  if (!CL && units == 0) return;
   const int r = lane >> 2, c = lane & 3;
   uint8_t* const stages = smem + (size_t)group * S * STAGE;
   uint64_t* const full = bars + group * S;
@@ -406,31 +494,33 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
 #pragma unroll
     for (int i = 0; i < ppt; i++) page[i] = idx[i] = -1;
     if (from + lane >= units) return;
-    const AttendItem it = locate<R>(p, base, ids, u0 + from + lane);
-    head = it.head;
-    const int rows = min(it.row0 + R, it.nrows) - 1;
+    AttendItem x = it;
+    if constexpr (CL) x.k = (int)u0 + from + lane;
+    else x = locate<R>(p, base, ids, u0 + from + lane);
+    head = x.head;
+    const int rows = min(x.row0 + R, x.nrows) - 1;
     // positions that some row of the item may see: [vis0, vis1)
-    const int vis1 = p.causal ? row_pos(p, it, rows) + 1 : it.seq.len;
-    const int vis0 = p.window > 0 ? row_pos(p, it, it.row0) - p.window + 1 : 0;
+    const int vis1 = p.causal ? row_pos(p, x, rows) + 1 : x.seq.len;
+    const int vis0 = p.window > 0 ? row_pos(p, x, x.row0) - p.window + 1 : 0;
 #pragma unroll
     for (int i = 0; i < ppt; i++) {
       int pg;
       if (p.sel) {
-        const int j = it.k * ppt + i;
-        const long long at = ((long long)it.tbase * p.kv.H + it.head) * p.n_sel + j;
+        const int j = x.k * ppt + i;
+        const long long at = ((long long)x.tbase * p.kv.H + x.head) * p.n_sel + j;
         pg = j < p.n_sel && QMV_CHECK(in_range(at, 1, p.sel_len, p.kv.err)) ? p.sel[at] : -1;
         if (pg >= p.kv.max_pages) {
           set_error(p.kv.err, QMV_DEVERR_PAGE);
           pg = -1;
         }
         // a token that no sequence covers has no pages
-        if (it.tbase < it.seq.t0 || it.tbase >= it.seq.t0 + it.seq.n) pg = -1;
+        if (x.tbase < x.seq.t0 || x.tbase >= x.seq.t0 + x.seq.n) pg = -1;
       } else {
-        pg = (it.tile0 + it.k) * ppt + i;
+        pg = (x.tile0 + x.k) * ppt + i;
       }
       const long long pos = (long long)pg * P;
-      if (pg < 0 || pos >= vis1 || pos >= it.seq.len || pos + P <= vis0) continue;
-      page[i] = kv_page(p.kv, it.s, pg);
+      if (pg < 0 || pos >= vis1 || pos >= x.seq.len || pos + P <= vis0) continue;
+      page[i] = kv_page(p.kv, x.s, pg);
       idx[i] = page[i] < 0 ? -1 : pg;
     }
   };
@@ -489,8 +579,8 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
   };
 
   long long u = u0;
-  AttendItem it = locate<R>(p, base, ids, u);
-  for (; u < u1; next_item<R>(p, base, it)) {
+  if constexpr (!CL) it = locate<R>(p, base, ids, u);
+  for (;; next_item<R>(p, base, it)) {
     const int seg = (int)min((long long)(it.tiles - it.k), u1 - u);  // units of this item in the share
     // q of the lane's rows as A fragments
     uint32_t qa[MT][KS][4];
@@ -767,7 +857,9 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
       return HALF ? make_float2(x[2 * nr] * f, x[2 * nr + 1] * f) : make_float2((x[0] + x[2]) * f, (x[1] + x[3]) * f);
     };
     auto write_slot = [&](float* slot, int mt, int nr) {
-      if (!QMV_CHECK(in_range(slot - p.slots, at_slot_floats(D, R), p.slots_len, p.kv.err))) return;
+      if (CL ? !QMV_CHECK(smem_in_range(slot, at_slot_floats(D, R) * sizeof(float), p.kv.err))
+             : !QMV_CHECK(in_range(slot - p.slots, at_slot_floats(D, R), p.slots_len, p.kv.err)))
+        return;
       const int row = (mt * NR + nr) * 8 + r;
       if (c == 0 && part == 0) {
         // (the maximum of a row that is no number ignores that)
@@ -785,6 +877,74 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
         l[mt][nr] += __shfl_xor_sync(0xffffffffu, l[mt][nr], 1);
         l[mt][nr] += __shfl_xor_sync(0xffffffffu, l[mt][nr], 2);
       }
+    }
+    if constexpr (CL) {
+      // Parts in the workers' stages (which nothing comes into any more), a CTA's
+      // joined by its warps, a row each at a time, into the first; the cluster's
+      // parts of a row then by one of its CTAs.
+      static_assert(at_slot_floats(D, R) * (int)sizeof(float) <= S * STAGE, "a worker's stages hold its part");
+      float* const slot = reinterpret_cast<float*>(stages);
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++) {
+#pragma unroll
+        for (int nr = 0; nr < NR; nr++) write_slot(slot, mt, nr);
+      }
+      __syncthreads();
+      constexpr int E = D / 32;
+      float* const first = reinterpret_cast<float*>(smem);
+      float M, L, acc[E];
+      auto store = [&](int row) {
+        const int rr = it.row0 + row;
+        if (!covered || rr >= it.nrows) return;
+        const float inv = L > 0.f ? 1.f / L : L != L ? NAN : 0.f;
+        const long long at = ((long long)(it.tbase + rr / p.G) * p.n_heads + it.head * p.G + rr % p.G) * D + 2 * lane;
+#pragma unroll
+        for (int i = 0; i < E / 2; i++)
+          if (QMV_CHECK(in_range(at + 64 * i, 2, p.out_len, p.kv.err)))
+            store2(p.out, at + 64 * i, p.dtype, acc[2 * i] * inv, acc[2 * i + 1] * inv);
+      };
+      for (int row = warp; row < R; row += W) {
+        join_row<E, NG < 8 ? 4 : 8>(
+            NG,
+            [&](int g, float2& st, float (&x)[E]) {
+              const float* from = first + (size_t)g * (S * STAGE / sizeof(float));
+              st = *reinterpret_cast<const float2*>(from + 2 * row);
+#pragma unroll
+              for (int i = 0; i < E / 2; i++) {
+                const float2 v = *reinterpret_cast<const float2*>(from + 2 * R + row * D + 64 * i + 2 * lane);
+                x[2 * i] = v.x, x[2 * i + 1] = v.y;
+              }
+            },
+            M, L, acc);
+        if (ranks == 1) {
+          store(row);
+          continue;
+        }
+        __syncwarp();
+        if (lane == 0) *reinterpret_cast<float2*>(first + 2 * row) = make_float2(M, L);
+#pragma unroll
+        for (int i = 0; i < E / 2; i++)
+          *reinterpret_cast<float2*>(first + 2 * R + row * D + 64 * i + 2 * lane) = make_float2(acc[2 * i], acc[2 * i + 1]);
+      }
+      if (ranks > 1) {
+        cluster_sync();
+        for (int row = rank + warp * ranks; row < R; row += W * ranks) {
+          join_row<E, 4>(
+              ranks,
+              [&](int from, float2& st, float (&x)[E]) {
+                st = load_peer(first + 2 * row, from);
+#pragma unroll
+                for (int i = 0; i < E / 2; i++) {
+                  const float2 v = load_peer(first + 2 * R + row * D + 64 * i + 2 * lane, from);
+                  x[2 * i] = v.x, x[2 * i + 1] = v.y;
+                }
+              },
+              M, L, acc);
+          store(row);
+        }
+        cluster_sync();  // nobody leaves while its parts are read
+      }
+      break;
     }
     float* const slots = p.slots + (size_t)worker * 2 * at_slot_floats(D, R);
 #pragma unroll
@@ -817,6 +977,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
       if (it.id < p.max_items) p.joins[it.id] = j;
     }
     u += seg;
+    if (u >= u1) break;
   }
   // After a wait that ran out, copies that nobody waits for may be in flight:
   // the CTA keeps its shared memory a while longer than any copy takes.
@@ -848,43 +1009,26 @@ __global__ void __launch_bounds__(join_rows(JW) * JW * 32, JW == 1 ? 1 : 2) kv_j
   const AttendJoin j = p.joins[blockIdx.x];
   if ((int)blockIdx.x >= n_items || j.last < j.first) return;
   const int row = blockIdx.y * ROWS + rb, rr = j.row0 + row, parts = j.last - j.first + 1;
-  float M = -INFINITY, L = 0.f, acc[D / 32];
+  constexpr int E = D / 32;
+  float M, L, acc[E];
+  join_row<E, AHEAD>(
+      (parts - w + JW - 1) / JW,
+      [&](int i, float2& st, float (&x)[E]) {
+        const int k = w + i * JW;
+        const float* s = p.slots + ((size_t)(j.first + k) * 2 + (k == 0 ? 1 : 0)) * SLOT;
+        st = make_float2(-INFINITY, 0.f);
 #pragma unroll
-  for (int i = 0; i < D / 32; i++) acc[i] = 0.f;
-  for (int k0 = w; k0 < parts; k0 += JW * AHEAD) {
-    float2 st[AHEAD];
-    float xs[AHEAD][D / 32];
+        for (int e = 0; e < E; e++) x[e] = 0.f;
+        if (!QMV_CHECK(in_range(s - p.slots, SLOT, p.slots_len, p.kv.err))) return;
+        st = *reinterpret_cast<const float2*>(s + 2 * row);
 #pragma unroll
-    for (int i = 0; i < AHEAD; i++) {
-      const int k = min(k0 + i * JW, parts - 1);
-      const float* s = p.slots + ((size_t)(j.first + k) * 2 + (k == 0 ? 1 : 0)) * SLOT;
-      if (!QMV_CHECK(in_range(s - p.slots, SLOT, p.slots_len, p.kv.err))) return;
-      st[i] = *reinterpret_cast<const float2*>(s + 2 * row);
-#pragma unroll
-      for (int q = 0; q < D / 64; q++) {
-        const float2 v = *reinterpret_cast<const float2*>(s + 2 * R + row * D + 64 * q + 2 * lane);
-        xs[i][2 * q] = v.x;
-        xs[i][2 * q + 1] = v.y;
-      }
-    }
-    float top = M;
-#pragma unroll
-    for (int i = 0; i < AHEAD; i++)
-      if (k0 + i * JW < parts) top = fmaxf(top, st[i].x);
-    const float back = M == -INFINITY ? 0.f : ex2(M - top);
-    M = top;
-    L *= back;
-#pragma unroll
-    for (int e = 0; e < D / 32; e++) acc[e] *= back;
-#pragma unroll
-    for (int i = 0; i < AHEAD; i++) {
-      if (k0 + i * JW >= parts) continue;
-      const float f = st[i].x == -INFINITY ? 0.f : ex2(st[i].x - M);
-      L = fmaf(st[i].y, f, L);
-#pragma unroll
-      for (int e = 0; e < D / 32; e++) acc[e] = fmaf(xs[i][e], f, acc[e]);
-    }
-  }
+        for (int q = 0; q < E / 2; q++) {
+          const float2 v = *reinterpret_cast<const float2*>(s + 2 * R + row * D + 64 * q + 2 * lane);
+          x[2 * q] = v.x;
+          x[2 * q + 1] = v.y;
+        }
+      },
+      M, L, acc);
   if constexpr (JW > 1) {
     if (lane == 0) {
       sm[rb][w][0] = M;
@@ -894,18 +1038,14 @@ __global__ void __launch_bounds__(join_rows(JW) * JW * 32, JW == 1 ? 1 : 2) kv_j
     for (int e = 0; e < D / 32; e++) sx[rb][w][64 * (e >> 1) + 2 * lane + (e & 1)] = acc[e];
     __syncthreads();
     if (w != 0) return;
-    M = -INFINITY;
-    for (int i = 0; i < JW; i++) M = fmaxf(M, sm[rb][i][0]);
-    L = 0.f;
+    join_row<E, 4>(
+        JW,
+        [&](int i, float2& st, float (&x)[E]) {
+          st = make_float2(sm[rb][i][0], sm[rb][i][1]);
 #pragma unroll
-    for (int e = 0; e < D / 32; e++) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < JW; i++) {
-      const float m = sm[rb][i][0], l = sm[rb][i][1], f = m == -INFINITY && l == l ? 0.f : ex2(m - M);
-      L = fmaf(l, f, L);
-#pragma unroll
-      for (int e = 0; e < D / 32; e++) acc[e] = fmaf(sx[rb][i][64 * (e >> 1) + 2 * lane + (e & 1)], f, acc[e]);
-    }
+          for (int e = 0; e < E; e++) x[e] = sx[rb][i][64 * (e >> 1) + 2 * lane + (e & 1)];
+        },
+        M, L, acc);
   }
   if (rr >= j.nrows) return;
   const float inv = L > 0.f ? 1.f / L : L != L ? NAN : 0.f;
@@ -916,33 +1056,49 @@ __global__ void __launch_bounds__(join_rows(JW) * JW * 32, JW == 1 ? 1 : 2) kv_j
       store2(p.out, at + 64 * q, p.dtype, acc[2 * q] * inv, acc[2 * q + 1] * inv);
 }
 
+// Shared memory of a CTA.
 template <int D, int P, int MT, bool HALF>
-static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
+static size_t attend_smem(int n_seq) {
   constexpr int groups = at_warps(D, MT, HALF) / at_split(D);
-  const size_t fixed = (size_t)(p.kv.n_seq + 1) * (sizeof(long long) + sizeof(int)) + 256;
   const size_t exchange = at_split(D) > 1 ? at_split(D) * at_exchange_bytes(HALF ? 2 : 1) : 0;
-  const size_t smem = fixed + groups * (exchange + AT_RING * (at_stage_bytes(D, P) + sizeof(uint64_t)));
+  return (size_t)(n_seq + 1) * (sizeof(long long) + sizeof(int)) + 256 +
+         groups * (exchange + AT_RING * (at_stage_bytes(D, P) + sizeof(uint64_t)));
+}
+
+template <int D, int P, int MT, bool HALF, bool CL>
+static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
+  const size_t smem = attend_smem<D, P, MT, HALF>(p.kv.n_seq);
   static std::atomic<unsigned long long> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(configured.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(kv_attend_kernel<D, P, MT, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(kv_attend_kernel<D, P, MT, HALF, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              device_smem_optin() - 1024);
     if (e != cudaSuccess) return e;
     configured.fetch_or(1ull << dev);
   }
   const int sms = device_sm_count(), grid = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
   cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  constexpr int R = at_rows(MT, HALF);
+  if constexpr (CL) {
+    const int items = p.kv.n_tok * p.kv.H * ((p.G + R - 1) / R);
+    make_config(cfg, attr, dim3(items * p.cluster), dim3(at_warps(D, MT, HALF) * 32), smem, stream, true);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kv_attend_kernel<D, P, MT, HALF, CL>, p);
+  }
   make_config(cfg, attr, dim3(grid), dim3(at_warps(D, MT, HALF) * 32), smem, stream, true);
   // (exactly as many where a token is an item by itself; else at most)
-  constexpr int R = at_rows(MT, HALF);
   const long long each = (p.G + R - 1) / R;
   p.max_items = (int)(p.kv.H * (p.sel || !p.kv.starts
                                     ? each * p.kv.n_tok
                                     : ((long long)p.kv.n_tok * p.G + R - 1) / R + p.kv.n_seq));
-  e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<D, P, MT, HALF>, p);
+  e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<D, P, MT, HALF, CL>, p);
   if (e != cudaSuccess) return e;
   const bool few = (long long)p.max_items * R <= (D == 256 ? 2ll : 4ll) * sms;  // the blocks of 16 warps fit at once
   const int jw = few ? 16 : 1;
@@ -951,12 +1107,12 @@ static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
              : cudaLaunchKernelEx(&cfg, kv_join_kernel<D, R, 1>, p);
 }
 
-template <int D, int MT, bool HALF>
+template <int D, int MT, bool HALF, bool CL>
 static cudaError_t launch_attend_p(AttendParams& p, cudaStream_t stream) {
   switch (p.kv.P) {
-    case 16: return launch_attend<D, 16, MT, HALF>(p, stream);
-    case 32: return launch_attend<D, 32, MT, HALF>(p, stream);
-    default: return launch_attend<D, 64, MT, HALF>(p, stream);
+    case 16: return launch_attend<D, 16, MT, HALF, CL>(p, stream);
+    case 32: return launch_attend<D, 32, MT, HALF, CL>(p, stream);
+    default: return launch_attend<D, 64, MT, HALF, CL>(p, stream);
   }
 }
 // Rows that share a kv head, on average (with page lists a token's own).
@@ -964,20 +1120,23 @@ static long long attend_rows(const AttendParams& p) {
   return p.sel ? p.G : ((long long)p.kv.n_tok * p.G + p.kv.n_seq - 1) / p.kv.n_seq;
 }
 
-template <int D, bool HALF>
+// Row fragments of a warp.
+static int attend_mt(const AttendParams& p, int D, bool half) { return D == 64 && !half && attend_rows(p) > at_rows(1, half) ? 2 : 1; }
+
+template <int D, bool HALF, bool CL>
 static cudaError_t launch_attend_d(AttendParams& p, cudaStream_t stream) {
   if constexpr (D == 64 && !HALF)  // (else a second set of fragments and sums would not fit the registers)
-    if (attend_rows(p) > at_rows(1, HALF)) return launch_attend_p<D, 2, HALF>(p, stream);
-  return launch_attend_p<D, 1, HALF>(p, stream);
+    if (attend_mt(p, D, HALF) == 2) return launch_attend_p<D, 2, HALF, CL>(p, stream);
+  return launch_attend_p<D, 1, HALF, CL>(p, stream);
 }
 
-template <bool HALF>
+template <bool HALF, bool CL>
 static cudaError_t launch_attend_as(AttendParams& p, int D, cudaStream_t stream) {
   switch (D) {
-    case 64: return launch_attend_d<64, HALF>(p, stream);
-    case 128: return launch_attend_d<128, HALF>(p, stream);
-    case 192: return launch_attend_d<192, HALF>(p, stream);
-    default: return launch_attend_d<256, HALF>(p, stream);
+    case 64: return launch_attend_d<64, HALF, CL>(p, stream);
+    case 128: return launch_attend_d<128, HALF, CL>(p, stream);
+    case 192: return launch_attend_d<192, HALF, CL>(p, stream);
+    default: return launch_attend_d<256, HALF, CL>(p, stream);
   }
 }
 

@@ -4,7 +4,7 @@
 namespace qmv {
 
 cudaError_t launch_attend_half(AttendParams& p, int D, cudaStream_t stream) {
-  return launch_attend_as<true>(p, D, stream);
+  return launch_attend_as<true, false>(p, D, stream);
 }
 
 }  // namespace qmv

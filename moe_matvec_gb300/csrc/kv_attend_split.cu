@@ -4,7 +4,7 @@
 namespace qmv {
 
 cudaError_t launch_attend_split(AttendParams& p, int D, cudaStream_t stream) {
-  return launch_attend_as<false>(p, D, stream);
+  return launch_attend_as<false, false>(p, D, stream);
 }
 
 }  // namespace qmv

@@ -96,6 +96,33 @@ def test_the_largest_window(lib):
     assert torch.equal(out, api.kv_attend(pair.dev, q, dev32(table), dev32(lens), dev32(st)))
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D,P,G", [(64, 16, 3), (64, 64, 12), (128, 64, 4), (128, 32, 16), (192, 16, 5), (256, 64, 9)])
+def test_one_token_a_sequence_with_and_without_starts(lib, dtype, D, P, G):
+    # the same batch as items known beforehand (a cluster each) and as equal shares of the GPU
+    rng = np.random.default_rng(D + P + G)
+    lens = [1, 700, 0, 64, 333, 1500]
+    pair, table = filled(rng, 2, D, P, lens)
+    q = randn(rng, len(lens), 2 * G, D).to(dtype)
+    st = list(range(len(lens) + 1))
+    for window in (0, 70):
+        for starts in (None, dev32(st)):
+            out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), starts, window=window)
+            check(pair, q, table, lens, st, out, window=window)
+
+
+def test_rows_that_are_no_numbers_stay_so(lib):
+    rng = np.random.default_rng(28)
+    lens = [300, 50]
+    pair, table = filled(rng, 1, 128, 64, lens)
+    q = randn(rng, 2, 4, 128)
+    q[0, 1, 5] = float("nan")
+    for starts in (None, dev32([0, 1, 2])):
+        out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), starts)
+        assert out[0, 1].isnan().all()
+        assert not out[0, [0, 2, 3]].isnan().any() and not out[1].isnan().any()
+
+
 def test_a_whole_prompt(lib):
     rng = np.random.default_rng(30)
     lens = [260, 33]
