@@ -36,21 +36,24 @@ int attend_resident_clusters(int c);
 // tiles as its own sequence has: with page lists a number the host knows, else at
 // most what the table can hold (against one tile for the shares: how much of the
 // table is in use is not known here).  All clusters have to be resident at once.
-// Measured, shares / clusters: one sequence of 1000 tokens 9.5 / 8.0 us, 32 of 500
+// Measured, shares / clusters: one sequence of 1000 tokens 9.5 / 8.3 us, 32 of 500
 // 10.9 / 7.3, 64 listed pages of 16 sequences (8 tiles a warp, 7 in equal shares)
 // 32 / 28; where warps would get 5 tiles more than by shares (200 listed pages of 4
 // sequences, with append and selection) clusters lose, 31 / 34.
 constexpr int CL_TILES = 1;
-static int clusters_for(const AttendParams& p, int D, bool half) {
-  if (p.kv.starts && !p.sel) return 0;  // the items hang on starts
+static int clusters_for(AttendParams& p, int D, bool half) {
   const int mt = attend_mt(p, D, half), R = at_rows(mt, half), workers = at_warps(D, mt, half) / at_split(D);
-  const long long items = (long long)p.kv.n_tok * p.kv.H * ((p.G + R - 1) / R);
+  const bool several = p.kv.starts && !p.sel;  // tokens a sequence
+  const long long items = several ? p.kv.H * ((long long)p.kv.n_tok * p.G / R + p.kv.n_seq)
+                                  : (long long)p.kv.n_tok * p.kv.H * ((p.G + R - 1) / R);
   const long long slots = (long long)(p.sel ? p.n_sel : p.kv.max_pages) * p.kv.P;
   long long tiles = (slots + AT_TILE - 1) / AT_TILE;
-  if (p.window > 0 && !p.sel && (p.window + 62) / AT_TILE + 2 < tiles) tiles = (p.window + 62) / AT_TILE + 2;
+  const long long seen = p.window + (several ? p.kv.n_tok : 1);  // positions, at most
+  if (p.window > 0 && !p.sel && seen / AT_TILE + 2 < tiles) tiles = seen / AT_TILE + 2;
   int c = 1;
   while (c < 8 && c * workers < tiles && items <= attend_resident_clusters(2 * c)) c *= 2;
   if (items > attend_resident_clusters(c)) return 0;
+  p.max_items = (int)items;
   const long long here = (tiles + c * workers - 1) / (c * workers);
   const long long all = p.sel ? (items * tiles + workers * device_sm_count() - 1) / (workers * device_sm_count()) : 1;
   return here <= all + CL_TILES ? c : 0;

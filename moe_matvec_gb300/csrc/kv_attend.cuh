@@ -23,7 +23,7 @@
 //
 // Measured: 32 sequences of up to 8192 tokens, 40 query and 8 kv heads of 128
 // (395 MB): 68 us, 5.8 TB/s, 86% of a copy's bandwidth; one sequence of 131072
-// (269 MB): 50 us; one of 1000 (clusters): 8 us, of which the copies and products
+// (269 MB): 50 us; one of 1000 (clusters): 8.3 us, of which the copies and products
 // of its one tile a worker are 3 and the rest is the launch, dependent loads and
 // the join.
 //
@@ -303,14 +303,30 @@ __device__ __forceinline__ void store2(void* base, long long at, int dt, float x
     *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(base) + at) = __floats2bfloat162_rn(x, y);
 }
 
-// Item `id` of a batch whose items do not depend on its lengths (page lists, or
-// one token a sequence), from its first unit.  By a whole warp.
+// Item `id` of a batch dealt out by items, from its first unit; id -1 in the
+// answer: there is none.  By a whole warp.  Where sequences have several tokens,
+// sequence s owns the row tiles floor(starts[s] G / R) + s .. of each head, at
+// least as many as its rows need.
 template <int R>
 __device__ __forceinline__ AttendItem item_of(const AttendParams& p, int id) {
   AttendItem it;
-  const int n_rt = (p.G + R - 1) / R, th = id / n_rt;
   it.id = id;
   it.k = 0;
+  if (p.kv.starts && !p.sel) {
+    const int x = id / p.kv.H;
+    it.head = id - x * p.kv.H;
+    auto first_tile = [&](int t0, int s) { return (int)((long long)t0 * p.G / R) + s; };
+    it.s = last_seq_at_most(p.kv.n_seq, x, [&](int s) { return first_tile(p.kv.starts[s], s); });
+    it.seq = kv_seq(p.kv, it.s);
+    it.tbase = it.seq.t0;
+    it.nrows = it.seq.n * p.G;
+    const long long row0 = (long long)(x - first_tile(it.seq.t0, it.s)) * R;
+    if (row0 < 0 || row0 >= it.nrows) it.id = -1;
+    it.row0 = (int)row0;
+    seq_tiles(p, it.seq, it.tile0, it.tiles);
+    return it;
+  }
+  const int n_rt = (p.G + R - 1) / R, th = id / n_rt;
   it.row0 = (id - th * n_rt) * R;
   it.tbase = th / p.kv.H;
   it.head = th - it.tbase * p.kv.H;
@@ -416,6 +432,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
   const int ranks = CL ? p.cluster : 1, rank = CL ? blockIdx.x % ranks : 0;
   if constexpr (CL) {
     it = item_of<R>(p, blockIdx.x / ranks);
+    if (it.id < 0) return;  // (the whole cluster)
     const int each = (it.tiles + ranks * NG - 1) / (ranks * NG), w = group * ranks + rank;
     u0 = min(w * each, it.tiles);
     u1 = min((w + 1) * each, it.tiles);
@@ -1083,8 +1100,7 @@ static cudaError_t launch_attend(AttendParams& p, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   constexpr int R = at_rows(MT, HALF);
   if constexpr (CL) {
-    const int items = p.kv.n_tok * p.kv.H * ((p.G + R - 1) / R);
-    make_config(cfg, attr, dim3(items * p.cluster), dim3(at_warps(D, MT, HALF) * 32), smem, stream, true);
+    make_config(cfg, attr, dim3(p.max_items * p.cluster), dim3(at_warps(D, MT, HALF) * 32), smem, stream, true);
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = p.cluster;
     attr[1].val.clusterDim.y = 1;

@@ -111,14 +111,37 @@ def test_one_token_a_sequence_with_and_without_starts(lib, dtype, D, P, G):
             check(pair, q, table, lens, st, out, window=window)
 
 
+def wide(table, P):
+    """The same pages in a table of room for 100000 tokens."""
+    return np.concatenate([table, np.full((len(table), 100000 // P - table.shape[1]), -1, table.dtype)], 1)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D,P,G", [(64, 16, 3), (64, 64, 12), (128, 64, 4), (128, 32, 16), (192, 16, 5), (256, 64, 9)])
+def test_narrow_and_wide_tables(lib, dtype, D, P, G):
+    # few tiles by the table (a cluster per item) and possibly many (equal shares of the GPU)
+    rng = np.random.default_rng(D + P + G + 1)
+    for lens, news in (([1, 700, 0, 64, 333], [1, 5, 0, 2, 1]), ([0, 90, 200], [1, 1, 1]), ([40], [40])):
+        st = np.concatenate([[0], np.cumsum(news)])
+        pair, table = filled(rng, 2, D, P, lens)
+        q = randn(rng, st[-1], 2 * G, D).to(dtype)
+        for window, causal in ((0, True), (0, False), (70, True)):
+            for t in (table, wide(table, P)):
+                out = api.kv_attend(pair.dev, q, dev32(t), dev32(lens), dev32(st), causal=causal, window=window)
+                check(pair, q, table, lens, st, out, causal=causal, window=window)
+    ids = np.array([[[0, 1], [0, -1]]] * 40, np.int32)
+    out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), dev32(st), pages=dev32(ids))
+    check(pair, q, table, lens, st, out, pages=ids)
+
+
 def test_rows_that_are_no_numbers_stay_so(lib):
     rng = np.random.default_rng(28)
     lens = [300, 50]
     pair, table = filled(rng, 1, 128, 64, lens)
     q = randn(rng, 2, 4, 128)
     q[0, 1, 5] = float("nan")
-    for starts in (None, dev32([0, 1, 2])):
-        out = api.kv_attend(pair.dev, q, dev32(table), dev32(lens), starts)
+    for t in (table, wide(table, 64)):
+        out = api.kv_attend(pair.dev, q, dev32(t), dev32(lens))
         assert out[0, 1].isnan().all()
         assert not out[0, [0, 2, 3]].isnan().any() and not out[1].isnan().any()
 
