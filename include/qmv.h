@@ -539,10 +539,11 @@ int qmv_kv_read(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, void* k
  * (negative entries are skipped; an index listed twice counts twice).
  * q [n_tok][n_heads][D] (tokens q_stride elements apart), out
  * [n_tok][n_heads][D], n_heads a multiple of n_kv_heads.  Keys and values
- * enter as their exact codes; q and the softmax weights as two f16 parts (22
- * bits; f16 and bfloat16 queries from 9 rows per kv head on as one, exact but
- * for what lies 2^-25 below the row's largest); sums and the softmax
- * statistics are fp32.  The work is cut into equal
+ * enter as their exact codes; q, and the products of softmax weight and value
+ * scale, as two f16 parts (22 bits; f16 and bfloat16 queries from 9 rows per kv
+ * head on as one, exact but for what lies 2^-25 below the row's largest; a
+ * product below 2^-9 of the largest among the tokens that the row sees is off
+ * by up to 2^-31 of that one); sums and the softmax statistics are fp32.  The work is cut into equal
  * shares over the whole batch whatever its lengths, in a grid that does not
  * depend on them (a captured graph stays valid as lens grow), and joined in a
  * fixed order: results are bitwise reproducible.

@@ -62,12 +62,19 @@ constexpr int AT_TILE = 64;  // tokens of a unit
 // worker 32 x 8192 tokens of head_dim 128 took 71 us, with two 68.
 constexpr int AT_RING = 2;
 constexpr int AT_MAX_CTAS = 160;
-// Softmax weights enter f16 times 2^6 and may exceed 1 by 2^8 (a running
-// maximum is only followed when it is left behind by more than that) and, by
-// the reference scale, by 2: below 2^15, and 22 bits down to 2^-9 of the
-// largest, an error of 2^-31 of it below that.
-constexpr float AT_P_SCALE = 64.f;
-constexpr float AT_LAZY = 8.f;
+// What enters f16 for a token of a row is a dv / ref: its softmax weight a = 2^(s -
+// m), its page's value scale dv, and the row's own reference ref.  A running
+// maximum m is only followed when it is left behind by more than 2^8, so a is below
+// 2^8; ref follows the largest a dv / 2^8 of the tokens that the row sees, again
+// once that exceeds 2^8 ref.  Times 2^6 / 2^8 the largest product so far lies
+// between 2^6 and 2^14, and two f16 parts hold 22 bits of those down to 2^-9 of it
+// and leave an error of 2^-31 of it below that.  (One reference for all rows of a
+// worker, the largest dv of its pages, would cost rows their bits for pages that
+// they do not see or give no weight.)  ref is 2^-125 at least, for the divisions by
+// it: an error of less than 2^-132 where the values are too small for that.
+constexpr float AT_P_SCALE = 0.25f;  // 2^6 / 2^8
+constexpr float AT_LAZY = 8.f;       // powers of two
+constexpr float AT_REF_MIN = 0x1p-117f;
 
 // Warps of a CTA: the quarters of an SM hold whole warps, 8 of up to 255
 // registers a thread or 12 of up to 168, and q and the accumulators take them.
@@ -653,13 +660,14 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
         }
       }
     }
-    float o[MT][NV][4], m[MT][NR], l[MT][NR], vref = 0.f;
+    float o[MT][NV][4], m[MT][NR], l[MT][NR], ref[MT][NR];
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) {
 #pragma unroll
       for (int nr = 0; nr < NR; nr++) {
         m[mt][nr] = -INFINITY;
         l[mt][nr] = 0.f;
+        ref[mt][nr] = AT_REF_MIN;
       }
 #pragma unroll
       for (int n = 0; n < NV; n++) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
@@ -782,15 +790,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
             }
           }
         }
-        // values share one reference scale per warp: raised when a page's is over twice it
-        float vmax = fmaxf(dv, __shfl_xor_sync(0xffffffffu, dv, 1));
-        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-        float vfix = 1.f;
-        if (vmax > 2.f * vref) {
-          vfix = vref / vmax;
-          vref = vmax;
-        }
-        const float vrel = vref > 0.f ? __fdividef(dv, vref) * AT_P_SCALE : 0.f;
+        const float dvm = fminf(dv, 0x1p126f);  // (finite times a weight of 0; no finite scale is as large)
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
           float fix[NR];
@@ -799,20 +799,30 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
             // the lane's products share one factor to logits in powers of two
             // (not 0: a masked product is -inf)
             const float f = fmaxf(qs[mt][nr] * dk, 0x1p-120f);
-            float mx = s[mt][nr][0][0];
+            float mine = s[mt][nr][0][0];
 #pragma unroll
-            for (int j = 0; j < NJ; j++) mx = fmaxf(mx, fmaxf(s[mt][nr][j][0], s[mt][nr][j][1]));
-            mx *= f;
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            for (int j = 0; j < NJ; j++) mine = fmaxf(mine, fmaxf(s[mt][nr][j][0], s[mt][nr][j][1]));
+            mine *= f;
+            float mx = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            fix[nr] = vfix;
             if (mx > m[mt][nr] + AT_LAZY || (m[mt][nr] == -INFINITY && mx > m[mt][nr])) {
               const float alpha = ex2(m[mt][nr] - mx);
-              fix[nr] *= alpha;
               l[mt][nr] *= alpha;
+              ref[mt][nr] *= alpha;  // (in place of the sums)
               m[mt][nr] = mx;
             }
             const float ms = m[mt][nr] == -INFINITY ? 0.f : m[mt][nr];
+            // the largest of the lanes' pages that the row sees
+            float top = fmaxf(ex2(mine - ms - AT_LAZY) * dvm, AT_REF_MIN);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            fix[nr] = 1.f;
+            if (top > ref[mt][nr] * 256.f) {
+              fix[nr] = __fdividef(ref[mt][nr], top);
+              ref[mt][nr] = top;
+            }
+            // (finite for pages that the row does not see, whose weights are 0)
+            const float vrel = fminf(__fdividef(dv, ref[mt][nr]) * AT_P_SCALE, 0x1p127f);
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < NJ; j++) {
@@ -867,8 +877,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
     const bool begins = it.k == 0, ends = it.k + seg == it.tiles, whole = begins && ends;
     // (with page lists a token may lie in no sequence: its row is not written)
     const bool covered = it.tbase >= it.seq.t0 && it.tbase < it.seq.t0 + it.seq.n;
-    const float back = vref * (1.f / AT_P_SCALE);
-    // column pair n2 of the lane's row: o in fp32, without the reference scale
+    // column pair n2 of the lane's row: o in fp32 times f (the reference put back)
     auto pair = [&](int mt, int nr, int n2, float f) {
       const float(&x)[4] = o[mt][n2];
       return HALF ? make_float2(x[2 * nr] * f, x[2 * nr + 1] * f) : make_float2((x[0] + x[2]) * f, (x[1] + x[3]) * f);
@@ -885,7 +894,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
       }
       float* dst = slot + 2 * R + row * D + DW * part + 2 * c;
 #pragma unroll
-      for (int n2 = 0; n2 < NV; n2++) *reinterpret_cast<float2*>(dst + 8 * n2) = pair(mt, nr, n2, back);
+      for (int n2 = 0; n2 < NV; n2++) *reinterpret_cast<float2*>(dst + 8 * n2) = pair(mt, nr, n2, ref[mt][nr] * (1.f / AT_P_SCALE));
     };
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) {
@@ -973,6 +982,7 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
           write_slot(slots + (begins ? at_slot_floats(D, R) : 0), mt, nr);
         } else if (covered && rr < it.nrows) {
           // (a row that is no number stays one)
+          const float back = ref[mt][nr] * (1.f / AT_P_SCALE);
           const float f = l[mt][nr] > 0.f ? back / l[mt][nr] : l[mt][nr] != l[mt][nr] ? NAN : 0.f;
           const long long at = ((long long)(it.tbase + rr / p.G) * p.n_heads + it.head * p.G + rr % p.G) * D + DW * part + 2 * c;
 #pragma unroll
