@@ -524,7 +524,8 @@ def kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, lens: torch.
               stream=None) -> torch.Tensor:
     """Attention of the last tokens of each sequence over the cache (qmv_kv_attend).
     q [n_tok][n_heads][D] (tokens may be strided), scale 1 / sqrt(D) if None, pages int32
-    [n_tok][n_kv_heads][n_sel] (kv_select's) or None for all.  Returns out like q."""
+    [n_tok][n_kv_heads][n_sel] (kv_select's; n_sel 0 is refused) or None for all.
+    Returns out like q."""
     return _nat().kv_attend(ctypes.addressof(cache), q, table, lens, starts, scale, causal, window, pages, ws, out,
                             _on(stream))
 

@@ -389,6 +389,8 @@ PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (t.dim() != 3 || t.size(0) != n_tok || t.size(1) != c->n_kv_heads || t.size(2) > INT32_MAX)
         value_error("pages: [" + std::to_string(n_tok) + "][" + std::to_string(c->n_kv_heads) + "][n_sel] wanted, got " +
                     text(t.sizes()));
+      // (an empty tensor has no address, which would mean all pages)
+      if (t.size(2) < 1) check(QMV_ERR_SHAPE, "qmv_kv_attend");
       pages = ints(t);
       n_sel = (int)t.size(2);
     }
