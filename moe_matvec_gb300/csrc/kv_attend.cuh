@@ -532,13 +532,13 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
       if (p.sel) {
         const int j = x.k * ppt + i;
         const long long at = ((long long)x.tbase * p.kv.H + x.head) * p.n_sel + j;
-        pg = j < p.n_sel && QMV_CHECK(in_range(at, 1, p.sel_len, p.kv.err)) ? p.sel[at] : -1;
+        // a token that no sequence covers has no pages (its list may hold anything)
+        const bool listed = j < p.n_sel && x.tbase >= x.seq.t0 && x.tbase < x.seq.t0 + x.seq.n;
+        pg = listed && QMV_CHECK(in_range(at, 1, p.sel_len, p.kv.err)) ? p.sel[at] : -1;
         if (pg >= p.kv.max_pages) {
           set_error(p.kv.err, QMV_DEVERR_PAGE);
           pg = -1;
         }
-        // a token that no sequence covers has no pages
-        if (x.tbase < x.seq.t0 || x.tbase >= x.seq.t0 + x.seq.n) pg = -1;
       } else {
         pg = (x.tile0 + x.k) * ppt + i;
       }
