@@ -442,8 +442,9 @@ int moe_route_run(int fmt, const void* Wr, const float* x, int n_experts, int64_
  * one is): res [rows][K] = s and y [rows][K] in dtype, and y quantized by the
  * activation rule into the Q8 activation layout of qmv_quantize_act (q int8
  * [rows][K], d fp32 and sum int32 [rows][K/32], given together), which
- * qmv_run_q8 takes: no matvec then quantizes its input again.  res and y may
- * be r or (with ldx = K) x.
+ * qmv_run_q8 takes: no matvec then quantizes its input again.  Values that are
+ * no numbers (non-finite inputs; a zero row with eps 0) stay NaN in y and have
+ * the code 0.  res and y may be r or (with ldx = K) x.
  * Constraints: 1 <= K <= QMV_MAX_NORM (any K without q; with q K % 256 == 0
  * and ldx * element size a multiple of 16, else QMV_ERR_ALIGN), 1 <= rows <=
  * 2^24, eps >= 0. */

@@ -7,24 +7,35 @@
 
 namespace qmv {
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // The activation rule on a lane's eight values of a block (four lanes a
 // block, as quant_units): codes in two words, scale, sum.  A block whose
 // largest magnitude is 0 or at least 2^-100 rounds by adding and taking away
 // 1.5 * 2^23: the sum's low mantissa bits are then the integer, rounded half to
-// even, in two's complement (the exact product is below 127.5).  Other blocks
-// take the IEEE operations and the clamp.
+// even, in two's complement (the exact product is below 127.5).  Other blocks,
+// among them those with a NaN (whose code is 0), take the IEEE operations and the
+// clamp.
 __device__ __forceinline__ void quant8(const float (&v)[8], uint32_t& w0, uint32_t& w1, float& d, int& sum) {
-  float m = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
-                  fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
-  m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
-  m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
+  auto largest = [&](auto max) {
+    float m = max(max(max(fabsf(v[0]), fabsf(v[1])), max(fabsf(v[2]), fabsf(v[3]))),
+                  max(max(fabsf(v[4]), fabsf(v[5])), max(fabsf(v[6]), fabsf(v[7]))));
+    m = max(m, __shfl_xor_sync(FULL, m, 1));
+    return max(m, __shfl_xor_sync(FULL, m, 2));
+  };
+  float m = largest([](float a, float b) { return max_nan(a, b); });
   uint32_t q[8];
-  if (!__any_sync(FULL, m > 0.0f && !(m >= 0x1p-100f && m < INFINITY))) {
+  if (!__any_sync(FULL, m != 0.0f && !(m >= 0x1p-100f && m < INFINITY))) {
     d = div127_rn(m);
     const float id = m > 0.0f ? rcp_rn(fmaxf(d, 0x1p-126f)) : 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; k++) q[k] = __float_as_uint(__fadd_rn(__fmul_rn(v[k], id), 12582912.0f));
   } else {
+    m = largest([](float a, float b) { return fmaxf(a, b); });
     d = __fdiv_rn(m, 127.0f);
     const float id = d > 0.0f ? __frcp_rn(d) : 0.0f;
 #pragma unroll
