@@ -1,4 +1,5 @@
 """Norm rows at the edges of its arithmetic."""
+import numpy as np
 import pytest
 import torch
 
@@ -32,3 +33,22 @@ def test_codes_of_what_is_no_number(lib, dtype, K):
         assert (q[1:3] == 0).all() and (s[1:3] == 0).all()
         alone = api.rms_norm(x, weights, 0.0, want="q8")[1]
         assert torch.equal(alone[0], q) and torch.equal(alone[2], s) and torch.equal(bits(alone[1]), bits(d))
+
+
+@pytest.mark.parametrize("K", [16640, 32768, 32765])
+def test_one_large_value_and_many_small_ones(lib, K):
+    # Squares just under half a unit in the last place of the running sum: summed one
+    # after another into one register, every one of them is lost (64 terms a thread:
+    # 31 * 2^-24 of y).  Partial sums of eight values keep them: at most 8 + 8 terms
+    # a thread and 10 levels, half of 26 * 2^-24 from the sum; the reciprocal root is off
+    # by up to 4 * 2^-24, division, eps and the two products by 3 in all.
+    for first in range(8):
+        x = torch.full((1, K), 0.995 * 2.0 ** -12, device="cuda")
+        if K % 8 == 0:  # eight neighbours a thread and step
+            x[0, first:4096:8] = 1
+        else:  # a thread's values lie 512 apart
+            x[0, first * 512:first * 512 + 512] = 1
+        y = api.rms_norm(x, torch.ones(K, device="cuda"), 0.0)[0].double().cpu().numpy()
+        s = x.double().cpu().numpy()
+        want = s / np.sqrt((s * s).mean())
+        assert (np.abs(y - want) <= 20 * 2.0 ** -24 * np.abs(want)).all()
