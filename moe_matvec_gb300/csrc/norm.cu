@@ -7,9 +7,14 @@
 
 namespace qmv {
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one of them is
   float m;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
   return m;
 }
 
@@ -21,13 +26,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
 // among them those with a NaN (whose code is 0), take the IEEE operations and the
 // clamp.
 __device__ __forceinline__ void quant8(const float (&v)[8], uint32_t& w0, uint32_t& w1, float& d, int& sum) {
-  auto largest = [&](auto max) {
-    float m = max(max(max(fabsf(v[0]), fabsf(v[1])), max(fabsf(v[2]), fabsf(v[3]))),
-                  max(max(fabsf(v[4]), fabsf(v[5])), max(fabsf(v[6]), fabsf(v[7]))));
-    m = max(m, __shfl_xor_sync(FULL, m, 1));
-    return max(m, __shfl_xor_sync(FULL, m, 2));
-  };
-  float m = largest([](float a, float b) { return max_nan(a, b); });
+  float m = max_nan(max_nan(fabsf(v[0]), fabsf(v[1]), fabsf(v[2])), max_nan(fabsf(v[3]), fabsf(v[4]), fabsf(v[5])),
+                    max_nan(fabsf(v[6]), fabsf(v[7])));
+  m = max_nan(m, __shfl_xor_sync(FULL, m, 1));
+  m = max_nan(m, __shfl_xor_sync(FULL, m, 2));
   uint32_t q[8];
   if (!__any_sync(FULL, m != 0.0f && !(m >= 0x1p-100f && m < INFINITY))) {
     d = div127_rn(m);
@@ -35,7 +37,11 @@ __device__ __forceinline__ void quant8(const float (&v)[8], uint32_t& w0, uint32
 #pragma unroll
     for (int k = 0; k < 8; k++) q[k] = __float_as_uint(__fadd_rn(__fmul_rn(v[k], id), 12582912.0f));
   } else {
-    m = largest([](float a, float b) { return fmaxf(a, b); });
+    m = fabsf(v[0]);
+#pragma unroll
+    for (int k = 1; k < 8; k++) m = fmaxf(m, fabsf(v[k]));
+    m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
     d = __fdiv_rn(m, 127.0f);
     const float id = d > 0.0f ? __frcp_rn(d) : 0.0f;
 #pragma unroll
