@@ -1001,7 +1001,8 @@ __global__ void __launch_bounds__(at_warps(D, MT, HALF) * 32, 1) kv_attend_kerne
       j.row0 = it.row0;
       j.nrows = it.nrows;
       j.head = it.head;
-      if (it.id < p.max_items) p.joins[it.id] = j;
+      // (starts that descend can name more items than there is room for, or than 32 bits count)
+      if ((unsigned)it.id < (unsigned)p.max_items) p.joins[it.id] = j;
     }
     u += seg;
     if (u >= u1) break;
