@@ -104,20 +104,22 @@ _SIGS = {
 }
 
 _lib = None
-_native = None  # the native module, driving _lib
+_native = None  # the native module, driving _lib (None until a call needs it)
 _NATIVE_CALLS = ("qmv_rms_norm", "qmv_dequantize_act", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attend",
                  "qmv_kv_attend_workspace_bytes", "qmv_kv_select", "qmv_kv_select_workspace_bytes")
 
 
+def _bind():
+    """Point the native module at the active library."""
+    _native.bind(QmvError, *[ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS])
+
+
 def _activate(lib):
     """Make `lib` the library that every call goes to."""
-    global _lib, _native
-    if _native is None:
-        loader = importlib.machinery.ExtensionFileLoader("_binding", _build.build_binding())
-        _native = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
-        loader.exec_module(_native)
-    _native.bind(QmvError, *[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS])
+    global _lib
     _lib = lib
+    if _native is not None:
+        _bind()
     return lib
 
 
@@ -426,9 +428,16 @@ _WANT = {"float": 1, "q8": 2, "both": 3}
 
 
 def _nat():
-    """The native module (loading the library first if needed)."""
+    """The native module, built and loaded by the first call that goes through it
+    (the calls that go through ctypes need none of Python's and torch's headers)."""
+    global _native
     if _native is None:
         load()
+        loader = importlib.machinery.ExtensionFileLoader("_binding", _build.build_binding())
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+        loader.exec_module(module)
+        _native = module
+        _bind()
     return _native
 
 
