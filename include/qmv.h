@@ -488,10 +488,20 @@ typedef struct qmv_kv_cache {
  *   1 <= n_seq <= QMV_MAX_SEQS, 1 <= n_tok <= QMV_MAX_BATCH_TOKENS (qmv_kv_read:
  *   2^24), 1 <= max_pages <= 2^20.
  * The same lens serve qmv_kv_append, qmv_kv_select and qmv_kv_attend of one
- * step.  What only the device can see is checked there: a page index outside
- * [0, n_pages) sets QMV_DEVERR_PAGE and its tokens are left out; lens or
- * starts that contradict n_tok, max_pages or each other set QMV_DEVERR_BATCH
- * and are clamped.  Rows of tokens that no sequence covers are not written. */
+ * step.  What only the device can see is checked there, where it is used:
+ *   a page index outside [0, n_pages) sets QMV_DEVERR_PAGE and its tokens are
+ *   left out;
+ *   a sequence whose starts[s], starts[s+1] descend or leave [0, n_tok], or
+ *   whose lens[s] is negative or more than max_pages * P, sets
+ *   QMV_DEVERR_BATCH, and they are clamped;
+ *   of a sequence with more new tokens than lens[s], the first lie at positions
+ *   below 0: qmv_kv_append leaves these out, qmv_kv_read gives zeros (both set
+ *   QMV_DEVERR_BATCH, but for lens[s] = 0, an empty slot), in qmv_kv_attend they
+ *   see what their masks leave (causal: nothing) and qmv_kv_select picks no page
+ *   for them, without an error.
+ * Any content of these arrays leads to indexes inside the buffers alone.
+ * starts may begin above 0 and end below n_tok (padding): rows of tokens that no
+ * sequence covers are not written, nor their page lists read. */
 #define QMV_MAX_SEQS 1024
 #define QMV_MAX_BATCH_TOKENS 65535
 typedef struct qmv_kv_batch {
@@ -539,15 +549,20 @@ int qmv_kv_read(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, void* k
  * indices of the sequence listed there for the token and kv head are read
  * (negative entries are skipped; an index listed twice counts twice).
  * q [n_tok][n_heads][D] (tokens q_stride elements apart), out
- * [n_tok][n_heads][D], n_heads a multiple of n_kv_heads.  Keys and values
+ * [n_tok][n_heads][D], n_heads <= 16384 a multiple of n_kv_heads.  Keys and values
  * enter as their exact codes; q, and the products of softmax weight and value
  * scale, as two f16 parts (22 bits; f16 and bfloat16 queries from 9 rows per kv
  * head on as one, exact but for what lies 2^-25 below the row's largest; a
  * product below 2^-9 of the largest among the tokens that the row sees is off
- * by up to 2^-31 of that one); sums and the softmax statistics are fp32.  The work is cut into equal
- * shares over the whole batch whatever its lengths, in a grid that does not
- * depend on them (a captured graph stays valid as lens grow), and joined in a
- * fixed order: results are bitwise reproducible.
+ * by up to 2^-31 of that one); sums and the softmax statistics are fp32.
+ * The work is cut into equal shares over the whole batch whatever its lengths,
+ * or, where max_pages, the window or n_sel say that there are few tiles to an
+ * item and few items, into a cluster of 1 to 8 CTAs per (sequence, kv head, 8 to
+ * 16 rows).  Which one, and its grid, depend on the call's arguments and not on
+ * the contents of lens (a captured graph stays valid as they grow), and parts are
+ * joined in a fixed order: results are bitwise reproducible from call to call of
+ * the same arguments.  (The same pages in a wider table may take the other way,
+ * and their sums another order.)
  * ws: qmv_kv_attend_workspace_bytes(c, n_heads, n_tok, n_seq) bytes, any content. */
 size_t qmv_kv_attend_workspace_bytes(const qmv_kv_cache* c, int n_heads, int n_tok, int n_seq);
 int qmv_kv_attend(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const void* q, int64_t q_stride,
@@ -564,8 +579,9 @@ int qmv_kv_attend(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const
  * largest score among the pages before it (equal scores: the lower index),
  * in ascending order, -1 after the last where there are fewer.  The scores
  * have no rounding that depends on an order, so neither do the picks.
- * ids int32 [n_tok][n_kv_heads][n_sel], 1 <= n_sel <= 2^20; the cache has
- * bounds.  ws: qmv_kv_select_workspace_bytes(c, b) bytes, any content. */
+ * ids int32 [n_tok][n_kv_heads][n_sel], 1 <= n_sel <= 2^20; n_heads <= 16384 a
+ * multiple of n_kv_heads and at most 256 times it; the cache has bounds.
+ * ws: qmv_kv_select_workspace_bytes(c, b) bytes, any content. */
 size_t qmv_kv_select_workspace_bytes(const qmv_kv_cache* c, const qmv_kv_batch* b);
 int qmv_kv_select(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const void* q, int64_t q_stride,
                   int n_heads, int32_t* ids, int n_sel, void* ws, size_t ws_bytes, cudaStream_t stream);

@@ -1,7 +1,7 @@
 """lens and starts that contradict the call's sizes or each other: attention,
 selection and read-back stay inside their buffers (guard bands, and no failed
 check in the range-checked build, which goes first), flag what they use of them,
-and the next call is right again.  (Append: tests/test_kv_cache_gpu.py.)"""
+and the next call is right again.  (Append's bytes: tests/test_kv_cache_gpu.py.)"""
 import numpy as np
 import pytest
 import torch
@@ -67,3 +67,55 @@ def test_contradictions_stay_inside(lib, dbg, what, D, P, G, dtype):
                 k.check_guards("k"), v.check_guards("v")
                 good = api.kv_attend(pair.dev, q, td, dev32(LENS), dev32(STARTS))
                 check(pair, q, table, LENS, STARTS, good)
+
+
+def test_what_append_flags(lib):
+    rng = np.random.default_rng(1)
+    c = api.kv_cache(1, 64, 16, 8)
+    k = randn(rng, 4, 1, 64)
+
+    def call(lens, starts):
+        api.kv_append(c, k, k, dev32([[0, 1], [2, 3]]), dev32(lens), dev32(starts))
+        return api.get_device_error()
+
+    assert call([4, 4], [3, 1, 2]) == api.DEVERR_BATCH      # descending
+    assert call([4, 4], [0, 2, 5]) == api.DEVERR_BATCH      # past n_tok
+    assert call([4, 1], [0, 2, 4]) == api.DEVERR_BATCH      # two tokens of one
+    assert call([4, 0], [0, 2, 4]) == 0                     # an empty slot
+    assert call([4, 4], [1, 2, 3]) == 0                     # padding at both ends
+
+
+def test_more_new_tokens_than_the_sequence_holds(lib):
+    # three of four tokens lie before the sequence's first: zeros (flagged by the read-back), no picks, nothing seen
+    rng = np.random.default_rng(2)
+    lens, starts = [1, 33], [0, 4, 6]
+    pair, table = filled(rng, 2, 64, 16, lens)
+    q = randn(rng, 6, 4, 64)
+    args = dev32(lens), dev32(starts)
+    for t in (table, wide(table, 16)):
+        out = api.kv_attend(pair.dev, q, dev32(t), *args)
+        ids = api.kv_select(pair.dev, q, dev32(t), args[0], 2, args[1])
+        assert api.get_device_error() == 0
+        assert (out[:3] == 0).all() and (ids[:3] == -1).all()
+        check(pair, q, table, lens, starts, out)
+        k, v = api.kv_read(pair.dev, dev32(t), *args, 6)
+        assert api.get_device_error() == api.DEVERR_BATCH
+        assert (k[:3] == 0).all() and (v[:3] == 0).all()
+
+
+def test_padding_at_both_ends_is_left_alone(lib):
+    rng = np.random.default_rng(3)
+    lens, starts = [90, 20], [1, 4, 5]
+    pair, table = filled(rng, 2, 64, 16, lens)
+    q = randn(rng, 7, 4, 64)
+    for t in (table, wide(table, 16)):
+        td, args = dev32(t), (dev32(lens), dev32(starts))
+        out, k, v = torch.full_like(q, 7), *(torch.full((7, 2, 64), 7.0, device="cuda") for _ in range(2))
+        ids = torch.full((7, 2, 3), 7, dtype=torch.int32, device="cuda")
+        api.kv_attend(pair.dev, q, td, *args, out=out)
+        api.kv_select(pair.dev, q, td, args[0], 3, args[1], ids=ids)
+        api.kv_read(pair.dev, td, *args, 7, k=k, v=v)
+        assert api.get_device_error() == 0
+        for x in (out, ids, k, v):
+            assert (x[[0, 5, 6]] == 7).all()
+        check(pair, q[1:5], table, lens, [0, 3, 4], out[1:5])
