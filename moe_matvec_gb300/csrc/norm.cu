@@ -114,17 +114,23 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) rms_norm_kernel(const No
     T v[8];
   };
   Raw nx[NV], nr[NV];
-  auto fetch = [&](long long row) {
+  auto fetch_step = [&](long long row, int i) {
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-#pragma unroll
-      for (int j = 0; j < 8; j++) from_float(0.f, nx[i].v[j]), from_float(0.f, nr[i].v[j]);
-      if (row < p.rows) {
-        load(x, row * p.ldx, QMV_EXTENT(p.x_len), nx[i].v, i);
-        if (r) load(r, row * p.K, QMV_EXTENT(p.n), nr[i].v, i);
-      }
+    for (int j = 0; j < 8; j++) from_float(0.f, nx[i].v[j]), from_float(0.f, nr[i].v[j]);
+    if (row < p.rows) {
+      load(x, row * p.ldx, QMV_EXTENT(p.x_len), nx[i].v, i);
+      if (r) load(r, row * p.K, QMV_EXTENT(p.n), nr[i].v, i);
     }
   };
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) fetch_step(row, i);
+  };
+  // Rows of over 16384 values: fetched and summed a step at a time (the raw values
+  // of eight steps do not fit the registers beside their floats: 512 x 32768
+  // bfloat16 24 us, now 21), in partial sums of eight (64 squares a thread one after
+  // another lose many small ones beside a large one; so at most 16 roundings).
+  constexpr bool LONG = NV == NORM_MAX_STEPS;
   constexpr bool AHEAD = NV <= 2;   // the next row on its way (registers)
   constexpr bool KEEP_W = NV <= 2;  // else w is read again for every row
   if constexpr (AHEAD) fetch(row0);
@@ -138,19 +144,21 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) rms_norm_kernel(const No
   // every row of the CTA makes the same number of steps
   for (long long first = (long long)blockIdx.x * blockDim.y; first < p.rows; first += stride, turn ^= 1) {
     const long long row = first + threadIdx.y;
-    if constexpr (!AHEAD) fetch(row);
+    if constexpr (!AHEAD && !LONG) fetch(row);
     float v[NV][8];
-    float sum = 0.f;  // eight terms a partial sum: at most 16 roundings a thread
+    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
+      if constexpr (LONG) fetch_step(row, i);
       float eight = 0.f;
+      float& into = LONG ? eight : sum;
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         v[i][j] = to_float(nx[i].v[j]);
         if (r) v[i][j] += to_float(nr[i].v[j]);
-        eight = fmaf(v[i][j], v[i][j], eight);
+        into = fmaf(v[i][j], v[i][j], into);
       }
-      sum += eight;
+      if constexpr (LONG) sum += eight;
     }
     if constexpr (AHEAD)
       if (first + stride < p.rows) fetch(row + stride);
