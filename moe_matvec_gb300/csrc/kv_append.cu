@@ -107,11 +107,12 @@ __device__ __forceinline__ void transpose4(const uint32_t (&w)[4], uint32_t (&o)
 // NQ: groups of four slots a thread holds.  Prompts take 256 threads (512 for
 // wider heads, whose values would take too many registers): the fewer,
 // the smaller the share of finding the page and its scale.  Single tokens (ONE)
-// take 128, a group being one slot.  Bound by instructions (63% of issue slots)
-// and latency more than HBM at prompt sizes: ragged prompts of up to 6000
-// bfloat16 tokens, 6 sequences, 8 heads of 128 (122 MB): 29 us, 4.2 TB/s; by
-// latency (lens, table, scale, codes one after another) at single tokens: 64
-// sequences 4 us.
+// take 128, a group being one slot.  At prompt sizes neither HBM (3.0 TB/s read
+// and written) nor the issue slots (62%) are full: a CTA loads its page and then
+// packs it, five warps a scheduler, and loads are what they wait for most (2.0
+// warps per issue).  Ragged prompts of up to 6000 bfloat16 tokens, 6 sequences, 8
+// heads of 128 (122 MB): 29 us, 4.2 TB/s.  Single tokens are bound by latency
+// (lens, table, scale, codes one after another): 64 sequences 3.3 us.
 template <int DT, int D, bool ONE>
 struct AppendShape {
   static constexpr int THREADS = ONE ? 128 : D * sizeof(typename Elem<DT>::type) > 256 ? 512 : 256, HALF = THREADS / 2, COLS = D / 4, TG = HALF / COLS;

@@ -36,7 +36,7 @@ int attend_resident_clusters(int c);
 // tiles as its own sequence has: with page lists a number the host knows, else at
 // most what the table can hold (against one tile for the shares: how much of the
 // table is in use is not known here).  All clusters have to be resident at once.
-// Measured, shares / clusters: one sequence of 1000 tokens 9.5 / 8.3 us, 32 of 500
+// Measured, shares / clusters: one sequence of 1000 tokens 9.5 / 8.2 us, 32 of 500
 // 10.9 / 7.3, 64 listed pages of 16 sequences (8 tiles a warp, 7 in equal shares)
 // 32 / 28; where warps would get 5 tiles more than by shares (200 listed pages of 4
 // sequences, with append and selection) clusters lose, 31 / 34.

@@ -22,10 +22,13 @@
 // made of is worked out 32 tiles at a time, a lane each.
 //
 // Measured: 32 sequences of up to 8192 tokens, 40 query and 8 kv heads of 128
-// (395 MB): 68 us, 5.8 TB/s, 86% of a copy's bandwidth; one sequence of 131072
-// (269 MB): 50 us; one of 1000 (clusters): 8.3 us, of which the copies and products
+// (395 MB): 67 us, 5.9 TB/s, 87% of a copy's bandwidth; one sequence of 131072
+// (269 MB): 50 us; one of 1000 (clusters): 8.2 us, of which the copies and products
 // of its one tile a worker are 3 and the rest is the launch, dependent loads and
-// the join.
+// the join.  16 rows in halves (16 x 8192, 176 MB): 42 us; head_dim 192 / 256 (fp32,
+// 132 / 176 MB): 32 / 38 us, 4.0-4.5 TB/s with 34-38% of the issue slots and 27-38%
+// of the tensor pipe in use: two warps a scheduler, each of which waits for
+// its own chain of codes, products and softmax.
 //
 // The arithmetic (mma.sync m16n8k16, f16 operands, fp32 sums) has codes, exact
 // in f16, in B.  With fp32 queries the rows of A are 8 query rows in two f16

@@ -67,9 +67,10 @@ __device__ __forceinline__ void quant8(const float (&v)[8], uint32_t& w0, uint32
 // values, consecutive threads taking consecutive ones.
 //
 // Bound by HBM for many rows: 4096 x 5120 bfloat16 with the residual, the
-// float and the Q8 result (194 MB): 30 us, 6.4 TB/s (and the codes read back 44
-// us, 57 with one row a CTA).  One row of 5120: 2 us, the latency of a load, two
-// barriers and the stores.
+// float and the Q8 result (194 MB): 32 us, 6.1 TB/s (and the codes read back 44
+// us, 57 with one row a CTA).  One row of 5120: 2.7 us, the latency of a load, two
+// barriers and the stores.  Without VEC by the number of loads and stores: 2000 x
+// 4097 bfloat16 22 us, 1.5 TB/s (4096: 6.4 us).
 template <int DT, bool VEC, int NV>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) rms_norm_kernel(const NormParams p) {
   using T = typename Elem<DT>::type;
