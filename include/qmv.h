@@ -196,10 +196,15 @@ enum qmv_status {
 
 #define QMV_DEVERR_PAGE 0x10  /* a page index outside the cache (its tokens are left out) */
 #define QMV_DEVERR_BATCH 0x20 /* lens / starts that contradict the call's sizes (clamped) */
+#define QMV_DEVERR_ADAPTER 0x40 /* an adapter id past the pool (its token goes without) */
+#define QMV_DEVERR_TOKEN 0x80   /* a token id past the vocabulary (its log probability is NaN) */
 
 #define QMV_MAX_TOKENS 64
 #define QMV_MAX_PREFILL_TOKENS 16384 /* moe_qmv_prefill_run */
 #define QMV_MAX_TOPK 8
+#define QMV_MAX_TOP 32   /* alternatives of qmv_logprobs */
+#define QMV_MAX_GIVEN 64 /* given tokens a row of qmv_logprobs */
+#define QMV_MAX_RANK 128 /* qmv_lora_run */
 
 /* Bytes of one quantized row of K weights; negative QMV_ERR_* if fmt or K is
  * invalid. */
@@ -585,6 +590,134 @@ int qmv_kv_attend(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const
 size_t qmv_kv_select_workspace_bytes(const qmv_kv_cache* c, const qmv_kv_batch* b);
 int qmv_kv_select(const qmv_kv_cache* c, const qmv_kv_batch* b, int dtype, const void* q, int64_t q_stride,
                   int n_heads, int32_t* ids, int n_sel, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The rest of a decode step: head norm and position rotation, low-rank
+ * adapters, expert selection from logits, log probabilities.  (The pages name
+ * the router's gating, top-k and weight normalization, "Castagna Veloce",
+ * section "Fused operations"; the formulas and interfaces here are this
+ * library's own.)
+ * ------------------------------------------------------------------------ */
+
+/* How a model turns its heads: the first R = 2 * (number of frequencies) of a
+ * head's D values are R / 2 pairs, pair i the values (i, i + R / 2), or
+ * (2i, 2i + 1) if interleaved.  Pair i of a token turns by the angle
+ * pos[axis[i]] * freq[i], a token having n_axes positions (one in text; time,
+ * height and width for images and video), and is multiplied by scale.
+ *   freq fp32 [R / 2] radians a position; axis uint8 [R / 2] below n_axes, NULL:
+ *   all 0 (an entry that is not below n_axes sets QMV_DEVERR_BATCH and counts
+ *   as 0).  Device memory.
+ * D is even, 2 <= D <= 256; 2 <= R <= D, even; 1 <= n_axes <= 4. */
+typedef struct qmv_rope {
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t n_axes;
+  float scale; /* 1, or the attention factor of a stretched context */
+  int32_t reserved;
+  const float* freq;
+  const uint8_t* axis;
+} qmv_rope;
+
+/* Norm of each head and its rotation, queries and keys in one pass, as they
+ * enter qmv_kv_append, qmv_kv_select and qmv_kv_attend:
+ *   u = x * (1 / sqrt(mean(x^2) + eps)) * w  over the head's D values (w fp32
+ *   [D]; w NULL: u = x), then with c, s = cos, sin of the pair's angle
+ *   (a, b) -> scale * (a c - b s, b c + a s), values past R as they are in u.
+ * The angle is formed and reduced in 64 bits (any int32 position), everything
+ * else is fp32.  q [n_tok][n_heads][D] with tokens q_stride elements apart, q_out
+ * likewise (q itself with the same stride: in place); k the same with n_kv_heads
+ * (NULL with n_kv_heads 0: none).
+ * Positions: pos int32 [n_tok][n_axes], or NULL and the batch's lens int32
+ * [n_seq] and starts int32 [n_seq + 1] as in qmv_kv_batch (starts NULL: one token
+ * per sequence): token i of sequence s lies at lens[s] - (starts[s+1] -
+ * starts[s]) + i on every axis.  Rows that no sequence covers are not written; starts
+ * and lens that contradict n_tok set QMV_DEVERR_BATCH.
+ * Constraints: 1 <= n_tok <= QMV_MAX_BATCH_TOKENS, n_heads and n_kv_heads <=
+ * 16384; pointers and token strides multiples of 16 bytes. */
+int qmv_norm_rope(const qmv_rope* rope, int dtype, const void* q, int64_t q_stride, void* q_out,
+                  int64_t q_out_stride, int n_heads, const float* q_w, const void* k, int64_t k_stride, void* k_out,
+                  int64_t k_out_stride, int n_kv_heads, const float* k_w, float eps, const int32_t* pos,
+                  const int32_t* lens, const int32_t* starts, int n_seq, int n_tok, cudaStream_t stream);
+
+/* A pool of low-rank adapters of one projection K -> M:
+ *   A [n_adapters][rank][K] and B [n_adapters][M][rank] of one qmv_dtype;
+ *   ranks int32 [n_adapters] (NULL: rank): how many of an adapter's rows of A and
+ *   columns of B count (clamped to 0 .. rank; the others are not used); scales
+ *   fp32 [n_adapters] (NULL: 1).  Device memory.
+ * rank % 4 == 0, 4 <= rank <= QMV_MAX_RANK; 1 <= n_adapters <= 2^20. */
+typedef struct qmv_lora {
+  int32_t n_adapters;
+  int32_t rank;
+  int32_t dtype;
+  int32_t reserved;
+  const void* A;
+  const void* B;
+  const int32_t* ranks;
+  const float* scales;
+} qmv_lora;
+
+/* Beside a shared projection (res = its result, as from qmv_run): each token
+ * with its own adapter,
+ *   y[t] = res[t] + scales[a] * (B_a (A_a x[t])),  a = ids[t]
+ * ids int32 [n_tok]; a token whose id is negative has none (y = res), one whose id
+ * is n_adapters or more likewise and sets QMV_DEVERR_ADAPTER.  x fp32 [n_tok][K], res
+ * and y fp32 [n_tok][M] (y may be res).  All sums are fp32, in an order that
+ * depends on K, M and n_tok alone, so a token's result does not depend on the
+ * other tokens' adapters.  Each adapter in use is read once per four of its tokens.
+ * Constraints: K % 8 == 0, 8 <= K <= 2^20, 1 <= M <= 2^30, 1 <= n_tok <= 64.
+ * ws: qmv_lora_workspace_bytes bytes, any content.  Two launches. */
+size_t qmv_lora_workspace_bytes(const qmv_lora* l, int64_t K, int n_tok);
+int qmv_lora_run(const qmv_lora* l, const int32_t* ids, const float* x, const float* res, float* y, int64_t K,
+                 int64_t M, int n_tok, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Experts from router logits (moe_route_run's, or any [n_tok][E] in dtype, rows
+ * ld elements apart), with what it lacks: a bias for balance, groups, a scale,
+ * and batches as large as moe_qmv_prefill_run takes:
+ *   s = softmax(l) over all E, or 1 / (1 + exp(-l));   c = s + bias[e]
+ *   (bias fp32 [E], NULL: 0; it decides picks and never enters a gate)
+ *   groups of E / n_groups consecutive experts; a group's score is the sum of its
+ *   group_top (1 or 2) largest c; the keep groups of the largest score stay;
+ *   ids[t][0 .. top_k): the experts of the largest c among them, in decreasing
+ *   order; gates[t][k] = s of the pick, over the picks' sum if renorm (0 if that
+ *   is 0), times scale.
+ * Of equal values the lower index comes first, for groups and experts.  What is
+ * compared are the values of 64-bit arithmetic (without a bias experts are compared
+ * by their logits): fp32 decides where its errors cannot, and tokens with closer
+ * values are decided again in 64 bits.  A logit that is NaN counts as -inf, whose
+ * score is 0; +inf as the largest float; a bias of -inf (or NaN) puts an expert
+ * behind all others.  ids are distinct and in range whatever the logits.
+ * ids int32, gates fp32 [n_tok][top_k].  Constraints: 1 <= E <= 512, 1 <= n_groups
+ * <= 32 dividing E, 1 <= keep <= n_groups, group_top 1 or 2 and at most E / n_groups
+ * (not looked at with keep = n_groups), 1 <= top_k <= 8 and at most keep * E /
+ * n_groups, 1 <= n_tok <= QMV_MAX_PREFILL_TOKENS, ld >= E, scale finite. */
+int moe_route_select(int dtype, const void* logits, int64_t ld, const float* bias, int n_experts, int n_tok, int top_k,
+                     int gating, int n_groups, int keep, int group_top, int renorm, float scale, int32_t* ids,
+                     float* gates, cudaStream_t stream);
+
+/* Log probabilities of rows of logits [rows][V] (in dtype, rows ld elements
+ * apart, any alignment) under softmax(scale * l), scale being an inverse
+ * temperature:
+ *   lse[r] = log sum_i exp(scale * l_i);
+ *   logp[r][j] = scale * l_t - lse for the given tokens t = tokens[r][j];
+ *   entropy[r] = -sum_i p_i log p_i (nats);
+ *   top_ids[r][0 .. n_top): the tokens of the largest logits, larger first, of equal
+ *   ones the lower index first, and top_logp their log probabilities; tokens whose
+ *   logit is -inf or NaN are not listed (-1 and -inf after the last).
+ * tokens int32 [rows][n_given]: a negative one gives 0, one of V or more NaN and
+ * QMV_DEVERR_TOKEN.  A row of -inf alone has lse and logp -inf and entropy 0;
+ * a row with a NaN or +inf has NaN for lse, logp, entropy and top_logp.
+ * Results are fp32 (exponentials fp32, within 2^-21; sums of at most some
+ * hundreds of terms in a row before they are joined), and formed without the
+ * row's largest term: log probabilities near 0 and entropies near 0 keep their
+ * relative precision.  lse and entropy NULL where not wanted; logp and tokens go with n_given,
+ * top_ids and top_logp with n_top.  One launch, no workspace; results are bitwise
+ * reproducible.
+ * Constraints: 1 <= rows <= 2^24, 1 <= V <= 2^28, ld >= V, 0 <= n_given <=
+ * QMV_MAX_GIVEN, 0 <= n_top <= QMV_MAX_TOP, 0 < scale < inf, at least one result. */
+int qmv_logprobs(int dtype, const void* logits, int64_t ld, int64_t rows, int64_t V, float scale,
+                 const int32_t* tokens, int n_given, float* logp, float* lse, float* entropy, int n_top,
+                 int32_t* top_ids, float* top_logp, cudaStream_t stream);
 
 /* Diagnostic (no counterpart on the pages): the activation quantizer uses
  * branch-free FMA sequences for d = amax / 127 and 1 / d; this compares them

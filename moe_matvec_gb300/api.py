@@ -1,8 +1,9 @@
 """Python binding of the C-ABI library libqmv.so (see include/qmv.h).
 
 Argument marshalling only (ctypes; for the norm, cache, attention and page
-selection calls of a decode layer a native module, csrc/binding.cpp): every
-computation runs in the library's CUDA kernels.  Tensors are torch CUDA tensors (PyTorch supplies device memory and
+selection calls of a decode layer a native module, csrc/binding.cpp, and for
+rotation, adapters, expert selection and log probabilities another,
+csrc/binding_step.cpp): every computation runs in the library's CUDA kernels.  Tensors are torch CUDA tensors (PyTorch supplies device memory and
 the current stream); results are returned as new tensors unless `out` is
 given.  There is no CPU fallback: importing this module without a buildable
 library raises.
@@ -35,6 +36,8 @@ DEVERR_TIMEOUT = 0x4
 DEVERR_RANGE = 0x8
 DEVERR_PAGE = 0x10
 DEVERR_BATCH = 0x20
+DEVERR_ADAPTER = 0x40
+DEVERR_TOKEN = 0x80
 
 
 class QmvError(RuntimeError):
@@ -58,6 +61,18 @@ class KvBatch(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p),
                 ("n_seq", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_tok", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("freq", ctypes.c_void_p), ("axis", ctypes.c_void_p)]
+
+
+class Lora(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 _i64, _vp, _int, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -93,6 +108,14 @@ _SIGS = {
     "qmv_kv_select_workspace_bytes": (_sz, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch)]),
     "qmv_kv_select": (_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), _int, _vp, _i64, _int, _vp, _int,
                              _vp, _sz, _vp]),
+    "qmv_norm_rope": (_int, [ctypes.POINTER(Rope), _int, _vp, _i64, _vp, _i64, _int, _vp, _vp, _i64, _vp, _i64, _int,
+                             _vp, ctypes.c_float, _vp, _vp, _vp, _int, _int, _vp]),
+    "qmv_lora_workspace_bytes": (_sz, [ctypes.POINTER(Lora), _i64, _int]),
+    "qmv_lora_run": (_int, [ctypes.POINTER(Lora), _vp, _vp, _vp, _vp, _i64, _i64, _int, _vp, _sz, _vp]),
+    "moe_route_select": (_int, [_int, _vp, _i64, _vp, _int, _int, _int, _int, _int, _int, _int, _int, ctypes.c_float,
+                                _vp, _vp, _vp]),
+    "qmv_logprobs": (_int, [_int, _vp, _i64, _i64, _i64, ctypes.c_float, _vp, _int, _vp, _vp, _vp, _int, _vp, _vp,
+                            _vp]),
     "qmv_get_device_error": (_int, [_vp, ctypes.POINTER(_int)]),
     "qmv_debug_shrink_outputs": (_int, [_i64]),
     "qmv_wait_probe": (_int, [ctypes.c_longlong, _vp, _vp]),
@@ -105,13 +128,15 @@ _SIGS = {
 
 _lib = None
 _native = None  # the native module, driving _lib (None until a call needs it)
+_step = None    # the second one, likewise
 _NATIVE_CALLS = ("qmv_rms_norm", "qmv_dequantize_act", "qmv_kv_append", "qmv_kv_read", "qmv_kv_attend",
                  "qmv_kv_attend_workspace_bytes", "qmv_kv_select", "qmv_kv_select_workspace_bytes")
+_STEP_CALLS = ("qmv_norm_rope", "qmv_lora_run", "qmv_lora_workspace_bytes", "moe_route_select", "qmv_logprobs")
 
 
-def _bind():
-    """Point the native module at the active library."""
-    _native.bind(QmvError, *[ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS])
+def _bind(module, calls):
+    """Point a native module at the active library."""
+    module.bind(QmvError, *[ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in calls])
 
 
 def _activate(lib):
@@ -119,7 +144,9 @@ def _activate(lib):
     global _lib
     _lib = lib
     if _native is not None:
-        _bind()
+        _bind(_native, _NATIVE_CALLS)
+    if _step is not None:
+        _bind(_step, _STEP_CALLS)
     return lib
 
 
@@ -427,17 +454,21 @@ MAX_BATCH_TOKENS = 65535
 _WANT = {"float": 1, "q8": 2, "both": 3}
 
 
+def _native_module(name: str, calls):
+    load()
+    loader = importlib.machinery.ExtensionFileLoader(name, _build.build_binding(name))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+    loader.exec_module(module)
+    _bind(module, calls)
+    return module
+
+
 def _nat():
     """The native module, built and loaded by the first call that goes through it
     (the calls that go through ctypes need none of Python's and torch's headers)."""
     global _native
     if _native is None:
-        load()
-        loader = importlib.machinery.ExtensionFileLoader("_binding", _build.build_binding())
-        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
-        loader.exec_module(module)
-        _native = module
-        _bind()
+        _native = _native_module("_binding", _NATIVE_CALLS)
     return _native
 
 
@@ -551,6 +582,105 @@ def kv_select(cache: KvCache, q: torch.Tensor, table: torch.Tensor, lens: torch.
     int32 [n_tok][n_kv_heads][n_sel], ascending, -1 after the last; for kv_attend's pages.
     The cache must have bounds."""
     return _nat().kv_select(ctypes.addressof(cache), q, table, lens, starts, n_sel, ws, ids, _on(stream))
+
+
+# ---------------------------------------------------------------------------
+# The rest of a decode step: rotation, adapters, expert selection, log
+# probabilities
+# ---------------------------------------------------------------------------
+MAX_RANK = 128
+MAX_TOP = 32
+MAX_GIVEN = 64
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _stp():
+    """The second native module, as _nat."""
+    global _step
+    if _step is None:
+        _step = _native_module("_binding_step", _STEP_CALLS)
+    return _step
+
+
+def rope(head_dim: int, freq: torch.Tensor, axis: torch.Tensor | None = None, n_axes: int = 1,
+         interleaved: bool = False, scale: float = 1.0) -> Rope:
+    """How a model's heads turn (qmv_rope).  freq fp32 [R / 2]: radians a position of each
+    pair of the first R of head_dim values (pair i: values i and i + R / 2, or 2i and 2i + 1 if
+    interleaved); axis uint8 [R / 2]: which of a token's n_axes positions each pair goes by
+    (None: the first); scale multiplies the turned values.  It holds references to both
+    tensors."""
+    if freq.dim() != 1 or freq.dtype is not torch.float32:
+        raise ValueError(f"freq: torch.float32 [R / 2] wanted, got {freq.dtype} {tuple(freq.shape)}")
+    if axis is not None and (axis.dtype is not torch.uint8 or axis.shape != freq.shape):
+        raise ValueError(f"axis: torch.uint8 {tuple(freq.shape)} wanted, got {axis.dtype} {tuple(axis.shape)}")
+    r = Rope(int(head_dim), 2 * freq.numel(), int(interleaved), int(n_axes), float(scale), 0, _ptr(freq), _ptr(axis))
+    r._tensors = (freq, axis)
+    return r
+
+
+def norm_rope(rope: Rope, q: torch.Tensor, k: torch.Tensor | None = None, q_w: torch.Tensor | None = None,
+              k_w: torch.Tensor | None = None, eps: float = 1e-6, pos: torch.Tensor | None = None,
+              lens: torch.Tensor | None = None, starts: torch.Tensor | None = None,
+              q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Norm of each query and key head and its rotation (qmv_norm_rope).  q [n_tok][n_heads][D]
+    and k [n_tok][n_kv_heads][D] (tokens may be strided), q_w and k_w fp32 [D] (None: no norm).
+    Positions: pos int32 [n_tok][n_axes], or lens int32 [n_seq] and starts int32 [n_seq + 1] (None:
+    one token per sequence) as for kv_append.  q_out and k_out may be strided, and q and k
+    themselves.  Returns (q_out, k_out)."""
+    return _stp().norm_rope(ctypes.addressof(rope), q, k, q_w, k_w, eps, pos, lens, starts, q_out, k_out, _on(stream))
+
+
+def lora(A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor | None = None,
+         ranks: torch.Tensor | None = None) -> Lora:
+    """A pool of low-rank adapters of one projection (qmv_lora): A [n][rank][K] and B [n][M][rank]
+    of one float type, scales fp32 [n] (None: 1), ranks int32 [n] (None: rank; how many of an
+    adapter's rows of A and columns of B count).  It holds references to the tensors."""
+    if A.dtype not in _DTYPES or A.dim() != 3 or B.dim() != 3 or B.dtype is not A.dtype or \
+            (B.shape[0], B.shape[2]) != tuple(A.shape[:2]):
+        raise ValueError(f"A [n][rank][K] and B [n][M][rank] of one float type wanted, got {A.dtype} "
+                         f"{tuple(A.shape)} and {B.dtype} {tuple(B.shape)}")
+    n, rank, K = A.shape
+    for t, dt, what in ((scales, torch.float32, "scales"), (ranks, torch.int32, "ranks")):
+        if t is not None and (t.dtype is not dt or t.shape != (n,)):
+            raise ValueError(f"{what}: {dt} ({n},) wanted, got {t.dtype} {tuple(t.shape)}")
+    d = Lora(n, rank, _DTYPES[A.dtype], 0, _ptr(A), _ptr(B), _ptr(ranks), _ptr(scales))
+    d._tensors = (A, B, ranks, scales)
+    d.K, d.M = K, B.shape[1]
+    return d
+
+
+def lora_workspace_bytes(lora: Lora, n_tok: int) -> int:
+    return int(load().qmv_lora_workspace_bytes(ctypes.byref(lora), lora.K, int(n_tok)))
+
+
+def lora_run(lora: Lora, ids: torch.Tensor, x: torch.Tensor, r: torch.Tensor, out: torch.Tensor | None = None,
+             ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t] = r[t] + scale_a B_a (A_a x[t]) with a = ids[t], none for a negative id (qmv_lora_run):
+    adapters of many requests beside a shared projection whose result is r.  ids int32 [n_tok], x
+    fp32 [n_tok][K], r fp32 [n_tok][M]; out may be r."""
+    return _stp().lora_run(ctypes.addressof(lora), lora.K, lora.M, ids, x, r, out, ws, _on(stream))
+
+
+def route_select(logits: torch.Tensor, top_k: int, gating: int = GATING_SOFTMAX, bias: torch.Tensor | None = None,
+                 groups: int = 1, keep: int = 1, group_top: int = 2, renorm: bool = True, scale: float = 1.0,
+                 ids: torch.Tensor | None = None, gates: torch.Tensor | None = None, stream=None):
+    """Experts from router logits [n][E] (rows may be strided) (moe_route_select): scores by
+    gating, bias fp32 [E] added for the choice alone, the `keep` of `groups` groups with the
+    largest sum of their group_top best, top_k of those; gates are the picks' scores, over
+    their sum if renorm, times scale.  Returns (ids int32 [n][top_k], gates fp32 [n][top_k]) for
+    moe_run and moe_prefill_run."""
+    return _stp().route_select(logits, top_k, gating, bias, groups, keep, group_top, renorm, scale, ids, gates,
+                               _on(stream))
+
+
+def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, n_top: int = 0, scale: float = 1.0,
+             logp: torch.Tensor | None = None, lse: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+             ids: torch.Tensor | None = None, top: torch.Tensor | None = None, stream=None):
+    """Log probabilities under softmax(scale * logits) (qmv_logprobs).  logits [rows][V] (rows may
+    be strided), tokens int32 [rows][n] or None.  Returns (logp fp32 [rows][n] of the tokens, lse
+    and entropy fp32 [rows], ids int32 and top fp32 [rows][n_top]: the largest logits' tokens and
+    log probabilities), None for what was not asked for; each may be given as an output."""
+    return _stp().logprobs(logits, tokens, n_top, scale, logp, lse, entropy, ids, top, _on(stream))
 
 
 def check_rounding(stream=None):

@@ -4,9 +4,9 @@ Every .cu unit under csrc/ is compiled in parallel, then linked into
 moe_matvec_gb300/_build/libqmv.so.  Rebuilds only when a source is newer than
 the library.  build(debug=True) compiles the same sources with QMV_DEBUG (the
 kernels' software range checks, see qmv_debug_shrink_outputs in qmv.h) into
-moe_matvec_gb300/_build_debug/libqmv_debug.so.  build_binding() compiles the
-CPython binding (csrc/binding.cpp) against the installed PyTorch with g++ into
-moe_matvec_gb300/_build/_binding.so."""
+moe_matvec_gb300/_build_debug/libqmv_debug.so.  build_binding(name) compiles a
+CPython binding (csrc/binding.cpp, csrc/binding_step.cpp) against the installed
+PyTorch with g++ into moe_matvec_gb300/_build/<name>.so."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -91,32 +91,37 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
     return lib
 
 
-BINDING_SRC = os.path.join(CSRC, "binding.cpp")
-BINDING = os.path.join(BUILD, "_binding.so")
+BINDINGS = {"_binding": "binding.cpp", "_binding_step": "binding_step.cpp"}
 
 
-def build_binding(force: bool = False) -> str:
+def build_binding(name: str = "_binding", force: bool = False) -> str:
     import torch
     from torch.utils import cpp_extension
-    deps = [BINDING_SRC, os.path.join(ROOT, "include", "qmv.h"), torch.__file__]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
-        return BINDING
+    src, lib = os.path.join(CSRC, BINDINGS[name]), os.path.join(BUILD, name + ".so")
+    deps = [src, os.path.join(CSRC, "binding_util.h"), os.path.join(ROOT, "include", "qmv.h"), torch.__file__]
+    if not force and os.path.exists(lib) and all(os.path.getmtime(d) <= os.path.getmtime(lib) for d in deps):
+        return lib
     os.makedirs(BUILD, exist_ok=True)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     inc = [os.path.join(ROOT, "include"), *cpp_extension.include_paths(), os.path.join(cuda, "include"),
            sysconfig.get_paths()["include"]]
-    tmp = BINDING + f".{os.getpid()}.tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING_SRC, "-o", tmp]
+    tmp = lib + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-Wno-unused-function",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp]
     for d in inc:
         cmd += ["-isystem" if "torch" in d else "-I", d]
     cmd += ["-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
             "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stderr}")
+    os.replace(tmp, lib)
+    return lib
+
+
+def build_bindings() -> None:
+    with cf.ThreadPoolExecutor(max_workers=len(BINDINGS)) as ex:
+        list(ex.map(build_binding, BINDINGS))
 
 
 if __name__ == "__main__":
