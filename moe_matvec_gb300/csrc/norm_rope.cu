@@ -8,6 +8,8 @@ namespace qmv {
 
 constexpr int ROPE_WARPS = 4;         // warps of a CTA, each on its own
 constexpr int ROPE_MAX_PAIRS = 128;   // head_dim 256
+constexpr int ROPE_AHEAD = 2;
+constexpr int ROPE_CTAS = 5;          // CTAs an SM
 
 // cos and sin of pair i at position pos.  The turn pos * freq / (2 pi) is formed
 // and reduced to its fraction in 64 bits: in 32 a position of 131072 leaves 2^-7
@@ -20,69 +22,91 @@ __device__ __forceinline__ float2 turn_of(int pos, float freq, float scale) {
 }
 
 // y = x * w / sqrt(mean(x^2) + eps) (w given, else y = x), then each pair (a, b) of
-// the first R values becomes (a cos - b sin, a sin + b cos).
+// the first R values becomes (a cos - b sin, b cos + a sin).
 //
 // A head is D / (2 CH) units of two chunks of CH consecutive values, one unit a
 // lane (UL units for CH = 1): the two halves of CH pairs (pair i: values i and
 // i + R / 2), or 2 CH consecutive values (pair i: 2i, 2i + 1), or two chunks
 // that do not turn.  So a lane holds whole pairs, the norm is a sum over the
-// head's lanes, and the same lane has the same pairs in every head: its cosines
-// and sines stay in registers while the warp goes through the token's heads,
-// 32 / (lanes of a head) at a time.  The warp's lanes share out the token's angles
-// (64 bits, the only costly arithmetic) through shared memory; meanwhile the first
-// heads are on their way.
+// head's lanes, and the same lane has the same pairs in every head: the products
+// of its cosines and sines with the weights stay in registers while the warp goes
+// through the token's heads, 32 / (lanes of a head) at a time, the next ones on
+// their way.  The warp's lanes share out the token's angles (64 bits, the only
+// costly arithmetic) through shared memory; meanwhile the first heads travel.
 //
 // Bound by HBM for many tokens.
 template <int DT, int CH, int UL, bool INTER>
-__global__ void __launch_bounds__(32 * ROPE_WARPS) norm_rope_kernel(const RopeParams p, int lph_log, int split) {
+__global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
+    norm_rope_kernel(const RopeParams p, int lph_log, int split) {
   using T = typename Elem<DT>::type;
-  struct alignas(CH * sizeof(T) < 16 ? CH * sizeof(T) : 16) Chunk {
-    T v[CH];
-  };
-  constexpr int PF = UL == 1 ? 4 : 1;  // head groups on their way at once
+  using Chunk = Packed<T, CH>;
+  constexpr int PF = UL == 1 ? ROPE_AHEAD : 1;  // head groups on their way
   __shared__ float2 turns[ROPE_WARPS][ROPE_MAX_PAIRS];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const long long item = (long long)blockIdx.x * ROPE_WARPS + wid;
-  const long long t = item / split;
+  const unsigned item = blockIdx.x * ROPE_WARPS + wid;
+  const unsigned t = item / (unsigned)split;
   const int part = (int)(item - t * split);
-  if (t >= p.n_tok) return;
+  if (t >= (unsigned)p.n_tok) return;
   const int hpw = 32 >> lph_log, li = lane & ((1 << lph_log) - 1), sub = lane >> lph_log;
   const int units = p.D / (2 * CH), turning = p.R / (2 * CH);
-  const int q_steps = (p.q.n + hpw - 1) / hpw, steps = q_steps + (p.k.n + hpw - 1) / hpw;
-  const int s0 = (int)((long long)steps * part / split), s1 = (int)((long long)steps * (part + 1) / split);
-  // the two chunks of the lane's unit i
+  const int q_steps = (p.q.n + hpw - 1) >> (5 - lph_log), steps = q_steps + ((p.k.n + hpw - 1) >> (5 - lph_log));
+  const int s0 = steps * part / split, s1 = steps * (part + 1) / split;
+  // the lane's unit i, and the places of its two chunks in a head
   auto unit = [&](int i) { return li + (i << lph_log); };
-  auto places = [&](int u, int& a, int& b) {
+  int pa[UL], pb[UL];
+#pragma unroll
+  for (int i = 0; i < UL; i++) {
+    const int u = unit(i);
     if (INTER || u >= turning) {
-      a = u * 2 * CH;
-      b = a + CH;
+      pa[i] = u * 2 * CH;
+      pb[i] = pa[i] + CH;
     } else {
-      a = u * CH;
-      b = p.R / 2 + a;
+      pa[i] = u * CH;
+      pb[i] = p.R / 2 + pa[i];
+    }
+  }
+  // The token's head groups in order, queries first: the lane's head of a group
+  // (x) and how many heads there are from the group's first on.
+  struct Cursor {
+    T* x;
+    int left;
+  };
+  auto group = [&](int s, bool out) {
+    const bool keys = s >= q_steps;
+    const RopeHeads& h = keys ? p.k : p.q;
+    const int head = (keys ? s - q_steps : s) * hpw;
+    T* x = out ? static_cast<T*>(h.y) + t * h.ys : const_cast<T*>(static_cast<const T*>(h.x)) + t * h.xs;
+    return Cursor{x + (head + sub) * p.D, h.n - head};
+  };
+  auto advance = [&](Cursor& c, int s, bool out) {  // from group s - 1 to s
+    if (s == q_steps) {
+      c = group(s, out);
+    } else {
+      c.x += hpw * p.D;
+      c.left -= hpw;
     }
   };
   Chunk ra[PF][UL], rb[PF][UL];
-  auto fetch = [&](int s, Chunk(&xa)[UL], Chunk(&xb)[UL]) {
-    const RopeHeads& h = s < q_steps ? p.q : p.k;
-    const int head = (s < q_steps ? s : s - q_steps) * hpw + sub;
+  Cursor in = group(s0, false), out = group(s0, true);
+  int ahead = s0;
+  auto fetch = [&](Chunk(&xa)[UL], Chunk(&xb)[UL]) {
 #pragma unroll
     for (int i = 0; i < UL; i++) {
-#pragma unroll
-      for (int j = 0; j < CH; j++) from_float(0.f, xa[i].v[j]), from_float(0.f, xb[i].v[j]);
-      int a, b;
-      places(unit(i), a, b);
-      const long long at = t * h.xs + (long long)head * p.D;
-      if (s < s1 && head < h.n && unit(i) < units && QMV_CHECK(in_range(at + a, CH, h.x_len, p.err)) &&
-          QMV_CHECK(in_range(at + b, CH, h.x_len, p.err))) {
-        xa[i] = *reinterpret_cast<const Chunk*>(static_cast<const T*>(h.x) + at + a);
-        xb[i] = *reinterpret_cast<const Chunk*>(static_cast<const T*>(h.x) + at + b);
+      xa[i].clear();
+      xb[i].clear();
+      QMV_DEBUG_ONLY(const RopeHeads& h = ahead < q_steps ? p.q : p.k; const long long at = in.x - static_cast<const T*>(h.x);)
+      if (ahead < s1 && sub < in.left && unit(i) < units && QMV_CHECK(in_range(at + pa[i], CH, h.x_len, p.err)) &&
+          QMV_CHECK(in_range(at + pb[i], CH, h.x_len, p.err))) {
+        xa[i].load(in.x + pa[i]);
+        xb[i].load(in.x + pb[i]);
       }
     }
+    advance(in, ++ahead, false);
   };
 #pragma unroll
-  for (int k = 0; k < PF; k++) fetch(s0 + k, ra[k], rb[k]);
+  for (int k = 0; k < PF; k++) fetch(ra[k], rb[k]);
 
   int pos = 0;
   if (!p.pos) {
@@ -94,7 +118,7 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS) norm_rope_kernel(const RopePa
     }
     const int len = p.lens[seq];
     if (a < 0 || b < a || b > p.n_tok || len < 0) set_error(p.err, QMV_DEVERR_BATCH);
-    if (t < a || t >= b) return;  // no sequence's token (the whole warp)
+    if ((int)t < a || (int)t >= b) return;  // no sequence's token (the whole warp)
     pos = (int)((long long)max(len, 0) - b + t);
   }
   for (int i = lane; i < p.R / 2; i += 32) {
@@ -105,98 +129,97 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS) norm_rope_kernel(const RopePa
         set_error(p.err, QMV_DEVERR_BATCH);
         ax = 0;
       }
-      at = p.pos[t * p.n_axes + ax];
+      at = p.pos[(long long)t * p.n_axes + ax];
     }
     turns[wid][i] = turn_of(at, p.freq[i], p.scale);
   }
   __syncwarp();
-  float co[UL][CH], si[UL][CH];
+  // Pair (a, b) becomes rstd (a ca - b sb, b cb + a sa): cosines and sines times the
+  // weights of a and b.
+  constexpr int NP = UL * CH;
+  float ca[NP], sa[NP], cb[NP], sb[NP];
+  auto factors = [&](const float* w) {
 #pragma unroll
-  for (int i = 0; i < UL; i++)
+    for (int i = 0; i < UL; i++)
 #pragma unroll
-    for (int j = 0; j < CH; j++) {
-      const bool turns_here = unit(i) < turning;
-      const float2 cs = turns[wid][turns_here ? unit(i) * CH + j : 0];
-      co[i][j] = turns_here ? cs.x : 1.f;
-      si[i][j] = turns_here ? cs.y : 0.f;
-    }
-  float wa[UL][CH], wb[UL][CH];
-  const float* w_held = nullptr;
+      for (int j = 0; j < CH; j++) {
+        const bool turn = unit(i) < turning;
+        const float2 cs = turn ? turns[wid][unit(i) * CH + j] : make_float2(1.f, 0.f);
+        float wa = 1.f, wb = 1.f;
+        if (w && unit(i) < units) {
+          // (values 2j and 2j + 1 of the unit where pairs are neighbours)
+          const bool next = INTER && turn;
+          wa = w[next ? pa[i] + 2 * j : pa[i] + j];
+          wb = w[next ? pa[i] + 2 * j + 1 : pb[i] + j];
+        }
+        ca[i * CH + j] = cs.x * wa, sa[i * CH + j] = cs.y * wa;
+        cb[i * CH + j] = cs.x * wb, sb[i * CH + j] = cs.y * wb;
+      }
+  };
+  factors(s0 < q_steps ? p.q.w : p.k.w);
   const float inv_d = 1.0f / (float)p.D;
   for (int s = s0; s < s1; s += PF) {
-    if (s > s0) {
-#pragma unroll
-      for (int k = 0; k < PF; k++) fetch(s + k, ra[k], rb[k]);
-    }
 #pragma unroll
     for (int k = 0; k < PF; k++) {
       if (s + k >= s1) break;
-      const RopeHeads& h = s + k < q_steps ? p.q : p.k;
-      const int head = (s + k < q_steps ? s + k : s + k - q_steps) * hpw + sub;
-      float va[UL][CH], vb[UL][CH];
+      if (s + k == q_steps && s + k > s0) factors(p.k.w);  // from queries to keys
+      const bool norm = (s + k < q_steps ? p.q.w : p.k.w) != nullptr;
+      float va[NP], vb[NP];
 #pragma unroll
-      for (int i = 0; i < UL; i++)
+      for (int i = 0; i < UL; i++) {
+        float xa[CH], xb[CH];
+        ra[k][i].to(xa);
+        rb[k][i].to(xb);
 #pragma unroll
-        for (int j = 0; j < CH; j++) {
-          va[i][j] = to_float(ra[k][i].v[j]);
-          vb[i][j] = to_float(rb[k][i].v[j]);
+        for (int j = 0; j < CH; j++) va[i * CH + j] = xa[j], vb[i * CH + j] = xb[j];
+      }
+      fetch(ra[k], rb[k]);
+      float rstd = 1.f;
+      if (norm) {
+        float sum = 0.f, other = 0.f;
+#pragma unroll
+        for (int i = 0; i < NP; i++) {
+          sum = fmaf(va[i], va[i], sum);
+          other = fmaf(vb[i], vb[i], other);
         }
-      if (h.w) {
-        if (h.w != w_held) {  // queries' weights, then keys'
-          w_held = h.w;
-#pragma unroll
-          for (int i = 0; i < UL; i++) {
-            int a, b;
-            places(unit(i), a, b);
-#pragma unroll
-            for (int j = 0; j < CH; j++) {
-              wa[i][j] = unit(i) < units ? h.w[a + j] : 0.f;
-              wb[i][j] = unit(i) < units ? h.w[b + j] : 0.f;
-            }
-          }
-        }
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < UL; i++)
-#pragma unroll
-          for (int j = 0; j < CH; j++) sum = fmaf(va[i][j], va[i][j], fmaf(vb[i][j], vb[i][j], sum));
+        sum += other;
         for (int o = 1; o < 1 << lph_log; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float rstd = rsqrtf(fmaf(sum, inv_d, p.eps));  // at most 2 units in the last place off
-#pragma unroll
-        for (int i = 0; i < UL; i++)
-#pragma unroll
-          for (int j = 0; j < CH; j++) {
-            va[i][j] = (va[i][j] * rstd) * wa[i][j];
-            vb[i][j] = (vb[i][j] * rstd) * wb[i][j];
-          }
+        rstd = rsqrtf(fmaf(sum, inv_d, p.eps));  // at most 2 units in the last place off
       }
 #pragma unroll
       for (int i = 0; i < UL; i++) {
+        if (INTER && CH > 1 && unit(i) < turning) {  // from neighbours to pairs
+          float x[2 * CH];
+#pragma unroll
+          for (int j = 0; j < CH; j++) x[j] = va[i * CH + j], x[CH + j] = vb[i * CH + j];
+#pragma unroll
+          for (int j = 0; j < CH; j++) va[i * CH + j] = x[2 * j], vb[i * CH + j] = x[2 * j + 1];
+        }
         Chunk oa, ob;
+        float ya[CH], yb[CH];
 #pragma unroll
         for (int j = 0; j < CH; j++) {
-          if (INTER && CH > 1) {  // pairs 0 .. CH / 2 of the unit lie in the first chunk
-            if (j % 2 == 0) {
-              const float c = co[i][j / 2], n = si[i][j / 2], c2 = co[i][(CH + j) / 2], n2 = si[i][(CH + j) / 2];
-              from_float(va[i][j] * c - va[i][j + 1] * n, oa.v[j]);
-              from_float(va[i][j + 1] * c + va[i][j] * n, oa.v[j + 1]);
-              from_float(vb[i][j] * c2 - vb[i][j + 1] * n2, ob.v[j]);
-              from_float(vb[i][j + 1] * c2 + vb[i][j] * n2, ob.v[j + 1]);
-            }
-          } else {
-            from_float(va[i][j] * co[i][j] - vb[i][j] * si[i][j], oa.v[j]);
-            from_float(vb[i][j] * co[i][j] + va[i][j] * si[i][j], ob.v[j]);
-          }
+          const int e = i * CH + j;
+          ya[j] = rstd * (va[e] * ca[e] - vb[e] * sb[e]);
+          yb[j] = rstd * (vb[e] * cb[e] + va[e] * sa[e]);
         }
-        int a, b;
-        places(unit(i), a, b);
-        const long long at = t * h.ys + (long long)head * p.D;
-        if (head < h.n && unit(i) < units && QMV_CHECK(in_range(at + a, CH, h.y_len, p.err)) &&
-            QMV_CHECK(in_range(at + b, CH, h.y_len, p.err))) {
-          *reinterpret_cast<Chunk*>(static_cast<T*>(h.y) + at + a) = oa;
-          *reinterpret_cast<Chunk*>(static_cast<T*>(h.y) + at + b) = ob;
+        if (INTER && CH > 1 && unit(i) < turning) {
+          float x[2 * CH];
+#pragma unroll
+          for (int j = 0; j < CH; j++) x[2 * j] = ya[j], x[2 * j + 1] = yb[j];
+#pragma unroll
+          for (int j = 0; j < CH; j++) ya[j] = x[j], yb[j] = x[CH + j];
+        }
+        oa.from(ya);
+        ob.from(yb);
+        QMV_DEBUG_ONLY(const RopeHeads& h = s + k < q_steps ? p.q : p.k; const long long at = out.x - static_cast<const T*>(h.y);)
+        if (sub < out.left && unit(i) < units && QMV_CHECK(in_range(at + pa[i], CH, h.y_len, p.err)) &&
+            QMV_CHECK(in_range(at + pb[i], CH, h.y_len, p.err))) {
+          oa.store(out.x + pa[i]);
+          ob.store(out.x + pb[i]);
         }
       }
+      advance(out, s + k + 1, true);
     }
   }
 }
