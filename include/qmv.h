@@ -663,7 +663,7 @@ typedef struct qmv_lora {
  * ids int32 [n_tok]; a token whose id is negative has none (y = res), one whose id
  * is n_adapters or more likewise and sets QMV_DEVERR_ADAPTER.  x fp32 [n_tok][K], res
  * and y fp32 [n_tok][M] (y may be res).  All sums are fp32, in an order that
- * depends on K, M and n_tok alone, so a token's result does not depend on the
+ * depends on K, n_tok and the pool's rank alone, so a token's result does not depend on the
  * other tokens' adapters.  Each adapter in use is read once per four of its tokens.
  * Constraints: K % 8 == 0, 8 <= K <= 2^20, 1 <= M <= 2^30, 1 <= n_tok <= 64.
  * ws: qmv_lora_workspace_bytes bytes, any content.  Two launches. */
@@ -684,8 +684,8 @@ int qmv_lora_run(const qmv_lora* l, const int32_t* ids, const float* x, const fl
  * Of equal values the lower index comes first, for groups and experts.  What is
  * compared are the values of 64-bit arithmetic (without a bias experts are compared
  * by their logits): fp32 decides where its errors cannot, and tokens with closer
- * values are decided again in 64 bits.  A logit that is NaN counts as -inf, whose
- * score is 0; +inf as the largest float; a bias of -inf (or NaN) puts an expert
+ * values are decided again in 64 bits.  A logit or bias that is NaN counts as -inf, +inf as
+ * the largest float; a logit of -inf has the score 0, a bias of -inf puts an expert
  * behind all others.  ids are distinct and in range whatever the logits.
  * ids int32, gates fp32 [n_tok][top_k].  Constraints: 1 <= E <= 512, 1 <= n_groups
  * <= 32 dividing E, 1 <= keep <= n_groups, group_top 1 or 2 and at most E / n_groups

@@ -9,10 +9,10 @@
 
 namespace qmv {
 
-constexpr int LP_THREADS = 512, LP_WARPS = LP_THREADS / 32;
 constexpr int LP_UNROLL = 4;        // 16-byte loads of a thread on their way
 constexpr int LP_MAX_CLUSTER = 8;
-constexpr int LP_CAND = 2048;       // candidates for the top list that shared memory holds
+constexpr int LP_SEGS = 16;         // stretches of a thread's loads whose largest logit is kept
+constexpr int LP_CAND = 1024;       // candidates for the top list that shared memory holds
 // The smallest exponent (of 2) that matters; also what exp2 of a masked logit takes,
 // so that 0 * -inf never enters a sum.
 constexpr float LP_LOWEST = -1.0e4f;
@@ -75,16 +75,36 @@ struct LogitVec {
     const uint32_t w = DT == QMV_DT_F32 ? 0xff800000u : DT == QMV_DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
     raw = make_uint4(w, w, w, w);
   }
-  __device__ __forceinline__ float largest() const {
+};
+
+// The largest of some vectors' logits (NaN left out).
+template <int DT, int U>
+__device__ __forceinline__ float largest(const LogitVec<DT> (&x)[U]) {
+  if constexpr (DT == QMV_DT_F32) {
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < N / 2; i++) {
-      const float2 v = pair(i);
-      m = fmaxf(m, fmaxf(v.x, v.y));
-    }
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        const float2 v = x[u].pair(i);
+        m = fmaxf(m, fmaxf(v.x, v.y));
+      }
     return m;
+  } else {
+    using Two = typename std::conditional<DT == QMV_DT_BF16, __nv_bfloat162, __half2>::type;
+    Two m;
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const uint32_t w[4] = {x[u].raw.x, x[u].raw.y, x[u].raw.z, x[u].raw.w};
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const Two v = *reinterpret_cast<const Two*>(&w[i]);
+        m = u + i ? __hmax2(m, v) : v;
+      }
+    }
+    return fmaxf(fmaxf(to_float(m.x), to_float(m.y)), -INFINITY);  // (both NaN: -inf)
   }
-};
+}
 
 __device__ __forceinline__ unsigned long long candidate(float v, int at) {  // larger first, then the lower index
   v += 0.0f;  // (-0 as 0)
@@ -97,57 +117,64 @@ __device__ __forceinline__ float value_of(unsigned long long c) {
 }
 __device__ __forceinline__ int index_of(unsigned long long c) { return (int)(0xffffffffu - (uint32_t)c); }
 
-// What a CTA knows of its part of a row: its largest logit M, and over its other
-// logits s = sum 2^d and t = sum 2^d d with d = (l - M) k, k = scale / ln 2.  The
+// What a warp knows of its part of a row: its largest logit m, and over its other
+// logits s = sum 2^d and t = sum 2^d d with d = (l - m) k, k = scale / ln 2.  The
 // largest one itself (2^0) is left out, so that a row that is nearly certain keeps
-// the digits of what is left: log-sum-exp = scale M + log1p(s).
+// the digits of what is left: log-sum-exp = scale m + log1p(s).
 struct LpPart {
-  float M, s, t;
-  int n;  // entries of its list
+  float m, s, t;  // m -inf: no logit above -inf (s and t are 0, or NaN)
 };
 
-// A cluster a row, each CTA a run of its 16-byte vectors; a thread takes every 512th.
+__device__ __forceinline__ uint32_t peer(const void* here, int rank) {  // the same place in another CTA of the cluster
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(here)), "r"(rank));
+  return at;
+}
+
+// A cluster a row, each CTA a run of its 16-byte vectors; a thread takes every NT-th.
 //
 // One pass over the logits: sums of 2^d and 2^d d relative to the warp's largest
-// logit so far (when that grows, both are rescaled), and each thread's largest.
-// Then a little of the row is read again from L2: the thread that met the CTA's
-// largest has its sums formed anew without that one (above), and the top list's
-// candidates are taken from the threads whose largest reaches a floor that at least
-// n_top threads reach: the q-th largest among the warps' r-th largest thread maxima,
-// q r >= n_top.  Every logit of the list is at least that floor and is met by such a
-// thread.  Candidates are ordered by (value, index), so no order of arrival shows;
-// where they overflow shared memory (many equal logits) the list is found entry
-// by entry, each by a pass of its own.
+// logit so far, that one left out (when it grows, both are rescaled and the former
+// one joins them), and the largest of each stretch of each thread's loads.  For the
+// top list a little of the row is then read again from L2: the stretches whose
+// largest reaches a floor that at least n_top threads reach, the q-th largest among all
+// warps' r-th largest thread maxima, q r >= n_top.  Every logit of the list is at least
+// that floor and lies in such a stretch.  These candidates are ordered by (value,
+// index), so no order of arrival shows; where they overflow shared memory (many equal
+// logits) the list is found entry by entry, each by a pass of its own.
 //
 // Bound by HBM for many rows: about 6 instructions a logit.
-template <int DT>
-__global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const LogprobsParams p, int ranks) {
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobsParams p, int ranks) {
   using Vec = LogitVec<DT>;
   using T = typename Vec::T;
-  constexpr int N = Vec::N;
-  __shared__ unsigned long long cand[LP_CAND];
-  __shared__ unsigned long long lists[LP_MAX_CLUSTER][QMV_MAX_TOP];
-  __shared__ LpPart parts[LP_MAX_CLUSTER];
-  __shared__ float w_max[LP_WARPS], w_floor[LP_WARPS], w_s[LP_WARPS], w_t[LP_WARPS];
-  __shared__ int w_owner[LP_WARPS];
-  __shared__ int n_cand;
-  __shared__ unsigned long long w_best[LP_WARPS];
+  constexpr int N = Vec::N, WARPS = NT / 32, MAX_PARTS = (NT == 512 ? LP_MAX_CLUSTER : 1) * WARPS;
+  __shared__ unsigned long long cand[LP_CAND];     // the first CTA's: the row's
+  __shared__ float seg_max[LP_SEGS][NT];
+  __shared__ LpPart parts[MAX_PARTS];              // the first CTA's: all warps'
+  __shared__ float reach[MAX_PARTS];               // all warps' r-th largest thread maxima
+  __shared__ int n_cand, n_again, again[NT];
+  __shared__ float s_floor;
+  __shared__ unsigned long long w_best[WARPS];
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = ranks > 1 ? blockIdx.x % ranks : 0;
-  const long long r = blockIdx.x / ranks;
-  if (tid == 0) n_cand = 0;
+  const long long r = ranks > 1 ? blockIdx.x / ranks : blockIdx.x;
+  const int n_parts = ranks * WARPS;
+  if (tid == 0) n_cand = n_again = 0;
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
-  if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const T* row = static_cast<const T*>(p.logits) + r * p.ld;
-  // vectors of 16 aligned bytes; the first may begin before the row
+  // vectors of 16 aligned bytes; the first may begin before the row, the last end after it
   const int shift = (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(T);
   const int n_vec = (int)((p.V + shift + N - 1) / N);
   const int v0 = (int)((long long)n_vec * rank / ranks), v1 = (int)((long long)n_vec * (rank + 1) / ranks);
-  auto load = [&](int v) {
+  const int whole0 = max(v0, shift > 0), whole1 = min(v1, (p.V + shift) / N);  // whole ones of the CTA
+  // vector v of the row if it lies before `end`
+  auto load = [&](int v, int end) {
     Vec x;
     x.mask();
-    if (v < v1) {
+    if (v < end) {
       const int e = v * N - shift;
       if (e >= 0 && e + N <= p.V) {
         if (QMV_CHECK(in_range(r * p.ld + e, N, p.logits_len, p.err))) x.raw = __ldg(reinterpret_cast<const uint4*>(row + e));
@@ -172,203 +199,192 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const LogprobsP
   }
 
   const float k = p.scale * 1.4426950408889634f;
-  float m = -FLT_MAX, mine = -INFINITY;
+  const F2 k2 = F2::of(k, k);
+  float m = -FLT_MAX, mine = -INFINITY, stretch = -INFINITY;
+  bool out = false;  // the warp's largest is left out of the sums
   F2 S = F2::of(0.f, 0.f), D = S;
-  for (int v = v0 + tid; v - lane < v1; v += LP_THREADS * LP_UNROLL) {
+  constexpr int STEP = NT * LP_UNROLL;
+  const int steps = (v1 - v0 + STEP - 1) / STEP, per_seg = (steps + LP_SEGS - 1) / LP_SEGS;
+  int seg = 0, in_seg = 0;
+  for (int v = v0 + tid; v - tid < v1; v += STEP) {
     Vec x[LP_UNROLL];
+    const int w = v - lane;  // the warp's first
+    if (w >= whole0 && w + NT * (LP_UNROLL - 1) + 32 <= whole1 &&
+        QMV_CHECK(in_range(r * p.ld + (long long)v * N - shift, (long long)NT * (LP_UNROLL - 1) * N + N, p.logits_len, p.err))) {
+      const uint4* at = reinterpret_cast<const uint4*>(row + (v * N - shift));
 #pragma unroll
-    for (int u = 0; u < LP_UNROLL; u++) x[u] = load(v + u * LP_THREADS);
-    float bm = x[0].largest();
+      for (int u = 0; u < LP_UNROLL; u++) x[u].raw = __ldg(at + u * NT);
+    } else {
 #pragma unroll
-    for (int u = 1; u < LP_UNROLL; u++) bm = fmaxf(bm, x[u].largest());
+      for (int u = 0; u < LP_UNROLL; u++) x[u] = load(v + u * NT, v1);
+    }
+    const float bm = largest(x);
     mine = fmaxf(mine, bm);
-    if (__any_sync(0xffffffffu, bm > m)) {
-      const float now = fmaxf(m, warp_max(bm)), d = fmaxf((m - now) * k, LP_LOWEST), f = ex2(d);
-      const F2 f2 = F2::of(f, f);
+    stretch = fmaxf(stretch, bm);
+    if (++in_seg == per_seg) {
+      seg_max[seg][tid] = stretch;
+      seg++;
+      in_seg = 0;
+      stretch = -INFINITY;
+    }
+    const unsigned above = __ballot_sync(0xffffffffu, bm > m || (!out && bm == m));
+    if (above) {
+      const float now = warp_max(bm), d = fmaxf((m - now) * k, LP_LOWEST), f = ex2(d);
+      const F2 f2 = F2::of(f, f), was = F2::of(out && lane == 0 ? 1.f : 0.f, 0.f);
+      // the former largest joins the sums (d is 0 for it)
+      S = S + was;
       D = f2 * fma2(F2::of(d, d), S, D);
       S = f2 * S;
       m = now;
+      out = true;
+      bool leave = lane == __ffs(__ballot_sync(0xffffffffu, bm == now)) - 1;
+#pragma unroll
+      for (int u = 0; u < LP_UNROLL; u++)
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+          const float2 two = x[u].pair(i / 2);
+          const float l = i & 1 ? two.y : two.x;
+          const float dl = at_least((l - m) * k, LP_LOWEST);
+          const bool skip = leave && l == m;
+          leave &= !skip;
+          const float e = skip ? 0.f : ex2(dl);
+          S = S + F2::of(e, 0.f);
+          D = fma2(F2::of(e, 0.f), F2::of(dl, 0.f), D);
+        }
+    } else {
+      const F2 m2 = F2::of(-m, -m);
+#pragma unroll
+      for (int u = 0; u < LP_UNROLL; u++)
+#pragma unroll
+        for (int i = 0; i < N / 2; i++) {
+          const float2 l = x[u].pair(i);
+          F2 d = (F2::of(l.x, l.y) + m2) * k2;
+          d = F2::of(at_least(d.x(), LP_LOWEST), at_least(d.y(), LP_LOWEST));
+          const F2 e = F2::of(ex2(d.x()), ex2(d.y()));
+          S = S + e;
+          D = fma2(e, d, D);
+        }
     }
-    const F2 m2 = F2::of(-m, -m), k2 = F2::of(k, k);
-#pragma unroll
-    for (int u = 0; u < LP_UNROLL; u++)
-#pragma unroll
-      for (int i = 0; i < N / 2; i++) {
-        const float2 l = x[u].pair(i);
-        F2 d = (F2::of(l.x, l.y) + m2) * k2;
-        d = F2::of(at_least(d.x(), LP_LOWEST), at_least(d.y(), LP_LOWEST));
-        const F2 e = F2::of(ex2(d.x()), ex2(d.y()));
-        S = S + e;
-        D = fma2(e, d, D);
-      }
   }
+  if (in_seg) seg_max[seg][tid] = stretch;
 
-  // the warp's largest thread maximum and its r-th
-  const int n_top = p.n_top, nr = (n_top + 7) / 8, nq = nr ? (n_top + nr - 1) / nr : 0;
-  {
-    float left = mine;
-    for (int i = 0; i < max(nr, 1); i++) {
-      const float w = warp_max(left);
-      const int from = __ffs(__ballot_sync(0xffffffffu, left == w)) - 1;
-      if (lane == 0) {
-        if (i == 0) w_max[warp] = w, w_owner[warp] = from;
-        w_floor[warp] = w;
-      }
-      if (lane == from) left = -INFINITY;
-    }
-  }
-  __syncthreads();
-  float M = lane < LP_WARPS ? w_max[lane] : -INFINITY;
-  const float all = warp_max(M);
-  const int owner_warp = __ffs(__ballot_sync(0xffffffffu, M == all)) - 1;
-  M = all;
-  const bool owner = warp == owner_warp && lane == w_owner[warp];
-  float floor = INFINITY;
-  if (n_top) {
-    float left = lane < LP_WARPS ? w_floor[lane] : -INFINITY;
-    for (int i = 0; i < nq; i++) {
-      floor = warp_max(left);
-      const int from = __ffs(__ballot_sync(0xffffffffu, left == floor)) - 1;
-      if (lane == from) left = -INFINITY;
-    }
-  }
-  // the sums relative to M, without the owner's
-  float s = 0.f, t = 0.f;
-  if (!owner || !(mine > -INFINITY)) {
-    const float d = fmaxf((m - fmaxf(M, -FLT_MAX)) * k, LP_LOWEST), f = ex2(d);
-    s = f * (S.x() + S.y());
-    t = f * (D.x() + D.y()) + d * s;
-  }
-  // some threads' logits again
-  unsigned again = __ballot_sync(0xffffffffu, (owner || mine >= floor) && mine > -INFINITY);
-  while (again) {
-    const int from = __ffs(again) - 1;
-    again &= again - 1;
-    const bool sums = warp == owner_warp && from == w_owner[warp];
-    int equal = 0;
-    for (int v = v0 + warp * 32 + from + lane * LP_THREADS; v < v1; v += 32 * LP_THREADS) {
-      const Vec x = load(v);
-#pragma unroll
-      for (int i = 0; i < N; i++) {
-        const float2 two = x.pair(i / 2);
-        const float l = i & 1 ? two.y : two.x;
-        if (l >= floor && l > -INFINITY) {
-          const int at = atomicAdd(&n_cand, 1);
-          if (at < LP_CAND) cand[at] = candidate(l, v * N - shift + i);
-        }
-        if (sums) {
-          if (l == M) equal++;
-          else {
-            const float d = at_least((l - M) * k, LP_LOWEST), e = ex2(d);
-            s += e;
-            t = fmaf(e, d, t);
-          }
-        }
-      }
-    }
-    if (sums) {  // all but one of those that equal it
-      equal = __reduce_add_sync(0xffffffffu, equal) - 1;
-      if (lane == 0) s += (float)equal;
-    }
-  }
+  const int n_top = p.n_top;
+  const int nr = (2 * n_top + n_parts - 1) / n_parts, nq = nr ? (n_top + nr - 1) / nr : 0;  // (n_parts is at least 8)
+  float s = S.x() + S.y(), t = D.x() + D.y();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
     t += __shfl_xor_sync(0xffffffffu, t, o);
   }
-  if (lane == 0) {
-    w_s[warp] = s;
-    w_t[warp] = t;
-  }
-  __syncthreads();
-  // the CTA's list, largest first
-  int have = min(n_cand, n_top);
-  if (n_cand <= LP_CAND) {
-    for (int i = tid; i < n_cand; i += LP_THREADS) {
-      const unsigned long long c = cand[i];
-      int before = 0;
-      for (int j = 0; j < n_cand; j++) before += cand[j] > c;
-      if (before < n_top) lists[0][before] = c;
-    }
-  } else {
-    unsigned long long last = ~0ull;
-    have = 0;
-    for (int i = 0; i < n_top; i++) {
-      unsigned long long best = 0;
-      for (int v = v0 + tid; v < v1; v += LP_THREADS) {
-        const Vec x = load(v);
-#pragma unroll
-        for (int j = 0; j < N; j++) {
-          const float2 two = x.pair(j / 2);
-          const float l = j & 1 ? two.y : two.x;
-          const unsigned long long c = l > -INFINITY ? candidate(l, v * N - shift + j) : 0;
-          if (c < last && c > best) best = c;
-        }
-      }
-      for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-      __syncthreads();  // (the last entry's values are read)
-      if (lane == 0) w_best[warp] = best;
-      __syncthreads();
-      for (int j = 0; j < LP_WARPS; j++) best = max(best, w_best[j]);
-      if (!best) break;
-      if (tid == 0) lists[0][i] = best;
-      last = best;
-      have = i + 1;
+  float rth = -INFINITY;
+  {
+    float left = mine;
+    for (int i = 0; i < nr; i++) {
+      rth = warp_max(left);
+      if (i + 1 < nr && lane == __ffs(__ballot_sync(0xffffffffu, left == rth)) - 1) left = -INFINITY;
     }
   }
-  LpPart part;
-  if (warp == 0) {
-    s = lane < LP_WARPS ? w_s[lane] : 0.f;
-    t = lane < LP_WARPS ? w_t[lane] : 0.f;
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
-    part = LpPart{M, s, t, have};
-  }
-  __syncthreads();
+  const LpPart part{out ? m : -INFINITY, s, t};
+  const int me = rank * WARPS + warp;
   if (ranks > 1) {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    if (rank > 0) {
-      uint32_t to;
-      if (tid < have) {
-        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_u32(&lists[rank][tid])));
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(lists[0][tid]) : "memory");
-      }
-      if (tid == 0) {
-        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_u32(&parts[rank])));
-        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(__float_as_uint(part.M)),
-                     "r"(__float_as_uint(part.s)), "r"(__float_as_uint(part.t)), "r"(part.n)
-                     : "memory");
-      }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all CTAs are there
+    if (lane < ranks && n_top)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer(&reach[me], lane)), "f"(rth) : "memory");
+    if (lane == 0) {
+      const uint32_t to = peer(&parts[me], 0);
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(part.m) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4), "f"(part.s) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8), "f"(part.t) : "memory");
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (rank > 0) return;
-  }
-  if (tid == 0) parts[0] = part;
-  __syncthreads();
-  // the row's M, s and t, in the CTAs' order, by every thread
-  float top = parts[0].M;
-  for (int i = 1; i < ranks; i++) top = fmaxf(top, parts[i].M);
-  float rs = 0.f, rt = 0.f;
-  bool left_out = false;  // the one that is left out of s
-  for (int i = 0; i < ranks; i++) {
-    const LpPart q = parts[i];
-    if (!(q.M > -INFINITY)) {
-      rs += q.s, rt += q.t;  // 0, or NaN
-      continue;
+    if (rank > 0 && !n_top) return;
+  } else {
+    if (lane == 0) {
+      reach[me] = rth;
+      parts[me] = part;
     }
-    if (q.M == top && !left_out) {
-      left_out = true;
-      rs += q.s;
+    __syncthreads();
+  }
+  if (n_top) {
+    // the floor: the nq-th largest of all warps' values (one of equal ones before the next)
+    if (tid < n_parts) {
+      const float v = reach[tid];
+      int before = 0;
+#pragma unroll 8
+      for (int i = 0; i < n_parts; i++) before += reach[i] > v || (reach[i] == v && i < tid);
+      if (before == nq - 1) s_floor = v;
+    }
+    __syncthreads();
+    const float floor = s_floor;
+    // the stretches that reach it
+    if (mine >= floor && mine > -INFINITY)
+      for (int i = 0; i * per_seg < steps; i++)
+        if (seg_max[i][tid] >= floor) {
+          const int at = atomicAdd(&n_again, 1);
+          if (at < NT) again[at] = i * NT + tid;
+        }
+    __syncthreads();
+    const bool all = n_again > NT;  // too many to list: everything again
+    const int loads = per_seg * LP_UNROLL, items = all ? v1 - v0 : n_again * loads;
+    const uint32_t counter = peer(&n_cand, 0);
+    for (int i = tid; i < items; i += NT) {
+      int v = v0 + i;
+      if (!all) {
+        const int which = i / loads, of = again[which], first = of / NT * per_seg * STEP;
+        v = v0 + first + of % NT + (i - which * loads) * NT;
+      }
+      const Vec x = load(v, v1);
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        const float2 two = x.pair(j / 2);
+        const float l = j & 1 ? two.y : two.x;
+        if (l >= floor && l > -INFINITY) {
+          const unsigned long long c = candidate(l, v * N - shift + j);
+          int at;
+          if (ranks > 1) {
+            asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(counter) : "memory");
+            if (at < LP_CAND) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(peer(&cand[at], 0)), "l"(c) : "memory");
+          } else {
+            at = atomicAdd(&n_cand, 1);
+            if (at < LP_CAND) cand[at] = c;
+          }
+        }
+      }
+    }
+    if (ranks > 1) {
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      if (rank > 0) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        return;
+      }
+    }
+  }
+
+  // The row's largest, s and t: the warps' in a fixed order, by every warp.
+  float top = -INFINITY;
+  for (int i = lane; i < n_parts; i += 32) top = fmaxf(top, parts[i].m);
+  top = warp_max(top);
+  int owner = n_parts;  // the warp whose largest stays out of s
+  for (int i = lane; i < n_parts; i += 32)
+    if (parts[i].m == top) owner = min(owner, i);
+  owner = __reduce_min_sync(0xffffffffu, owner);
+  float rs = 0.f, rt = 0.f;
+  for (int i = lane; i < n_parts; i += 32) {
+    const LpPart q = parts[i];
+    if (i == owner || !(q.m > -INFINITY)) {
+      rs += q.s;  // (0 or NaN where there is no logit)
       rt += q.t;
     } else {
-      const float d = at_least((q.M - top) * k, LP_LOWEST), f = ex2(d);
+      const float d = at_least((q.m - top) * k, LP_LOWEST), f = ex2(d);
       rs += f * (1.0f + q.s);
       rt += f * (q.t + d * (1.0f + q.s));
     }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    rs += __shfl_xor_sync(0xffffffffu, rs, o);
+    rt += __shfl_xor_sync(0xffffffffu, rt, o);
   }
   if (top == INFINITY) rs = NAN;
   const bool none = !(top > -INFINITY) && rs == rs;  // every logit is -inf
@@ -382,54 +398,70 @@ __global__ void __launch_bounds__(LP_THREADS, 2) logprobs_kernel(const LogprobsP
   }
   if (tid < p.n_given && QMV_CHECK(in_range(r * p.n_given + tid, 1, p.given_len, p.err)))
     p.logp[r * p.n_given + tid] = token < 0 ? 0.f : token >= p.V ? NAN : logp(given);
-  if (n_top) {
-    // entry i of list j: as many before it as in its own list and, by a search, in the others
-    for (int e = tid; e < ranks * n_top; e += LP_THREADS) {
-      const int j = e / n_top, i = e - j * n_top;
-      if (i >= parts[j].n) continue;
-      const unsigned long long c = lists[j][i];
-      int before = i;
-      for (int o = 0; o < ranks; o++) {
-        if (o == j) continue;
-        int lo = 0, hi = parts[o].n;
-        while (lo < hi) {
-          const int mid = (lo + hi) / 2;
-          if (lists[o][mid] > c) lo = mid + 1;
-          else hi = mid;
-        }
-        before += lo;
-      }
-      if (before < n_top && QMV_CHECK(in_range(r * n_top + before, 1, p.top_len, p.err))) {
-        p.top_ids[r * n_top + before] = index_of(c);
-        p.top_logp[r * n_top + before] = logp(value_of(c));
+  if (!n_top) return;
+  if (ranks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else __syncthreads();
+  auto list = [&](int at, unsigned long long c) {
+    if (QMV_CHECK(in_range(r * n_top + at, 1, p.top_len, p.err))) {
+      p.top_ids[r * n_top + at] = c ? index_of(c) : -1;
+      p.top_logp[r * n_top + at] = c ? logp(value_of(c)) : -INFINITY;
+    }
+  };
+  const int n = n_cand;
+  if (n <= LP_CAND) {
+    for (int i = warp; i < n; i += WARPS) {
+      const unsigned long long c = cand[i];
+      int before = 0;
+      for (int j = 0; j < n; j += 32) before += __popc(__ballot_sync(0xffffffffu, j + lane < n && cand[j + lane] > c));
+      if (lane == 0 && before < n_top) list(before, c);
+    }
+    for (int i = n + tid; i < n_top; i += NT) list(i, 0);
+    return;
+  }
+  unsigned long long last = ~0ull;
+  for (int i = 0; i < n_top; i++) {
+    unsigned long long best = 0;
+    for (int v = tid; v < n_vec; v += NT) {
+      const Vec x = load(v, n_vec);
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        const float2 two = x.pair(j / 2);
+        const float l = j & 1 ? two.y : two.x;
+        const unsigned long long c = l > -INFINITY ? candidate(l, v * N - shift + j) : 0;
+        if (c < last && c > best) best = c;
       }
     }
-    int total = 0;
-    for (int i = 0; i < ranks; i++) total += parts[i].n;
-    for (int e = total + tid; e < n_top; e += LP_THREADS)
-      if (QMV_CHECK(in_range(r * n_top + e, 1, p.top_len, p.err))) {
-        p.top_ids[r * n_top + e] = -1;
-        p.top_logp[r * n_top + e] = -INFINITY;
-      }
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    __syncthreads();  // (the last entry's values are read)
+    if (lane == 0) w_best[warp] = best;
+    __syncthreads();
+    for (int j = 0; j < WARPS; j++) best = max(best, w_best[j]);
+    if (tid == 0) list(i, best);
+    last = best;
   }
 }
 
-template <int DT>
-static cudaError_t launch_dt(const LogprobsParams& p, cudaStream_t stream) {
-  // Few rows: a cluster each, while all of them still fit the GPU twice over and a
-  // CTA keeps a round of loads of its own.
-  const int round = LP_THREADS * LP_UNROLL * LogitVec<DT>::N / 2;
-  int ranks = 1;
-  while (ranks < LP_MAX_CLUSTER && p.rows * ranks <= device_sm_count() && p.V > (long long)ranks * round) ranks *= 2;
+template <int DT, int NT>
+static cudaError_t launch_as(const LogprobsParams& p, int ranks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  make_config(cfg, attr, dim3((unsigned)(p.rows * ranks)), dim3(LP_THREADS), 0, stream, true);
+  make_config(cfg, attr, dim3((unsigned)(p.rows * ranks)), dim3(NT), 0, stream, true);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = ranks;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = ranks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<DT>, p, ranks);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, NT>, p, ranks);
+}
+
+template <int DT>
+static cudaError_t launch_dt(const LogprobsParams& p, cudaStream_t stream) {
+  // Few rows: a cluster each, while all of them still fit the GPU and a CTA keeps a
+  // round of loads of its own.
+  const int round = 512 * LP_UNROLL * LogitVec<DT>::N / 2;
+  int ranks = 1;
+  while (ranks < LP_MAX_CLUSTER && p.rows * ranks <= device_sm_count() && p.V > (long long)ranks * round) ranks *= 2;
+  return ranks > 1 ? launch_as<DT, 512>(p, ranks, stream) : launch_as<DT, 256>(p, ranks, stream);
 }
 
 cudaError_t launch_logprobs(int dtype, const LogprobsParams& p, cudaStream_t stream) {

@@ -6,141 +6,201 @@
 
 namespace qmv {
 
-constexpr int LORA_WARPS = 8, LORA_THREADS = 32 * LORA_WARPS;
+constexpr int LORA_WARPS = 4, LORA_THREADS = 32 * LORA_WARPS;
+constexpr int LORA_CTAS = 4;     // CTAs an SM
 constexpr int LORA_TOK = 4;      // tokens of one adapter that a CTA takes
 constexpr int LORA_COLS = 8;     // consecutive columns a lane
 constexpr int LORA_WIN = 32 * LORA_COLS;
 constexpr int LORA_ROWS = 4;     // rows of A a warp holds sums for
 constexpr int LORA_SMS = 152;    // what the splits of the columns are made for (on any device: they decide the sums' order)
 
-// The tokens of one CTA: up to LORA_TOK of those with token t's adapter, from t
-// on; n = 0 where another CTA (an earlier token's) has t among its own.
+// The tokens of one CTA: up to LORA_TOK with the same adapter, and what part of
+// their work is its own.  The tokens of each adapter (and those without one) form
+// groups of LORA_TOK in their order; the call's CTAs are dealt out to the groups,
+// which only the device knows.
 struct LoraTokens {
-  int a;  // the adapter, -1: none
-  int n;
+  int a;             // the adapter, -1: none
+  int n;             // 0: nothing left for this CTA
+  int part, parts;   // this CTA's part of its group's work
   int tok[LORA_TOK];
 };
-// (two loads a lane: ids, as every warp of a CTA comes by them)
-__device__ __forceinline__ LoraTokens lora_tokens(const LoraParams& p, int t) {
+// (every warp of a CTA comes by them alone: a lane has tokens `lane` and `lane` + 32)
+__device__ __forceinline__ LoraTokens lora_tokens(const LoraParams& p) {
   const int lane = threadIdx.x & 31;
-  int id[2];
+  int id[2], before[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 2; i++) {
     const int k = lane + 32 * i;
     id[i] = k < p.n_tok ? __ldcg(p.ids + k) : -2;
     if (k < p.n_tok && (id[i] < 0 || id[i] >= p.n)) {
-      if (id[i] >= p.n && k == t) set_error(p.err, QMV_DEVERR_ADAPTER);
+      if (id[i] >= p.n && blockIdx.x == 0) set_error(p.err, QMV_DEVERR_ADAPTER);
       id[i] = -1;
     }
   }
+  const int low = min(p.n_tok, 32);
+  for (int j = 0; j < low; j++) {  // tokens of the same adapter before the lane's
+    const int other = __shfl_sync(0xffffffffu, id[0], j);
+    before[0] += other == id[0] && j < lane;
+    before[1] += other == id[1];
+  }
+  for (int j = 32; j < p.n_tok; j++) before[1] += __shfl_sync(0xffffffffu, id[1], j - 32) == id[1] && j < lane + 32;
+  const unsigned lead0 = __ballot_sync(0xffffffffu, lane < p.n_tok && before[0] % LORA_TOK == 0);
+  const unsigned lead1 = __ballot_sync(0xffffffffu, lane + 32 < p.n_tok && before[1] % LORA_TOK == 0);
+  const int first = __popc(lead0), groups = first + __popc(lead1);
+  const int g = (int)blockIdx.x % groups;
+  // the group's first token: the g-th of those that lead one
+  const unsigned below = (1u << lane) - 1;
+  const unsigned at0 = __ballot_sync(0xffffffffu, (lead0 >> lane & 1) && __popc(lead0 & below) == g);
+  const unsigned at1 = __ballot_sync(0xffffffffu, (lead1 >> lane & 1) && first + __popc(lead1 & below) == g);
+  const int t = at0 ? __ffs(at0) - 1 : __ffs(at1) + 31;
   LoraTokens q;
   q.a = __shfl_sync(0xffffffffu, t < 32 ? id[0] : id[1], t & 31);
+  q.part = (int)blockIdx.x / groups;
+  q.parts = (int)gridDim.x / groups;
   unsigned long long same = (unsigned long long)__ballot_sync(0xffffffffu, id[1] == q.a) << 32 |
                             __ballot_sync(0xffffffffu, id[0] == q.a);
-  q.n = 0;
-  if (__popcll(same & ((1ull << t) - 1)) % LORA_TOK) return q;
   same &= ~0ull << t;
+  q.n = 0;
 #pragma unroll
   for (int i = 0; i < LORA_TOK; i++) {
     q.tok[i] = same ? __ffsll(same) - 1 : t;
     if (same) q.n = i + 1;
     same &= same - 1;
   }
+  if (q.part >= q.parts) q.n = 0;
   return q;
 }
 __device__ __forceinline__ int rank_of(const LoraParams& p, int a) {
   return p.ranks ? min(max(__ldcg(p.ranks + a), 0), p.r) : p.r;
 }
 
-// v = A x over one split of the columns: part[split][token][row].  A warp takes
-// four rows; a lane has 8 columns of each window of 256, the next window's rows on
-// their way while one is worked on.  The four rows' sums for up to four tokens are
-// added over the lanes together (16 shuffles for 16 sums).  x of the CTA's tokens
-// lies in shared memory.  Adapter rows are read once per four of its tokens.
-template <int DT>
-__global__ void __launch_bounds__(LORA_THREADS, 2) lora_down_kernel(const LoraParams p) {
+// v = A x: part[split][token][row], each over one split of the columns.  The work
+// of a group of tokens is (split, four rows) units; a CTA takes a run of rows of one
+// split, a warp every fourth unit of it, and a lane has 8 columns of each window of
+// 256.  The next windows' rows are on their way while one is worked on, across
+// units.  The four rows' sums for up to four tokens are added over the lanes
+// together (16 shuffles for 16 sums).  x of the CTA's tokens lies in shared memory.
+// Adapter rows are read once per four of its tokens.
+template <int DT, int NT>
+__device__ __forceinline__ void lora_down(const LoraParams& p, const LoraTokens& q, float* lora_x) {
   using T = typename Elem<DT>::type;
   using Row = Packed<T, LORA_COLS>;
+  constexpr int AHEAD = DT == QMV_DT_F32 ? 1 : 2;  // windows on their way: 4 KB a warp
+  constexpr int SUMS = LORA_ROWS * NT;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = rank_of(p, q.a);
+  // this CTA's split of the columns and run of units
+  const int split = q.part % p.splits, nth = q.part / p.splits, of = q.parts / p.splits;
+  const int units = (rank + LORA_ROWS - 1) / LORA_ROWS;
+  const int u0 = units * nth / of, u1 = units * (nth + 1) / of;
+  if (nth >= of || u0 == u1) return;
+  const int c0 = split * p.window, cols = min(p.window, p.K - c0), wins = (cols + LORA_WIN - 1) / LORA_WIN;
+  const T* A = static_cast<const T*>(p.A) + (long long)q.a * p.r * p.K + c0 + lane * LORA_COLS;
+  Row w[AHEAD][LORA_ROWS];
+  // The loads go through (unit, window) in order, AHEAD of the sums.
+  int next_unit = u0 + warp, next_win = 0;
+  const T* next = A + (long long)next_unit * LORA_ROWS * p.K;
+  auto fetch = [&](Row& x, int i) {  // row i of the next unit's next window
+    x.clear();
+    if (next_unit < u1 && next_unit * LORA_ROWS + i < rank && next_win * LORA_WIN + lane * LORA_COLS < cols &&
+        QMV_CHECK(in_range(next + (long long)i * p.K - static_cast<const T*>(p.A), LORA_COLS, p.a_len, p.err)))
+      x.load(next + (long long)i * p.K);
+  };
+  auto advance = [&]() {
+    next += LORA_WIN;
+    if (++next_win == wins) {
+      next_win = 0;
+      next_unit += LORA_WARPS;
+      next = A + (long long)next_unit * LORA_ROWS * p.K;
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < AHEAD; u++) {
+#pragma unroll
+    for (int i = 0; i < LORA_ROWS; i++) fetch(w[u][i], i);
+    advance();
+  }
+  for (int i = 4 * tid; i < p.window; i += 4 * LORA_THREADS)
+#pragma unroll
+    for (int k = 0; k < NT; k++)
+      if (k < q.n)
+        *reinterpret_cast<float4*>(lora_x + k * p.window + i) =
+            i < cols ? *reinterpret_cast<const float4*>(p.x + (long long)q.tok[k] * p.K + c0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  int win = 0, unit = u0 + warp;
+  float acc[LORA_ROWS][NT];
+#pragma unroll
+  for (int i = 0; i < LORA_ROWS; i++)
+#pragma unroll
+    for (int k = 0; k < NT; k++) acc[i][k] = 0.f;
+  while (unit < u1) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; u++) {
+      if (unit >= u1) break;
+      float x[NT][LORA_COLS];
+#pragma unroll
+      for (int k = 0; k < NT; k++)
+        load_vec<LORA_COLS>(lora_x + (k < q.n ? k : 0) * p.window + win * LORA_WIN + lane * LORA_COLS, x[k]);
+#pragma unroll
+      for (int i = 0; i < LORA_ROWS; i++) {
+        float v[LORA_COLS];
+        w[u][i].to(v);
+        fetch(w[u][i], i);
+#pragma unroll
+        for (int k = 0; k < NT; k++)
+#pragma unroll
+          for (int e = 0; e < LORA_COLS; e++) acc[i][k] = fmaf(v[e], x[k][e], acc[i][k]);
+      }
+      advance();
+      if (++win < wins) continue;
+      // The unit's sums over the lanes, by lane bits 3, 2, 1, 0, 4 (one order for any
+      // number of sums): halves the sums that a lane holds at each step, down to one.
+      float* s = &acc[0][0];
+      int have = SUMS;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        if (have > 1) {
+          have /= 2;
+          const bool up = lane & o;
+#pragma unroll
+          for (int i = 0; i < SUMS / 2; i++)
+            if (i < have) {
+              const float give = up ? s[i] : s[i + have], keep = up ? s[i + have] : s[i];
+              s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+        } else {
+          s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+        }
+      }
+      s[0] += __shfl_xor_sync(0xffffffffu, s[0], 16);
+      constexpr int SHARE = 16 / SUMS;  // lanes that end with the same sum
+      const int at = (lane & 15) / SHARE, j = unit * LORA_ROWS + at / NT, k = at % NT;
+      int tok = q.tok[0];
+#pragma unroll
+      for (int i = 1; i < NT; i++)
+        if (i == k) tok = q.tok[i];
+      if (lane < 16 && lane % SHARE == 0 && j < rank && k < q.n) p.part[((long long)split * p.n_tok + tok) * p.r + j] = s[0];
+      win = 0;
+      unit += LORA_WARPS;
+#pragma unroll
+      for (int i = 0; i < LORA_ROWS; i++)
+#pragma unroll
+        for (int k2 = 0; k2 < NT; k2++) acc[i][k2] = 0.f;
+    }
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_down_kernel(const LoraParams p) {
   extern __shared__ __align__(16) float lora_x[];  // [LORA_TOK][window]
   // The second kernel may start (and read the adapters' other half) once what came
   // before this call is done.
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const LoraTokens q = lora_tokens(p, blockIdx.y);
+  const LoraTokens q = lora_tokens(p);
   if (q.n == 0 || q.a < 0) return;
-  const int rank = rank_of(p, q.a);
-  const int c0 = blockIdx.x * p.window, c1 = min(c0 + p.window, p.K);
-  const T* A = static_cast<const T*>(p.A) + (long long)q.a * p.r * p.K;
-  constexpr int AHEAD = DT == QMV_DT_F32 ? 1 : 2;  // windows on their way: 4 KB a warp
-  Row w[AHEAD][LORA_ROWS];
-  auto fetch = [&](Row& x, int j, int c) {
-    x.clear();
-    if (j < rank && c < c1 && QMV_CHECK(in_range(((long long)q.a * p.r + j) * p.K + c, LORA_COLS, p.a_len, p.err)))
-      x.load(A + (long long)j * p.K + c);
-  };
-  auto begin = [&](int j0) {
-#pragma unroll
-    for (int u = 0; u < AHEAD; u++)
-#pragma unroll
-      for (int i = 0; i < LORA_ROWS; i++) fetch(w[u][i], j0 + i, c0 + lane * LORA_COLS + u * LORA_WIN);
-  };
-  begin(warp * LORA_ROWS);
-  for (int i = 4 * tid; i < p.window; i += 4 * LORA_THREADS)
-#pragma unroll
-    for (int k = 0; k < LORA_TOK; k++)
-      if (k < q.n)
-        *reinterpret_cast<float4*>(lora_x + k * p.window + i) =
-            c0 + i < p.K ? *reinterpret_cast<const float4*>(p.x + (long long)q.tok[k] * p.K + c0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-  __syncthreads();
-  for (int j0 = warp * LORA_ROWS; j0 < rank; j0 += LORA_WARPS * LORA_ROWS) {
-    if (j0 != warp * LORA_ROWS) begin(j0);
-    float acc[LORA_ROWS][LORA_TOK];
-#pragma unroll
-    for (int i = 0; i < LORA_ROWS; i++)
-#pragma unroll
-      for (int k = 0; k < LORA_TOK; k++) acc[i][k] = 0.f;
-    for (int base = c0; base < c1; base += AHEAD * LORA_WIN) {
-#pragma unroll
-      for (int u = 0; u < AHEAD; u++) {
-        const int c = base + u * LORA_WIN + lane * LORA_COLS;
-        if (base + u * LORA_WIN >= c1) break;
-        float x[LORA_TOK][LORA_COLS];
-#pragma unroll
-        for (int k = 0; k < LORA_TOK; k++)
-          if (k < q.n) load_vec<LORA_COLS>(lora_x + k * p.window + c - c0, x[k]);
-#pragma unroll
-        for (int i = 0; i < LORA_ROWS; i++) {
-          float v[LORA_COLS];
-          w[u][i].to(v);
-          fetch(w[u][i], j0 + i, c + AHEAD * LORA_WIN);
-#pragma unroll
-          for (int k = 0; k < LORA_TOK; k++)
-            if (k < q.n)
-#pragma unroll
-              for (int e = 0; e < LORA_COLS; e++) acc[i][k] = fmaf(v[e], x[k][e], acc[i][k]);
-        }
-      }
-    }
-    // sum `lane` % 16 of the 16 over the lanes: halves the sums a lane holds at each step
-    float* s = &acc[0][0];
-#pragma unroll
-    for (int o = LORA_ROWS * LORA_TOK / 2; o > 0; o >>= 1) {
-      const bool up = lane & o;
-#pragma unroll
-      for (int i = 0; i < o; i++) {
-        const float give = up ? s[i] : s[i + o], keep = up ? s[i + o] : s[i];
-        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-      }
-    }
-    s[0] += __shfl_xor_sync(0xffffffffu, s[0], LORA_ROWS * LORA_TOK);
-    const int j = j0 + lane / LORA_TOK, k = lane % LORA_TOK;
-    int tok = q.tok[0];
-#pragma unroll
-    for (int i = 1; i < LORA_TOK; i++)
-      if (i == k) tok = q.tok[i];
-    if (lane < LORA_ROWS * LORA_TOK && j < rank && k < q.n) p.part[((long long)blockIdx.x * p.n_tok + tok) * p.r + j] = s[0];
-  }
+  if (q.n == 1) lora_down<DT, 1>(p, q, lora_x);
+  else lora_down<DT, LORA_TOK>(p, q, lora_x);
 }
 
 // y = res + scale B v: v's parts are added in order, then each warp goes through
@@ -149,142 +209,169 @@ __global__ void __launch_bounds__(LORA_THREADS, 2) lora_down_kernel(const LoraPa
 // values each; the partial sums of `gather` loads are added over those lanes
 // together, so that afterwards each lane has one row's sum and up to 32 consecutive
 // rows of y and res are read and written at once.
-template <int DT, int VW, int LPR_LOG>
-__global__ void __launch_bounds__(LORA_THREADS, 2) lora_up_kernel(const LoraParams p, int rows_per_warp) {
+template <int DT, int VW, int LPR_LOG, int NT>
+__device__ __forceinline__ void lora_up(const LoraParams& p, const LoraTokens& q, float (&v)[LORA_TOK][QMV_MAX_RANK],
+                                        long long m0, int rows) {
   using T = typename Elem<DT>::type;
   using Row = Packed<T, VW>;
   constexpr int LPR = 1 << LPR_LOG, RPL = 32 >> LPR_LOG;               // lanes a row, rows a load
   constexpr int GATHER_LOG = LPR_LOG < 3 ? LPR_LOG : 3, GATHER = 1 << GATHER_LOG;
   constexpr int LOADS = 8, BLOCK = GATHER * RPL;                       // rows whose sums are gathered at once
-  __shared__ float v[LORA_TOK][QMV_MAX_RANK];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long first = ((long long)blockIdx.x * LORA_WARPS + warp) * rows_per_warp;
-  const long long m0 = min(first, p.M), m1 = min(first + rows_per_warp, p.M);
-  pdl_launch_dependents();
-  const LoraTokens q = lora_tokens(p, blockIdx.y);
-  if (q.n == 0) return;  // (another CTA has these rows of the token)
-  if (q.a < 0) {         // no adapter
-    pdl_wait();
-    if (p.y != p.res)
-      for (int k = 0; k < q.n; k++)
-        for (long long m = m0 + lane; m < m1; m += 32)
-          if (QMV_CHECK(in_range(q.tok[k] * p.M + m, 1, p.y_len, p.err))) p.y[q.tok[k] * p.M + m] = p.res[q.tok[k] * p.M + m];
-    return;
-  }
+  const int tid = threadIdx.x, lane = tid & 31;
   const int rank = rank_of(p, q.a);
   const int li = lane & (LPR - 1), j0 = li * VW, sub = lane >> LPR_LOG;
-  const T* B = static_cast<const T*>(p.B) + (long long)q.a * p.M * p.r + j0;
+  const bool ragged = rank % VW != 0;  // a lane's values may end at the rank
+  const T* B = static_cast<const T*>(p.B) + ((long long)q.a * p.M + m0 + sub) * p.r + j0;
+  // rows that the lane may load: none past its adapter's rank
+  const int live = j0 < rank ? rows - sub : 0, step = RPL * p.r;
   Row w[LOADS];
-  auto fetch = [&](Row& x, long long m) {
+  auto fetch = [&](Row& x, const T* at, int m) {
     x.clear();
-    if (m < m1 && j0 < rank && QMV_CHECK(in_range(((long long)q.a * p.M + m) * p.r + j0, VW, p.b_len, p.err)))
-      x.load(B + m * p.r);
+    if (m < live && QMV_CHECK(in_range(at - static_cast<const T*>(p.B), VW, p.b_len, p.err))) x.load(at);
   };
 #pragma unroll
-  for (int i = 0; i < LOADS; i++) fetch(w[i], m0 + i * RPL + sub);
+  for (int i = 0; i < LOADS; i++) fetch(w[i], B + i * step, i * RPL);
   const float scale = p.scales ? __ldcg(p.scales + q.a) : 1.0f;
   pdl_wait();
-  for (int i = tid; i < LORA_TOK * p.r; i += LORA_THREADS) {
+  for (int i = tid; i < NT * p.r; i += LORA_THREADS) {
     const int k = i / p.r, j = i - k * p.r;
     float sum = 0.f;
     if (k < q.n && j < rank) {
       int tok = q.tok[0];
 #pragma unroll
-      for (int o = 1; o < LORA_TOK; o++)
+      for (int o = 1; o < NT; o++)
         if (o == k) tok = q.tok[o];
       const float* part = p.part + (long long)tok * p.r + j;
-      const long long step = (long long)p.n_tok * p.r;
+      const int stride = p.n_tok * p.r;
 #pragma unroll 8
-      for (int s = 0; s < p.splits; s++) sum += __ldcg(part + s * step);
+      for (int s = 0; s < p.splits; s++) sum += __ldcg(part + (long long)s * stride);
     }
     v[k][j] = sum * scale;
   }
   __syncthreads();
-  float x[LORA_TOK][VW];
+  float x[NT][VW];
 #pragma unroll
-  for (int k = 0; k < LORA_TOK; k++)
+  for (int k = 0; k < NT; k++)
 #pragma unroll
     for (int e = 0; e < VW; e++) x[k][e] = j0 + e < rank && k < q.n ? v[k][j0 + e] : 0.f;
   // the row of a block whose sum ends up here
-  const int mine = GATHER == 1 ? sub : (li & (GATHER - 1)) * RPL + sub;
+  const int mine = (li & (GATHER - 1)) * RPL + sub;
   const bool writer = LPR <= GATHER || li < GATHER;
-  for (long long m = m0; m < m1; m += LOADS * RPL) {
+  const float* res[NT];
+  float* y[NT];
+#pragma unroll
+  for (int k = 0; k < NT; k++) {
+    res[k] = p.res + q.tok[k] * p.M + m0 + mine;
+    y[k] = p.y + q.tok[k] * p.M + m0 + mine;
+  }
+  for (int m = 0; m < rows; m += LOADS * RPL) {
+    B += LOADS * step;
 #pragma unroll
     for (int g = 0; g < LOADS / GATHER; g++) {
-      float acc[LORA_TOK][GATHER], res[LORA_TOK];
-      const long long row = m + g * BLOCK + mine;
+      float acc[NT][GATHER], r[NT];
+      const int row = m + g * BLOCK;
+      const bool here = writer && row + mine < rows;
 #pragma unroll
-      for (int k = 0; k < LORA_TOK; k++) res[k] = k < q.n && writer && row < m1 ? p.res[q.tok[k] * p.M + row] : 0.f;
+      for (int k = 0; k < NT; k++) r[k] = here && k < q.n ? res[k][row] : 0.f;
 #pragma unroll
       for (int i = 0; i < GATHER; i++) {
         float b[VW];
         w[g * GATHER + i].to(b);
-        fetch(w[g * GATHER + i], m + (LOADS + g * GATHER + i) * RPL + sub);
-        if (j0 + VW > rank) {
+        fetch(w[g * GATHER + i], B + (g * GATHER + i) * step, m + (LOADS + g * GATHER + i) * RPL);
+        if (ragged) {
 #pragma unroll
           for (int e = 0; e < VW; e++)
             if (j0 + e >= rank) b[e] = 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < LORA_TOK; k++) {
+        for (int k = 0; k < NT; k++) {
           acc[k][i] = 0.f;
-          if (k < q.n)
 #pragma unroll
-            for (int e = 0; e < VW; e++) acc[k][i] = fmaf(b[e], x[k][e], acc[k][i]);
+          for (int e = 0; e < VW; e++) acc[k][i] = fmaf(b[e], x[k][e], acc[k][i]);
         }
       }
 #pragma unroll
-      for (int k = 0; k < LORA_TOK; k++) {
-        if (k < q.n) {
+      for (int k = 0; k < NT; k++) {
 #pragma unroll
-          for (int o = GATHER / 2; o > 0; o >>= 1) {
-            const bool up = li & o;
+        for (int o = GATHER / 2; o > 0; o >>= 1) {
+          const bool up = li & o;
 #pragma unroll
-            for (int i = 0; i < o; i++) {
-              const float give = up ? acc[k][i] : acc[k][i + o], keep = up ? acc[k][i + o] : acc[k][i];
-              acc[k][i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-            }
+          for (int i = 0; i < o; i++) {
+            const float give = up ? acc[k][i] : acc[k][i + o], keep = up ? acc[k][i + o] : acc[k][i];
+            acc[k][i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
           }
-#pragma unroll
-          for (int o = GATHER; o < LPR; o <<= 1) acc[k][0] += __shfl_xor_sync(0xffffffffu, acc[k][0], o);
-          const long long at = q.tok[k] * p.M + row;
-          if (writer && row < m1 && QMV_CHECK(in_range(at, 1, p.y_len, p.err))) p.y[at] = res[k] + acc[k][0];
         }
+#pragma unroll
+        for (int o = GATHER; o < LPR; o <<= 1) acc[k][0] += __shfl_xor_sync(0xffffffffu, acc[k][0], o);
+        if (here && k < q.n && QMV_CHECK(in_range(y[k] + row - p.y, 1, p.y_len, p.err))) y[k][row] = r[k] + acc[k][0];
       }
     }
   }
 }
 
-// Splits of the columns: as many as give every SM two CTAs (each token taken to
-// have an adapter of its own), at most 16, a window of 256 columns each or more, and
-// at most 2048 columns (x of four tokens in shared memory).
-static int lora_window(long long K, int n_tok) {
-  const long long wins = (K + LORA_WIN - 1) / LORA_WIN;
-  long long splits = (2ll * LORA_SMS + n_tok - 1) / n_tok;
-  if (splits > 16) splits = 16;
-  if (splits > wins) splits = wins;
-  long long per = (wins + splits - 1) / splits;
-  if (per > 8) per = 8;
-  return (int)(per * LORA_WIN);
+template <int DT, int VW, int LPR_LOG>
+__global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_up_kernel(const LoraParams p) {
+  __shared__ float v[LORA_TOK][QMV_MAX_RANK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  const LoraTokens q = lora_tokens(p);
+  if (q.n == 0) return;  // (more CTAs than the groups' parts)
+  // this warp's rows: equal runs of at least 32, a multiple of 32
+  const long long warps = (long long)q.parts * LORA_WARPS;
+  const int per = (int)(((p.M + warps - 1) / warps + 31) / 32 * 32);
+  const long long m0 = min(((long long)q.part * LORA_WARPS + warp) * per, p.M);
+  const int rows = (int)min((long long)per, p.M - m0);
+  if (q.a < 0) {  // no adapter
+    pdl_wait();
+    if (p.y != p.res)
+      for (int k = 0; k < q.n; k++)
+        for (int m = lane; m < rows; m += 32)
+          if (QMV_CHECK(in_range(q.tok[k] * p.M + m0 + m, 1, p.y_len, p.err)))
+            p.y[q.tok[k] * p.M + m0 + m] = p.res[q.tok[k] * p.M + m0 + m];
+    return;
+  }
+  if (q.n == 1) lora_up<DT, VW, LPR_LOG, 1>(p, q, v, m0, rows);
+  else lora_up<DT, VW, LPR_LOG, LORA_TOK>(p, q, v, m0, rows);
 }
-int lora_splits(long long K, int n_tok) {
-  const int w = lora_window(K, n_tok);
+
+// Columns of a split: windows of 256, at most 8 (x of four tokens in shared memory)
+// and at most 16 splits (the second kernel adds them) where that leaves a choice.
+// Taken are those for which a warp has the fewest windows to go through, each token
+// taken to have an adapter of its own and its share of four CTAs an SM; fewer
+// splits among equals.
+static int lora_window(long long K, int n_tok, int r) {
+  const int wins = (int)((K + LORA_WIN - 1) / LORA_WIN), units = (r + LORA_ROWS - 1) / LORA_ROWS;
+  const int parts = LORA_CTAS * LORA_SMS / n_tok;
+  int best = 8, least = 0;
+  for (int want = 1; want <= 16 && want <= wins; want++) {
+    const int per = (wins + want - 1) / want, splits = (wins + per - 1) / per;
+    if (per > 8 || splits > parts) continue;
+    const int of = parts / splits, cost = ((units + of - 1) / of + LORA_WARPS - 1) / LORA_WARPS * per;
+    if (!least || cost < least) least = cost, best = per;
+  }
+  return best * LORA_WIN;
+}
+int lora_splits(long long K, int n_tok, int r) {
+  const int w = lora_window(K, n_tok, r);
   return (int)((K + w - 1) / w);
+}
+
+// CTAs of a launch: what the SMs hold at once, but not more than `units` for each
+// token, and at least `least` for each.
+static unsigned lora_grid(const LoraParams& p, long long units, long long least) {
+  long long ctas = (long long)LORA_CTAS * device_sm_count();
+  if (ctas > units * p.n_tok) ctas = units * p.n_tok;
+  if (ctas < least * p.n_tok) ctas = least * p.n_tok;
+  return (unsigned)ctas;
 }
 
 template <int DT, int VW, int LPR_LOG>
 static cudaError_t launch_up(const LoraParams& p, cudaStream_t stream) {
-  // Rows of a warp: so many that all warps fit the GPU at once (16 an SM), each
-  // token taken to have an adapter of its own; whole blocks.
-  constexpr int RPL = 32 >> LPR_LOG, BLOCK = (LPR_LOG < 3 ? 1 << LPR_LOG : 8) * RPL;
-  const long long warps = 16ll * device_sm_count() / p.n_tok;
-  long long rows = (p.M + warps - 1) / warps;
-  rows = (rows + BLOCK - 1) / BLOCK * BLOCK;
-  const long long per_cta = rows * LORA_WARPS;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  make_config(cfg, attr, dim3((unsigned)((p.M + per_cta - 1) / per_cta), p.n_tok), dim3(LORA_THREADS), 0, stream, true);
-  return cudaLaunchKernelEx(&cfg, lora_up_kernel<DT, VW, LPR_LOG>, p, (int)rows);
+  make_config(cfg, attr, dim3(lora_grid(p, (p.M + 32 * LORA_WARPS - 1) / (32 * LORA_WARPS), 1)), dim3(LORA_THREADS), 0, stream,
+              true);
+  return cudaLaunchKernelEx(&cfg, lora_up_kernel<DT, VW, LPR_LOG>, p);
 }
 
 template <int DT, int VW>
@@ -302,7 +389,9 @@ template <int DT>
 static cudaError_t launch_dt(const LoraParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  make_config(cfg, attr, dim3(p.splits, p.n_tok), dim3(LORA_THREADS), (size_t)LORA_TOK * p.window * sizeof(float), stream, true);
+  const long long units = (p.r + LORA_WARPS * LORA_ROWS - 1) / (LORA_WARPS * LORA_ROWS);
+  make_config(cfg, attr, dim3(lora_grid(p, p.splits * units, p.splits)), dim3(LORA_THREADS),
+              (size_t)LORA_TOK * p.window * sizeof(float), stream, true);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_down_kernel<DT>, p);
   if (e != cudaSuccess) return e;
   if constexpr (DT != QMV_DT_F32)
@@ -311,8 +400,8 @@ static cudaError_t launch_dt(const LoraParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_lora(int dtype, LoraParams p, cudaStream_t stream) {
-  p.window = lora_window(p.K, p.n_tok);
-  p.splits = lora_splits(p.K, p.n_tok);
+  p.window = lora_window(p.K, p.n_tok, p.r);
+  p.splits = lora_splits(p.K, p.n_tok, p.r);
   switch (dtype) {
     case QMV_DT_F16: return launch_dt<QMV_DT_F16>(p, stream);
     case QMV_DT_BF16: return launch_dt<QMV_DT_BF16>(p, stream);

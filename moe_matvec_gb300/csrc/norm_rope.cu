@@ -11,14 +11,41 @@ constexpr int ROPE_MAX_PAIRS = 128;   // head_dim 256
 constexpr int ROPE_AHEAD = 2;
 constexpr int ROPE_CTAS = 5;          // CTAs an SM
 
-// cos and sin of pair i at position pos.  The turn pos * freq / (2 pi) is formed
-// and reduced to its fraction in 64 bits: in 32 a position of 131072 leaves 2^-7
-// of the angle.  What remains is at most half a turn, to 2^-25 of a turn in fp32.
-__device__ __forceinline__ float2 turn_of(int pos, float freq, float scale) {
-  const double turn = (double)pos * ((double)freq * 0.15915494309189535);
+// A frequency (radians a position) in turns a position, as a fraction of 2^64: a
+// position times it, modulo 2^64, is the turn's fraction, whatever the position (in
+// fp32 a position of 131072 would leave 2^-7 of the angle).  Formed in 64-bit floats,
+// once per warp and pair.
+__device__ __forceinline__ unsigned long long turns_a_position(float freq) {
+  double f = (double)freq * 0.15915494309189535;  // 1 / (2 pi)
+  f -= rint(f);                                   // [-1/2, 1/2]
+  // (half a turn either way is 2^63; a frequency that is no number turns by 0)
+  return (unsigned long long)__double2ll_rn(f * 0x1p63) << 1;
+}
+// cos and sin of what is left of a turn: at most half a turn, to 2^-25 of it in fp32.
+__device__ __forceinline__ float2 turn_of(int pos, unsigned long long freq, float scale) {
+  const int left = (int)((unsigned long long)(long long)pos * freq >> 32);
   float s, c;
-  sincospif(2.0f * (float)(turn - rint(turn)), &s, &c);
+  sincospif((float)left * 0x1p-31f, &s, &c);
   return make_float2(c * scale, s * scale);
+}
+
+// The 2 CH consecutive values (a, b) of a unit whose pairs are neighbours: the
+// pairs' first values and their second ones, and back.
+template <int CH>
+__device__ __forceinline__ void to_pairs(float (&a)[CH], float (&b)[CH]) {
+  float x[2 * CH];
+#pragma unroll
+  for (int j = 0; j < CH; j++) x[j] = a[j], x[CH + j] = b[j];
+#pragma unroll
+  for (int j = 0; j < CH; j++) a[j] = x[2 * j], b[j] = x[2 * j + 1];
+}
+template <int CH>
+__device__ __forceinline__ void from_pairs(float (&a)[CH], float (&b)[CH]) {
+  float x[2 * CH];
+#pragma unroll
+  for (int j = 0; j < CH; j++) x[2 * j] = a[j], x[2 * j + 1] = b[j];
+#pragma unroll
+  for (int j = 0; j < CH; j++) a[j] = x[j], b[j] = x[CH + j];
 }
 
 // y = x * w / sqrt(mean(x^2) + eps) (w given, else y = x), then each pair (a, b) of
@@ -37,7 +64,7 @@ __device__ __forceinline__ float2 turn_of(int pos, float freq, float scale) {
 // Bound by HBM for many tokens.
 template <int DT, int CH, int UL, bool INTER>
 __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
-    norm_rope_kernel(const RopeParams p, int lph_log, int split) {
+    norm_rope_kernel(const RopeParams p, int lph_log, unsigned per, unsigned rest) {
   using T = typename Elem<DT>::type;
   using Chunk = Packed<T, CH>;
   constexpr int PF = UL == 1 ? ROPE_AHEAD : 1;  // head groups on their way
@@ -45,14 +72,20 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const unsigned item = blockIdx.x * ROPE_WARPS + wid;
-  const unsigned t = item / (unsigned)split;
-  const int part = (int)(item - t * split);
-  if (t >= (unsigned)p.n_tok) return;
   const int hpw = 32 >> lph_log, li = lane & ((1 << lph_log) - 1), sub = lane >> lph_log;
   const int units = p.D / (2 * CH), turning = p.R / (2 * CH);
   const int q_steps = (p.q.n + hpw - 1) >> (5 - lph_log), steps = q_steps + ((p.k.n + hpw - 1) >> (5 - lph_log));
-  const int s0 = steps * part / split, s1 = steps * (part + 1) / split;
+  // `per` groups for this warp, one more for the first `rest` warps
+  const unsigned w = blockIdx.x * ROPE_WARPS + wid, g0 = w * per + min(w, rest);
+  int todo = (int)(per + (w < rest));
+  unsigned t = g0 / (unsigned)steps;
+  int s0 = (int)(g0 - t * steps);
+  unsigned long long freq[ROPE_MAX_PAIRS / 32];
+#pragma unroll
+  for (int i = 0; i < ROPE_MAX_PAIRS / 32; i++) {
+    freq[i] = 0;
+    if (32 * i < p.R / 2) freq[i] = turns_a_position(lane + 32 * i < p.R / 2 ? p.freq[lane + 32 * i] : 0.f);
+  }
   // the lane's unit i, and the places of its two chunks in a head
   auto unit = [&](int i) { return li + (i << lph_log); };
   int pa[UL], pb[UL];
@@ -88,138 +121,144 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
       c.left -= hpw;
     }
   };
-  Chunk ra[PF][UL], rb[PF][UL];
-  Cursor in = group(s0, false), out = group(s0, true);
-  int ahead = s0;
-  auto fetch = [&](Chunk(&xa)[UL], Chunk(&xb)[UL]) {
-#pragma unroll
-    for (int i = 0; i < UL; i++) {
-      xa[i].clear();
-      xb[i].clear();
-      QMV_DEBUG_ONLY(const RopeHeads& h = ahead < q_steps ? p.q : p.k; const long long at = in.x - static_cast<const T*>(h.x);)
-      if (ahead < s1 && sub < in.left && unit(i) < units && QMV_CHECK(in_range(at + pa[i], CH, h.x_len, p.err)) &&
-          QMV_CHECK(in_range(at + pb[i], CH, h.x_len, p.err))) {
-        xa[i].load(in.x + pa[i]);
-        xb[i].load(in.x + pb[i]);
-      }
-    }
-    advance(in, ++ahead, false);
-  };
-#pragma unroll
-  for (int k = 0; k < PF; k++) fetch(ra[k], rb[k]);
-
-  int pos = 0;
-  if (!p.pos) {
-    int seq = (int)t, a = seq, b = seq + 1;
-    if (p.starts) {
-      seq = last_seq_at_most(p.n_seq, (int)t, [&](int s) { return p.starts[s]; });
-      a = p.starts[seq];
-      b = p.starts[seq + 1];
-    }
-    const int len = p.lens[seq];
-    if (a < 0 || b < a || b > p.n_tok || len < 0) set_error(p.err, QMV_DEVERR_BATCH);
-    if ((int)t < a || (int)t >= b) return;  // no sequence's token (the whole warp)
-    pos = (int)((long long)max(len, 0) - b + t);
-  }
-  for (int i = lane; i < p.R / 2; i += 32) {
-    int at = pos;
-    if (p.pos) {
-      int ax = p.axis ? p.axis[i] : 0;
-      if (ax >= p.n_axes) {
-        set_error(p.err, QMV_DEVERR_BATCH);
-        ax = 0;
-      }
-      at = p.pos[(long long)t * p.n_axes + ax];
-    }
-    turns[wid][i] = turn_of(at, p.freq[i], p.scale);
-  }
-  __syncwarp();
-  // Pair (a, b) becomes rstd (a ca - b sb, b cb + a sa): cosines and sines times the
-  // weights of a and b.
-  constexpr int NP = UL * CH;
-  float ca[NP], sa[NP], cb[NP], sb[NP];
-  auto factors = [&](const float* w) {
-#pragma unroll
-    for (int i = 0; i < UL; i++)
-#pragma unroll
-      for (int j = 0; j < CH; j++) {
-        const bool turn = unit(i) < turning;
-        const float2 cs = turn ? turns[wid][unit(i) * CH + j] : make_float2(1.f, 0.f);
-        float wa = 1.f, wb = 1.f;
-        if (w && unit(i) < units) {
-          // (values 2j and 2j + 1 of the unit where pairs are neighbours)
-          const bool next = INTER && turn;
-          wa = w[next ? pa[i] + 2 * j : pa[i] + j];
-          wb = w[next ? pa[i] + 2 * j + 1 : pb[i] + j];
-        }
-        ca[i * CH + j] = cs.x * wa, sa[i * CH + j] = cs.y * wa;
-        cb[i * CH + j] = cs.x * wb, sb[i * CH + j] = cs.y * wb;
-      }
-  };
-  factors(s0 < q_steps ? p.q.w : p.k.w);
   const float inv_d = 1.0f / (float)p.D;
-  for (int s = s0; s < s1; s += PF) {
-#pragma unroll
-    for (int k = 0; k < PF; k++) {
-      if (s + k >= s1) break;
-      if (s + k == q_steps && s + k > s0) factors(p.k.w);  // from queries to keys
-      const bool norm = (s + k < q_steps ? p.q.w : p.k.w) != nullptr;
-      float va[NP], vb[NP];
-#pragma unroll
-      for (int i = 0; i < UL; i++) {
-        float xa[CH], xb[CH];
-        ra[k][i].to(xa);
-        rb[k][i].to(xb);
-#pragma unroll
-        for (int j = 0; j < CH; j++) va[i * CH + j] = xa[j], vb[i * CH + j] = xb[j];
-      }
-      fetch(ra[k], rb[k]);
-      float rstd = 1.f;
-      if (norm) {
-        float sum = 0.f, other = 0.f;
-#pragma unroll
-        for (int i = 0; i < NP; i++) {
-          sum = fmaf(va[i], va[i], sum);
-          other = fmaf(vb[i], vb[i], other);
-        }
-        sum += other;
-        for (int o = 1; o < 1 << lph_log; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        rstd = rsqrtf(fmaf(sum, inv_d, p.eps));  // at most 2 units in the last place off
-      }
+  for (; todo > 0; t++, s0 = 0) {
+    const int s1 = min(s0 + todo, steps);
+    todo -= s1 - s0;
+    Chunk ra[PF][UL], rb[PF][UL];
+    Cursor in = group(s0, false), out = group(s0, true);
+    int ahead = s0;
+    auto fetch = [&](Chunk(&xa)[UL], Chunk(&xb)[UL]) {
 #pragma unroll
       for (int i = 0; i < UL; i++) {
-        if (INTER && CH > 1 && unit(i) < turning) {  // from neighbours to pairs
-          float x[2 * CH];
-#pragma unroll
-          for (int j = 0; j < CH; j++) x[j] = va[i * CH + j], x[CH + j] = vb[i * CH + j];
-#pragma unroll
-          for (int j = 0; j < CH; j++) va[i * CH + j] = x[2 * j], vb[i * CH + j] = x[2 * j + 1];
+        xa[i].clear();
+        xb[i].clear();
+        QMV_DEBUG_ONLY(const RopeHeads& h = ahead < q_steps ? p.q : p.k; const long long at = in.x - static_cast<const T*>(h.x);)
+        if (ahead < s1 && sub < in.left && unit(i) < units && QMV_CHECK(in_range(at + pa[i], CH, h.x_len, p.err)) &&
+            QMV_CHECK(in_range(at + pb[i], CH, h.x_len, p.err))) {
+          xa[i].load(in.x + pa[i]);
+          xb[i].load(in.x + pb[i]);
         }
-        Chunk oa, ob;
-        float ya[CH], yb[CH];
+      }
+      advance(in, ++ahead, false);
+    };
+#pragma unroll
+    for (int k = 0; k < PF; k++) fetch(ra[k], rb[k]);
+
+    int pos = 0;
+    if (!p.pos) {
+      int seq = (int)t, a = seq, b = seq + 1;
+      if (p.starts) {
+        seq = last_seq_at_most(p.n_seq, (int)t, [&](int s) { return p.starts[s]; });
+        a = p.starts[seq];
+        b = p.starts[seq + 1];
+      }
+      const int len = p.lens[seq];
+      if (a < 0 || b < a || b > p.n_tok || len < 0) set_error(p.err, QMV_DEVERR_BATCH);
+      if ((int)t < a || (int)t >= b) continue;  // no sequence's token (the whole warp)
+      pos = (int)((long long)max(len, 0) - b + t);
+    }
+    __syncwarp();  // (the last token's turns are read)
+#pragma unroll
+    for (int i = 0; i < ROPE_MAX_PAIRS / 32; i++) {
+      const int pair = lane + 32 * i;
+      if (pair >= p.R / 2) break;
+      int at = pos;
+      if (p.pos) {
+        int ax = p.axis ? p.axis[pair] : 0;
+        if (ax >= p.n_axes) {
+          set_error(p.err, QMV_DEVERR_BATCH);
+          ax = 0;
+        }
+        at = p.pos[(long long)t * p.n_axes + ax];
+      }
+      turns[wid][pair] = turn_of(at, freq[i], p.scale);
+    }
+    __syncwarp();
+    // Pair (a, b) becomes rstd (a ca - b sb, b cb + a sa): cosines and sines times the
+    // weights of a and b.
+    constexpr int NP = UL * CH;
+    float ca[NP], sa[NP], cb[NP], sb[NP];
+    auto factors = [&](const float* w) {
+#pragma unroll
+      for (int i = 0; i < UL; i++) {
+        const bool turn = unit(i) < turning;
+        float wa[CH], wb[CH];
+#pragma unroll
+        for (int j = 0; j < CH; j++) wa[j] = wb[j] = 1.f;
+        if (w && unit(i) < units) {
+          if constexpr (CH > 1) {
+            load_vec<CH>(w + pa[i], wa);
+            load_vec<CH>(w + pb[i], wb);
+          } else {
+            wa[0] = w[pa[i]];
+            wb[0] = w[pb[i]];
+          }
+          if (INTER && turn) to_pairs(wa, wb);
+        }
 #pragma unroll
         for (int j = 0; j < CH; j++) {
-          const int e = i * CH + j;
-          ya[j] = rstd * (va[e] * ca[e] - vb[e] * sb[e]);
-          yb[j] = rstd * (vb[e] * cb[e] + va[e] * sa[e]);
-        }
-        if (INTER && CH > 1 && unit(i) < turning) {
-          float x[2 * CH];
-#pragma unroll
-          for (int j = 0; j < CH; j++) x[2 * j] = ya[j], x[2 * j + 1] = yb[j];
-#pragma unroll
-          for (int j = 0; j < CH; j++) ya[j] = x[j], yb[j] = x[CH + j];
-        }
-        oa.from(ya);
-        ob.from(yb);
-        QMV_DEBUG_ONLY(const RopeHeads& h = s + k < q_steps ? p.q : p.k; const long long at = out.x - static_cast<const T*>(h.y);)
-        if (sub < out.left && unit(i) < units && QMV_CHECK(in_range(at + pa[i], CH, h.y_len, p.err)) &&
-            QMV_CHECK(in_range(at + pb[i], CH, h.y_len, p.err))) {
-          oa.store(out.x + pa[i]);
-          ob.store(out.x + pb[i]);
+          const float2 cs = turn ? turns[wid][unit(i) * CH + j] : make_float2(1.f, 0.f);
+          ca[i * CH + j] = cs.x * wa[j], sa[i * CH + j] = cs.y * wa[j];
+          cb[i * CH + j] = cs.x * wb[j], sb[i * CH + j] = cs.y * wb[j];
         }
       }
-      advance(out, s + k + 1, true);
+    };
+    factors(s0 < q_steps ? p.q.w : p.k.w);
+    for (int s = s0; s < s1; s += PF) {
+#pragma unroll
+      for (int k = 0; k < PF; k++) {
+        if (s + k >= s1) break;
+        if (s + k == q_steps && s + k > s0) factors(p.k.w);  // from queries to keys
+        const bool norm = (s + k < q_steps ? p.q.w : p.k.w) != nullptr;
+        float va[NP], vb[NP];
+#pragma unroll
+        for (int i = 0; i < UL; i++) {
+          float xa[CH], xb[CH];
+          ra[k][i].to(xa);
+          rb[k][i].to(xb);
+#pragma unroll
+          for (int j = 0; j < CH; j++) va[i * CH + j] = xa[j], vb[i * CH + j] = xb[j];
+        }
+        fetch(ra[k], rb[k]);
+        float rstd = 1.f;
+        if (norm) {
+          float sum = 0.f, other = 0.f;
+#pragma unroll
+          for (int i = 0; i < NP; i++) {
+            sum = fmaf(va[i], va[i], sum);
+            other = fmaf(vb[i], vb[i], other);
+          }
+          sum += other;
+          for (int o = 1; o < 1 << lph_log; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          rstd = rsqrtf(fmaf(sum, inv_d, p.eps));  // at most 2 units in the last place off
+        }
+#pragma unroll
+        for (int i = 0; i < UL; i++) {
+          Chunk oa, ob;
+          float xa[CH], xb[CH], ya[CH], yb[CH];
+#pragma unroll
+          for (int j = 0; j < CH; j++) xa[j] = va[i * CH + j], xb[j] = vb[i * CH + j];
+          const bool next = INTER && unit(i) < turning;
+          if (next) to_pairs(xa, xb);
+#pragma unroll
+          for (int j = 0; j < CH; j++) {
+            const int e = i * CH + j;
+            ya[j] = rstd * (xa[j] * ca[e] - xb[j] * sb[e]);
+            yb[j] = rstd * (xb[j] * cb[e] + xa[j] * sa[e]);
+          }
+          if (next) from_pairs(ya, yb);
+          oa.from(ya);
+          ob.from(yb);
+          QMV_DEBUG_ONLY(const RopeHeads& h = s + k < q_steps ? p.q : p.k; const long long at = out.x - static_cast<const T*>(h.y);)
+          if (sub < out.left && unit(i) < units && QMV_CHECK(in_range(at + pa[i], CH, h.y_len, p.err)) &&
+              QMV_CHECK(in_range(at + pb[i], CH, h.y_len, p.err))) {
+            oa.store(out.x + pa[i]);
+            ob.store(out.x + pb[i]);
+          }
+        }
+        advance(out, s + k + 1, true);
+      }
     }
   }
 }
@@ -231,17 +270,16 @@ static cudaError_t launch_as(bool interleaved, const RopeParams& p, cudaStream_t
   while ((1 << log) < units && log < 5) log++;
   const int hpw = 32 >> log;
   const int steps = (p.q.n + hpw - 1) / hpw + (p.k.n + hpw - 1) / hpw;
-  // Few tokens: their heads are shared out to more warps, as many as 8 warps an SM.
-  const long long warps = 8ll * device_sm_count();
-  int split = (int)(warps / p.n_tok);
-  if (split > steps) split = steps;
-  if (split < 1) split = 1;
-  const long long items = (long long)p.n_tok * split;
+  // As many warps as the GPU holds at once, or a group of heads each.
+  const long long total = (long long)p.n_tok * steps, ctas = (total + ROPE_WARPS - 1) / ROPE_WARPS;
+  const long long cap = (long long)(UL == 1 ? ROPE_CTAS : 3) * device_sm_count();
+  const unsigned grid = (unsigned)(ctas < cap ? ctas : cap);
+  const unsigned per = (unsigned)(total / (grid * ROPE_WARPS)), rest = (unsigned)(total % (grid * ROPE_WARPS));
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  make_config(cfg, attr, dim3((unsigned)((items + ROPE_WARPS - 1) / ROPE_WARPS)), dim3(32 * ROPE_WARPS), 0, stream, true);
-  if (interleaved) return cudaLaunchKernelEx(&cfg, norm_rope_kernel<DT, CH, UL, true>, p, log, split);
-  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<DT, CH, UL, false>, p, log, split);
+  make_config(cfg, attr, dim3(grid), dim3(32 * ROPE_WARPS), 0, stream, true);
+  if (interleaved) return cudaLaunchKernelEx(&cfg, norm_rope_kernel<DT, CH, UL, true>, p, log, per, rest);
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<DT, CH, UL, false>, p, log, per, rest);
 }
 
 // Chunks of 16 bytes where whole ones pair up (of 8 for 16-bit types whose sizes

@@ -17,28 +17,41 @@ struct RoutePlace {
   int log, per;
 };
 
-// A value's place in the order of real numbers, above 0; NaN as -inf.
+// A number's place in the order of real numbers, above 0 (-0 is not for it).
 __device__ __forceinline__ uint32_t order_of(float v) {
-  v = v == v ? v + 0.0f : -INFINITY;  // (-0 + 0 = 0: equal numbers are equal)
-  const uint32_t b = __float_as_uint(v);
-  return (int)b < 0 ? ~b : b | 0x80000000u;
+  const int b = __float_as_int(v);
+  return (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t o) {
-  return __uint_as_float((int)o < 0 ? o & 0x7fffffffu : ~o);
+  return __uint_as_float(o ^ ((uint32_t)~((int)o >> 31) | 0x80000000u));
 }
 
-// A logit as the scores take it: NaN as -inf, at most FLT_MAX.
-__device__ __forceinline__ float tame(float l) { return l == l ? fminf(l, FLT_MAX) : -INFINITY; }
+// A logit or bias as it is taken: NaN as -inf, at most FLT_MAX, -0 as 0.
+__device__ __forceinline__ float tame(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX) + 0.0f; }
 
-// The whole selection of a token in 64 bits, by one warp, for tokens whose
-// 32-bit scores come too close to a decision: the same steps as in the kernel
-// below, whose result it replaces.  Called for about one token in 300, so the
+__device__ __forceinline__ void put(const RouteParams& p, int t, int k, int expert, double gate) {
+  const long long at = (long long)t * p.top_k + k;
+  if (QMV_CHECK(in_range(at, 1, p.ids_len, p.err))) {
+    p.ids[at] = expert;
+    p.gates[at] = (float)gate;
+  }
+}
+__device__ __forceinline__ void put(const RouteParams& p, int t, int k, int expert, float gate) {
+  const long long at = (long long)t * p.top_k + k;
+  if (QMV_CHECK(in_range(at, 1, p.ids_len, p.err))) {
+    p.ids[at] = expert;
+    p.gates[at] = gate;
+  }
+}
+
+// The whole selection of token t in 64 bits, by one warp, where more experts are in
+// doubt than it has lanes: the same steps as in the kernel below.  Rare, so the
 // logits are read again and nothing is tuned.
 template <int PER, class T>
-__device__ __noinline__ void select_exactly(const RouteParams& p, RoutePlace pl, const T* row, int (&pick)[QMV_MAX_TOPK],
-                                            float (&gate)[QMV_MAX_TOPK]) {
+__device__ __noinline__ void select_exactly(const RouteParams& p, RoutePlace pl, int t) {
+  const T* row = static_cast<const T*>(p.logits) + (long long)t * p.ld;
   const int lane = threadIdx.x & 31;
-  const int lpg = 1 << pl.log, gs = p.E / p.groups, g = lane >> pl.log;
+  const int lpg = 1 << pl.log, gs = p.size, g = lane >> pl.log;
   const int first = (lane & (lpg - 1)) * pl.per;
   const int have = g < p.groups ? max(0, min(pl.per, gs - first)) : 0;
   const int e0 = g * gs + first;
@@ -64,8 +77,7 @@ __device__ __noinline__ void select_exactly(const RouteParams& p, RoutePlace pl,
       s[i] = raw(i);
       if (soft) s[i] = total > 0 ? s[i] / total : 0.0;
       c[i] = s[i];
-      if (p.bias) c[i] += (double)p.bias[e0 + i];
-      if (!(c[i] == c[i])) c[i] = -INFINITY;
+      if (p.bias) c[i] += (double)tame(p.bias[e0 + i]);
       if (c[i] > one) two = one, one = c[i];
       else if (c[i] > two) two = c[i];
       // without a bias larger logits are larger scores, whatever 64 bits leave of them
@@ -89,7 +101,8 @@ __device__ __noinline__ void select_exactly(const RouteParams& p, RoutePlace pl,
       for (int i = 0; i < PER; i++) s[i] = -1;  // left out
     }
   }
-  double picked[QMV_MAX_TOPK], sum = 0;
+  double mine = 0, sum = 0;  // lane k: pick k's score
+  int pick = 0;
   for (int k = 0; k < p.top_k; k++) {
     double best = -INFINITY, score = 0;
     int at = 0x7fffffff;
@@ -104,179 +117,314 @@ __device__ __noinline__ void select_exactly(const RouteParams& p, RoutePlace pl,
 #pragma unroll
     for (int i = 0; i < PER; i++)
       if (i < have && e0 + i == at) s[i] = -1;
-    pick[k] = at;
-    picked[k] = score;
+    if (lane == k) pick = at, mine = score;
     sum += score;
   }
-  for (int k = 0; k < p.top_k; k++)
-    gate[k] = (float)((p.renorm ? (sum > 0 ? picked[k] / sum : 0.0) : picked[k]) * (double)p.scale);
+  if (lane < p.top_k) put(p, t, lane, pick, (p.renorm ? (sum > 0 ? mine / sum : 0.0) : mine) * (double)p.scale);
 }
 
-// One warp a token: s = softmax(l) or sigmoid(l), c = s + bias; a group's score
-// is the sum of its one or two largest c; of the kept groups' experts the top_k
-// largest c are picked, larger first, ties to the lower index; gates are their s,
-// over their sum if renorm, times scale.
+// Largest first, by a bitonic network.
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int k = 2; k <= N; k *= 2)
+#pragma unroll
+    for (int j = k / 2; j > 0; j /= 2)
+#pragma unroll
+      for (int i = 0; i < N; i++)
+        if ((i ^ j) > i) {
+          const uint32_t lo = min(v[i], v[i ^ j]), hi = max(v[i], v[i ^ j]);
+          v[i] = i & k ? lo : hi;
+          v[i ^ j] = i & k ? hi : lo;
+        }
+}
+
+// A warp a token, by turns: s = softmax(l) or sigmoid(l), c = s + bias; a group's
+// score is the sum of its one or two largest c; of the kept groups' experts the
+// top_k largest c are picked, larger first, ties to the lower index; gates are their
+// s, over their sum if renorm, times scale.
 //
-// Without a bias an expert's c orders as its logit does, and the logits are
-// compared.  With one, and for sums of two, what is compared carries the errors of
-// fp32: score and sum are within about 2^-21 of s + |bias|.  Where two compared
-// values at a border (kept and next group; consecutive picks and the first left
-// out) lie closer than 2^-20 of their size plus 2^-24, the token is decided again
-// in 64 bits, so the picks are those of 64 bits everywhere.
+// Each lane has consecutive experts (lane order is expert order) and sorts their
+// keys: the places of c, or without a bias of the logits, in the order of real
+// numbers, whose lowest bits give way to the expert's slot in the lane.  A pick is
+// then the largest of the lanes' first keys, the first lane that has it, and a shift
+// of that lane's keys; lane k keeps pick k.
 //
-// Bound by the picks: 2 steps across the warp and one over a lane's experts each.
-template <int PER, int DT>
+// What is compared carries errors: those of fp32 (score and sum are within about
+// 2^-21 of s + |bias|; a logit is exact) and the slot's bits.  Where two compared
+// values at a border (kept and next group; consecutive picks and the first left out)
+// lie closer than that, what is in doubt is decided in 64 bits: the groups about the
+// border by their exact scores, the picks by the exact values of the picks and of
+// all experts that are as close after them, one a lane.  So the picks are those of 64
+// bits everywhere, at the cost of 64-bit arithmetic for about one token in a hundred.
+//
+// Bound by instructions.
+template <int PER, int DT, bool VEC>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_select_kernel(const RouteParams p, const RoutePlace pl) {
   using T = typename Elem<DT>::type;
+  constexpr uint32_t SLOT = PER - 1;  // the bits of a slot
+  __shared__ float scores[ROUTE_WARPS][32 * PER];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5);
-  if (t >= p.n_tok) return;
-  const T* row = static_cast<const T*>(p.logits) + (long long)t * p.ld;
-  const int lpg = 1 << pl.log, gs = p.E / p.groups, g = lane >> pl.log;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lpg = 1 << pl.log, gs = p.size, g = lane >> pl.log;
   const int first = (lane & (lpg - 1)) * pl.per;
   const int have = g < p.groups ? max(0, min(pl.per, gs - first)) : 0;
   const int e0 = g * gs + first;
-  float s[PER];
-  float top = -INFINITY;
+  const bool soft = p.gating == QMV_GATING_SOFTMAX, biased = p.bias != nullptr;
+  float bias[PER], widest = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; i++) {
-    s[i] = i < have && QMV_CHECK(in_range((long long)t * p.ld + e0 + i, 1, p.logits_len, p.err))
-               ? tame(to_float(row[e0 + i]))
-               : -INFINITY;
-    top = fmaxf(top, s[i]);
+    bias[i] = 0.f;
+    if (biased && i < have) {
+      bias[i] = tame(p.bias[e0 + i]);
+      if (fabsf(bias[i]) < INFINITY) widest = fmaxf(widest, fabsf(bias[i]));
+    }
   }
-  uint32_t key[PER];  // the place of what picks compare; 0: none
+  widest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(widest)));
+  // scores that this close may stand the other way round
+  auto close = [&](float a, float b, float more) {
+    return a == b || fabsf(a - b) <= 0x1p-20f * (fabsf(a) + fabsf(b) + 2.0f * widest) + 0x1p-24f + more;
+  };
+  auto expert = [&](int f) {  // of lane f / PER, slot f % PER
+    const int of = f / PER;
+    return (of >> pl.log) * gs + (of & (lpg - 1)) * pl.per + f % PER;
+  };
+  for (int t = blockIdx.x * ROUTE_WARPS + warp; t < p.n_tok; t += gridDim.x * ROUTE_WARPS) {
+    const T* row = static_cast<const T*>(p.logits) + (long long)t * p.ld;
+    float s[PER];
+    if constexpr (VEC) {  // lanes have whole fours
 #pragma unroll
-  for (int i = 0; i < PER; i++) key[i] = !p.bias && i < have ? order_of(s[i]) : 0;
-  float inv = 1.f;  // scores are inv * s
-  if (p.gating == QMV_GATING_SOFTMAX) {
-    top = value_of(__reduce_max_sync(0xffffffffu, order_of(top)));
-    float total = 0.f;
+      for (int i = 0; i < PER; i += 4) {
+        Packed<T, 4> x;
+        float l[4];
+        const bool in = i < have && QMV_CHECK(in_range((long long)t * p.ld + e0 + i, 4, p.logits_len, p.err));
+        x.clear();
+        if (in) x.load(row + e0 + i);
+        x.to(l);
+#pragma unroll
+        for (int j = 0; j < 4; j++) s[i + j] = in ? l[j] : -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; i++)
+        s[i] = i < have && QMV_CHECK(in_range((long long)t * p.ld + e0 + i, 1, p.logits_len, p.err)) ? to_float(row[e0 + i]) : -INFINITY;
+    }
+    float top = -INFINITY;
+    uint32_t key[PER];  // 0: none
 #pragma unroll
     for (int i = 0; i < PER; i++) {
-      s[i] = s[i] > -INFINITY ? expf(s[i] - top) : 0.f;
-      total += s[i];
+      s[i] = tame(s[i]);
+      top = fmaxf(top, s[i]);
+      if (!biased) key[i] = order_of(s[i]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    inv = total > 0.f ? 1.0f / total : 0.f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; i++) s[i] = s[i] > -INFINITY ? __frcp_rn(1.0f + expf(-s[i])) : 0.f;
-  }
-  float one = -INFINITY, two = -INFINITY, widest = 0.f;
-#pragma unroll
-  for (int i = 0; i < PER; i++)
-    if (i < have) {
-      float c = s[i] * inv;
-      if (p.bias) {
-        const float b = p.bias[e0 + i];
-        c += b;
-        key[i] = order_of(c);
-        c = value_of(key[i]);
-        if (fabsf(b) < INFINITY) widest = fmaxf(widest, fabsf(b));
-      }
-      two = fmaxf(two, fminf(one, c));
-      one = fmaxf(one, c);
-    }
-  widest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(widest)));
-  // two values that this close may stand the other way round
-  auto close = [&](float a, float b) {
-    return a == b || fabsf(a - b) <= 0x1p-20f * (fabsf(a) + fabsf(b) + 2.0f * widest) + 0x1p-24f;
-  };
-  bool doubt = false;
-  if (p.keep < p.groups) {
-    for (int o = 1; o < lpg; o <<= 1) {
-      const float a = __shfl_xor_sync(0xffffffffu, one, o), b = __shfl_xor_sync(0xffffffffu, two, o);
-      two = fmaxf(fminf(one, a), one >= a ? two : b);
-      one = fmaxf(one, a);
-    }
-    const float mine = p.group_top == 2 ? one + two : one;
-    int before = 0;
-    bool near = false;
-    for (int j = 0; j < p.groups; j++) {
-      const float other = __shfl_sync(0xffffffffu, mine, j << pl.log);
-      const bool first_of = other > mine || (other == mine && j < g);
-      before += first_of;
-      near |= j != g && close(mine, other);
-    }
-    // only a group next to the border between kept and left matters
-    doubt = near && g < p.groups && before + 1 >= p.keep && before <= p.keep;
-    if (before >= p.keep || g >= p.groups) {
-#pragma unroll
-      for (int i = 0; i < PER; i++) key[i] = 0;
-    }
-  }
-  doubt = __any_sync(0xffffffffu, doubt);
-
-  int pick[QMV_MAX_TOPK];
-  float gate[QMV_MAX_TOPK];
-  float sum = 0.f, last = 0.f;
-  uint32_t mine = 0;
-#pragma unroll
-  for (int i = 0; i < PER; i++) mine = max(mine, key[i]);
-#pragma unroll
-  for (int k = 0; k <= QMV_MAX_TOPK; k++) {
-    if (k > p.top_k) break;
-    const uint32_t best = __reduce_max_sync(0xffffffffu, mine);
-    if (p.bias && best) {
-      const float now = value_of(best);
-      if (k > 0) doubt |= close(last, now);
-      last = now;
-    }
-    if (k >= p.top_k || k >= QMV_MAX_TOPK) break;
-    const int from = __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1;
-    int at = 0;
-    float sc = 0.f;
-    if (lane == from) {
-      bool found = false;
-      mine = 0;
+    float inv = 1.f;  // scores are inv * s
+    if (soft) {
+      top = value_of(__reduce_max_sync(0xffffffffu, order_of(top)));
+      float total = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; i++) {
-        if (!found && key[i] == best) {
-          found = true;
-          at = e0 + i;
-          sc = s[i];
-          key[i] = 0;
+        s[i] = s[i] > -INFINITY ? expf(s[i] - top) : 0.f;
+        total += s[i];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      inv = total > 0.f ? 1.0f / total : 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; i++) s[i] = __fdividef(1.0f, 1.0f + expf(-s[i]));  // (2 ulp; -inf: 1 / inf = 0)
+    }
+    float c[PER];
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      scores[warp][lane * PER + i] = s[i];
+      c[i] = fmaf(s[i], inv, bias[i]);
+      if (biased) key[i] = order_of(c[i]);
+    }
+
+    // Exact values, by the whole warp where something is in doubt.  Scores of a softmax
+    // without a bias are compared without their common divisor.
+    double total = 1;
+    bool summed = false;
+    auto exact_sum = [&]() {
+      if (!soft || !biased || summed) return;
+      summed = true;
+      total = 0;
+#pragma unroll
+      for (int i = 0; i < PER; i++) {
+        const float l = i < have ? tame(to_float(row[e0 + i])) : -INFINITY;
+        total += l > -INFINITY ? exp((double)l - (double)top) : 0.0;
+      }
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    };
+    auto exact_score = [&](float l) -> double {
+      if (!(l > -INFINITY)) return 0.0;
+      return soft ? exp((double)l - (double)top) / total : 1.0 / (1.0 + exp(-(double)l));
+    };
+    auto exact = [&](int e, double& score) -> double {
+      score = exact_score(tame(to_float(row[e])));
+      return biased ? score + (double)tame(p.bias[e]) : score;
+    };
+
+    if (p.keep < p.groups) {
+      float one = -INFINITY, two = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PER; i++)
+        if (i < have) {
+          two = fmaxf(two, fminf(one, c[i]));
+          one = fmaxf(one, c[i]);
         }
-        mine = max(mine, key[i]);
+      for (int o = 1; o < lpg; o <<= 1) {
+        const float a = __shfl_xor_sync(0xffffffffu, one, o), b = __shfl_xor_sync(0xffffffffu, two, o);
+        two = fmaxf(fminf(one, a), one >= a ? two : b);
+        one = fmaxf(one, a);
+      }
+      const float score = p.group_top == 2 ? one + two : one;
+      const uint32_t mine = order_of(score + 0.0f);
+      int before = 0;
+      for (int j = 0; j < p.groups; j++) {
+        const uint32_t other = __shfl_sync(0xffffffffu, mine, j << pl.log);
+        before += other > mine || (other == mine && j < g);
+      }
+      bool in = g < p.groups && before < p.keep;
+      const float last = value_of(__reduce_min_sync(0xffffffffu, in ? mine : 0xffffffffu));
+      const float next = value_of(__reduce_max_sync(0xffffffffu, in || g >= p.groups ? 0u : mine));
+      if (close(last, next, 0.f)) {
+        const bool open = g < p.groups && (close(score, last, 0.f) || close(score, next, 0.f));
+        const unsigned lead = (lane & (lpg - 1)) == 0 ? 0xffffffffu : 0u;
+        unsigned opened = __ballot_sync(0xffffffffu, open && lead);
+        // what is left to be kept of these groups
+        const int want = p.keep - __popc(__ballot_sync(0xffffffffu, in && !open && lead));
+        exact_sum();
+        double value = 0;  // of the lane's group
+        for (unsigned todo = opened; todo; todo &= todo - 1) {
+          const int of = __ffs(todo) - 1, group = of >> pl.log;
+          double a = -INFINITY, b = -INFINITY, sc;
+          for (int i = lane; i < gs; i += 32) {
+            const double v = exact(group * gs + i, sc);
+            if (v > a) b = a, a = v;
+            else if (v > b) b = v;
+          }
+          for (int o = 16; o > 0; o >>= 1) {
+            const double x = __shfl_xor_sync(0xffffffffu, a, o), y = __shfl_xor_sync(0xffffffffu, b, o);
+            b = fmax(fmin(a, x), a >= x ? b : y);
+            a = fmax(a, x);
+          }
+          if (g == group) value = p.group_top == 2 ? a + b : a;
+        }
+        int ahead = 0;
+        for (unsigned todo = opened; todo; todo &= todo - 1) {
+          const int of = __ffs(todo) - 1;
+          const double other = __shfl_sync(0xffffffffu, value, of);
+          ahead += other > value || (other == value && (of >> pl.log) < g);
+        }
+        if (open) in = ahead < want;
+      }
+      if (!in) {
+#pragma unroll
+        for (int i = 0; i < PER; i++) key[i] = 0;
       }
     }
-    pick[k] = __shfl_sync(0xffffffffu, at, from);
-    gate[k] = __shfl_sync(0xffffffffu, sc, from);
-    sum += gate[k];
-  }
-  if (doubt) {
-    select_exactly<PER, T>(p, pl, row, pick, gate);
-  } else {
+#pragma unroll
+    for (int i = 0; i < PER; i++) key[i] = i < have && key[i] ? (key[i] & ~SLOT) | (SLOT - i) : 0;
+    sort_down(key);
+
+    uint32_t picked = 0;  // lane k: pick k's key, and its expert's lane and slot
+    int from = 0;
+    auto pick = [&](int k, int deep) {  // (keys past `deep` are not asked for any more)
+      const uint32_t head = key[0] & ~SLOT, best = __reduce_max_sync(0xffffffffu, head);
+      const int of = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
+      const int slot = SLOT - (__shfl_sync(0xffffffffu, key[0], of) & SLOT);
+      if (lane == k) {
+        picked = best;
+        from = of * PER + slot;
+      }
+      if (lane == of) {
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+          if (i < deep) key[i] = i + 1 < PER ? key[i + 1] : 0;
+      }
+    };
 #pragma unroll
     for (int k = 0; k < QMV_MAX_TOPK; k++)
-      if (k < p.top_k) gate[k] = (!p.renorm ? gate[k] * inv : sum > 0.f ? gate[k] / sum : 0.f) * p.scale;
-  }
+      if (k < p.top_k) pick(k, PER);
+    // consecutive picks, and the last one and what comes after it
+    const uint32_t after = __reduce_max_sync(0xffffffffu, key[0] & ~SLOT);
+    auto near = [&](uint32_t a, uint32_t b) {  // b is not above a
+      if (!biased) return DT == QMV_DT_F32 && a == b;  // (the slot's bits are 0 in logits of 16)
+      const float x = value_of(a), y = value_of(b);
+      return close(x, y, (float)PER * 0x1p-23f * fmaxf(fabsf(x), fabsf(y)));
+    };
+    uint32_t follower = __shfl_down_sync(0xffffffffu, picked, 1);
+    if (lane == p.top_k - 1) follower = after;
+    const bool doubt = __any_sync(0xffffffffu, lane < p.top_k && follower && near(picked, follower));
+    __syncwarp();
+    if (!doubt) {
+      const float score = lane < p.top_k ? scores[warp][from] : 0.f;
+      float sum = score;
 #pragma unroll
-  for (int k = 0; k < QMV_MAX_TOPK; k++)
-    if (k < p.top_k && lane == k && QMV_CHECK(in_range((long long)t * p.top_k + k, 1, p.ids_len, p.err))) {
-      p.ids[(long long)t * p.top_k + k] = pick[k];
-      p.gates[(long long)t * p.top_k + k] = gate[k];
+      for (int o = QMV_MAX_TOPK / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane < p.top_k)
+        put(p, t, lane, expert(from), (p.renorm ? (sum > 0.f ? score / sum : 0.f) : score * inv) * p.scale);
+      __syncwarp();  // (the scores are read)
+      continue;
     }
+    int n = p.top_k;
+    while (n < 32) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, key[0] & ~SLOT);
+      if (!best || !near(__shfl_sync(0xffffffffu, picked, n - 1), best)) break;
+      pick(n++, PER);
+    }
+    if (n == 32) {  // more than a warp can hold
+      select_exactly<PER, T>(p, pl, t);
+      continue;
+    }
+    const int e = expert(from);
+    double v = -INFINITY, score = 0;
+    if (biased) exact_sum();
+    if (lane < n) {
+      if (biased) {
+        v = exact(e, score);
+      } else {
+        v = tame(to_float(row[e]));
+        score = (double)scores[warp][from] * inv;
+      }
+    }
+    int before = 0;
+    for (int j = 0; j < n; j++) {
+      const double other = __shfl_sync(0xffffffffu, v, j);
+      const int i = __shfl_sync(0xffffffffu, e, j);
+      before += other > v || (other == v && i < e);
+    }
+    const bool in = lane < n && before < p.top_k;
+    double sum = in ? score : 0.0;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (in) put(p, t, before, e, (p.renorm ? (sum > 0 ? score / sum : 0.0) : score) * (double)p.scale);
+  }
+}
+
+template <int DT, bool VEC>
+static cudaError_t launch_as(const RouteParams& p, RoutePlace pl, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  // as many CTAs as the SMs hold at once (up to eights experts a lane); warps take tokens by turns
+  const int ctas = (p.n_tok + ROUTE_WARPS - 1) / ROUTE_WARPS, cap = 8 * device_sm_count();
+  make_config(cfg, attr, dim3((unsigned)(ctas < cap ? ctas : cap)), dim3(32 * ROUTE_WARPS), 0, stream, true);
+  if (pl.per <= 4) return cudaLaunchKernelEx(&cfg, route_select_kernel<4, DT, VEC>, p, pl);
+  if (pl.per <= 8) return cudaLaunchKernelEx(&cfg, route_select_kernel<8, DT, VEC>, p, pl);
+  if (pl.per <= 16) return cudaLaunchKernelEx(&cfg, route_select_kernel<16, DT, VEC>, p, pl);
+  return cudaLaunchKernelEx(&cfg, route_select_kernel<32, DT, VEC>, p, pl);
 }
 
 template <int DT>
-static cudaError_t launch_dt(const RouteParams& p, cudaStream_t stream) {
-  const int gs = p.E / p.groups;
+static cudaError_t launch_dt(RouteParams p, cudaStream_t stream) {
+  p.size = p.E / p.groups;
   RoutePlace pl{0, 0};
   while ((2 << pl.log) * p.groups <= 32) pl.log++;
-  pl.per = (gs + (1 << pl.log) - 1) >> pl.log;
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[1];
-  make_config(cfg, attr, dim3((unsigned)((p.n_tok + ROUTE_WARPS - 1) / ROUTE_WARPS)), dim3(32 * ROUTE_WARPS), 0, stream,
-              true);
-  if (pl.per <= 4) return cudaLaunchKernelEx(&cfg, route_select_kernel<4, DT>, p, pl);
-  if (pl.per <= 8) return cudaLaunchKernelEx(&cfg, route_select_kernel<8, DT>, p, pl);
-  if (pl.per <= 16) return cudaLaunchKernelEx(&cfg, route_select_kernel<16, DT>, p, pl);
-  return cudaLaunchKernelEx(&cfg, route_select_kernel<32, DT>, p, pl);
+  pl.per = (p.size + (1 << pl.log) - 1) >> pl.log;
+  // four experts a load where no lane's run of them is cut and all are aligned
+  const bool vec = pl.per % 4 == 0 && p.size % 4 == 0 && p.ld % 4 == 0;
+  return vec ? launch_as<DT, true>(p, pl, stream) : launch_as<DT, false>(p, pl, stream);
 }
 
 cudaError_t launch_route_select(int dtype, const RouteParams& p, cudaStream_t stream) {

@@ -39,7 +39,7 @@ struct RouteParams {
   int32_t* ids;
   float* gates;
   long long ld;
-  int E, n_tok, top_k, gating, groups, keep, group_top, renorm;
+  int E, size, n_tok, top_k, gating, groups, keep, group_top, renorm;  // size: experts of a group
   float scale;
 #ifdef QMV_DEBUG
   unsigned* err;
@@ -83,7 +83,7 @@ struct LoraParams {
   long long a_len, b_len, y_len;
 #endif
 };
-int lora_splits(long long K, int n_tok);
+int lora_splits(long long K, int n_tok, int r);
 cudaError_t launch_lora(int dtype, LoraParams p, cudaStream_t stream);
 
 }  // namespace qmv

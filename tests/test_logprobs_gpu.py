@@ -3,8 +3,8 @@
 With s the sum over the row but for its largest term, in units of 2^-24: a term of
 s and of the entropy's sum is off by its exponent's three roundings (3 |d|, of which
 what counts is weighed by the term: at most 3 ln V on average over a sum) and ex2 (4); a
-thread adds V / 1024 of them in two chains, and some 30 more join the sums.  So s is
-off by N = V / 1024 + 3 * 18 + 40 units of itself, the log-sum-exp's log1p(s) by as much
+thread adds them in two chains of at most V / 512 (256 threads a row), and some 30
+more join the sums.  So s is off by N = V / 512 + 3 * 18 + 40 units of itself, the log-sum-exp's log1p(s) by as much
 of itself (and 2 for log1pf), the entropy by twice that of itself, a log probability by
 that and 3 units of the difference to the largest."""
 import numpy as np
@@ -28,7 +28,7 @@ def check(logits, tokens, n_top, scale=1.0):
         assert np.array_equal(got[3].cpu().numpy(), want[3])
     else:
         assert got[3] is None and got[4] is None
-    N = l.shape[1] / 1024 + 3 * 18 + 40
+    N = l.shape[1] / 512 + 3 * 18 + 40
     log_s = np.log1p(rest)
     for i in (0, 1, 2, 4):
         if got[i] is None:
