@@ -3,6 +3,7 @@
 #include <cfloat>
 #include <cmath>
 
+#include "float2.cuh"
 #include "float_io.cuh"
 #include "launch.h"
 #include "step_launch.h"
@@ -32,33 +33,6 @@ __device__ __forceinline__ float warp_max(float v) {
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
   return m;
 }
-// Two floats at once (packed fp32 arithmetic).
-struct F2 {
-  unsigned long long u;
-  __device__ __forceinline__ static F2 of(float x, float y) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(x), "f"(y));
-    return r;
-  }
-  __device__ __forceinline__ float x() const { return __uint_as_float((uint32_t)u); }
-  __device__ __forceinline__ float y() const { return __uint_as_float((uint32_t)(u >> 32)); }
-};
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-  return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
-  return r;
-}
-
 // 16 bytes of logits.
 template <int DT>
 struct LogitVec {
@@ -70,6 +44,27 @@ struct LogitVec {
     if constexpr (DT == QMV_DT_F32) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     if constexpr (DT == QMV_DT_BF16) return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     if constexpr (DT == QMV_DT_F16) return __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+  }
+  // The first of the values that equals m, if any, becomes -inf; true if there was one.
+  __device__ __forceinline__ bool leave_out(float m) {
+    uint32_t* const w[4] = {&raw.x, &raw.y, &raw.z, &raw.w};
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if constexpr (DT == QMV_DT_F32) {
+        const bool here = !found && __uint_as_float(*w[i]) == m;
+        if (here) *w[i] = 0xff800000u;
+        found |= here;
+      } else {
+        const float2 v = pair(i);
+        const uint32_t low = DT == QMV_DT_BF16 ? 0xff80u : 0xfc00u;
+        const bool a = !found && v.x == m, b = !found && !a && v.y == m;
+        if (a) *w[i] = (*w[i] & 0xffff0000u) | low;
+        if (b) *w[i] = (*w[i] & 0xffffu) | low << 16;
+        found |= a || b;
+      }
+    }
+    return found;
   }
   __device__ __forceinline__ void mask() {  // all -inf
     const uint32_t w = DT == QMV_DT_F32 ? 0xff800000u : DT == QMV_DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
@@ -145,16 +140,16 @@ __device__ __forceinline__ uint32_t peer(const void* here, int rank) {  // the s
 //
 // Bound by HBM for many rows: about 6 instructions a logit.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobsParams p, int ranks) {
+__global__ void __launch_bounds__(NT, NT == 512 ? 1 : 3) logprobs_kernel(const LogprobsParams p, int ranks) {
   using Vec = LogitVec<DT>;
   using T = typename Vec::T;
-  constexpr int N = Vec::N, WARPS = NT / 32, MAX_PARTS = (NT == 512 ? LP_MAX_CLUSTER : 1) * WARPS;
+  constexpr int N = Vec::N, WARPS = NT / 32, MAX_PARTS = (NT == 512 ? LP_MAX_CLUSTER : 2) * WARPS;
   __shared__ unsigned long long cand[LP_CAND];     // the first CTA's: the row's
   __shared__ float seg_max[LP_SEGS][NT];
   __shared__ LpPart parts[MAX_PARTS];              // the first CTA's: all warps'
   __shared__ float reach[MAX_PARTS];               // all warps' r-th largest thread maxima
   __shared__ int n_cand, n_again, again[NT];
-  __shared__ float s_floor;
+  __shared__ float s_floor, s_top, s_log;
   __shared__ unsigned long long w_best[WARPS];
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -162,7 +157,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobsP
   const long long r = ranks > 1 ? blockIdx.x / ranks : blockIdx.x;
   const int n_parts = ranks * WARPS;
   if (tid == 0) n_cand = n_again = 0;
-  if (ranks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
   const T* row = static_cast<const T*>(p.logits) + r * p.ld;
   // vectors of 16 aligned bytes; the first may begin before the row, the last end after it
@@ -206,8 +201,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobsP
   constexpr int STEP = NT * LP_UNROLL;
   const int steps = (v1 - v0 + STEP - 1) / STEP, per_seg = (steps + LP_SEGS - 1) / LP_SEGS;
   int seg = 0, in_seg = 0;
-  for (int v = v0 + tid; v - tid < v1; v += STEP) {
-    Vec x[LP_UNROLL];
+  auto fetch = [&](int v, Vec(&x)[LP_UNROLL]) {
     const int w = v - lane;  // the warp's first
     if (w >= whole0 && w + NT * (LP_UNROLL - 1) + 32 <= whole1 &&
         QMV_CHECK(in_range(r * p.ld + (long long)v * N - shift, (long long)NT * (LP_UNROLL - 1) * N + N, p.logits_len, p.err))) {
@@ -218,6 +212,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobsP
 #pragma unroll
       for (int u = 0; u < LP_UNROLL; u++) x[u] = load(v + u * NT, v1);
     }
+  };
+  Vec next[LP_UNROLL];
+  fetch(v0 + tid, next);
+#pragma unroll 2
+  for (int v = v0 + tid; v - tid < v1; v += STEP) {
+    Vec x[LP_UNROLL];
+#pragma unroll
+    for (int u = 0; u < LP_UNROLL; u++) x[u] = next[u];
+    fetch(v + STEP, next);  // (the next step's are on their way)
     const float bm = largest(x);
     mine = fmaxf(mine, bm);
     stretch = fmaxf(stretch, bm);
@@ -237,34 +240,25 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobsP
       S = f2 * S;
       m = now;
       out = true;
-      bool leave = lane == __ffs(__ballot_sync(0xffffffffu, bm == now)) - 1;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, bm == now)) - 1) {
+        bool left = false;
 #pragma unroll
-      for (int u = 0; u < LP_UNROLL; u++)
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-          const float2 two = x[u].pair(i / 2);
-          const float l = i & 1 ? two.y : two.x;
-          const float dl = at_least((l - m) * k, LP_LOWEST);
-          const bool skip = leave && l == m;
-          leave &= !skip;
-          const float e = skip ? 0.f : ex2(dl);
-          S = S + F2::of(e, 0.f);
-          D = fma2(F2::of(e, 0.f), F2::of(dl, 0.f), D);
-        }
-    } else {
-      const F2 m2 = F2::of(-m, -m);
-#pragma unroll
-      for (int u = 0; u < LP_UNROLL; u++)
-#pragma unroll
-        for (int i = 0; i < N / 2; i++) {
-          const float2 l = x[u].pair(i);
-          F2 d = (F2::of(l.x, l.y) + m2) * k2;
-          d = F2::of(at_least(d.x(), LP_LOWEST), at_least(d.y(), LP_LOWEST));
-          const F2 e = F2::of(ex2(d.x()), ex2(d.y()));
-          S = S + e;
-          D = fma2(e, d, D);
-        }
+        for (int u = 0; u < LP_UNROLL; u++)
+          if (!left) left = x[u].leave_out(now);
+      }
     }
+    const F2 m2 = F2::of(-m, -m);
+#pragma unroll
+    for (int u = 0; u < LP_UNROLL; u++)
+#pragma unroll
+      for (int i = 0; i < N / 2; i++) {
+        const float2 l = x[u].pair(i);
+        F2 d = (F2::of(l.x, l.y) + m2) * k2;
+        d = F2::of(at_least(d.x(), LP_LOWEST), at_least(d.y(), LP_LOWEST));
+        const F2 e = F2::of(ex2(d.x()), ex2(d.y()));
+        S = S + e;
+        D = fma2(e, d, D);
+      }
   }
   if (in_seg) seg_max[seg][tid] = stretch;
 
@@ -307,12 +301,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobsP
     __syncthreads();
   }
   if (n_top) {
-    // the floor: the nq-th largest of all warps' values (one of equal ones before the next)
-    if (tid < n_parts) {
-      const float v = reach[tid];
+    // The floor: the nq-th largest of all warps' values (one of equal ones before the
+    // next).  Four threads count for each.
+    if (tid < 4 * n_parts) {
+      const int of = tid >> 2, quarter = n_parts >> 2;  // (n_parts is a multiple of 8)
+      const float v = reach[of];
       int before = 0;
 #pragma unroll 8
-      for (int i = 0; i < n_parts; i++) before += reach[i] > v || (reach[i] == v && i < tid);
+      for (int j = 0; j < quarter; j++) {
+        const int i = 4 * j + (tid & 3);
+        before += reach[i] > v || (reach[i] == v && i < of);
+      }
+      before += __shfl_xor_sync(0xffffffffu, before, 1);
+      before += __shfl_xor_sync(0xffffffffu, before, 2);
       if (before == nq - 1) s_floor = v;
     }
     __syncthreads();
@@ -361,46 +362,59 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobsP
     }
   }
 
-  // The row's largest, s and t: the warps' in a fixed order, by every warp.
-  float top = -INFINITY;
-  for (int i = lane; i < n_parts; i += 32) top = fmaxf(top, parts[i].m);
-  top = warp_max(top);
-  int owner = n_parts;  // the warp whose largest stays out of s
-  for (int i = lane; i < n_parts; i += 32)
-    if (parts[i].m == top) owner = min(owner, i);
-  owner = __reduce_min_sync(0xffffffffu, owner);
-  float rs = 0.f, rt = 0.f;
-  for (int i = lane; i < n_parts; i += 32) {
-    const LpPart q = parts[i];
-    if (i == owner || !(q.m > -INFINITY)) {
-      rs += q.s;  // (0 or NaN where there is no logit)
-      rt += q.t;
-    } else {
-      const float d = at_least((q.m - top) * k, LP_LOWEST), f = ex2(d);
-      rs += f * (1.0f + q.s);
-      rt += f * (q.t + d * (1.0f + q.s));
-    }
-  }
+  // The row's largest, s and t: the warps' in a fixed order, by the first warp.
+  if (warp == 0) {
+    LpPart q[MAX_PARTS / 32 + (MAX_PARTS < 32)];
+    float top = -INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    rs += __shfl_xor_sync(0xffffffffu, rs, o);
-    rt += __shfl_xor_sync(0xffffffffu, rt, o);
-  }
-  if (top == INFINITY) rs = NAN;
-  const bool none = !(top > -INFINITY) && rs == rs;  // every logit is -inf
-  const float log_s = log1pf(rs);
-  auto logp = [&](float l) { return none ? -INFINITY : (l - top) * p.scale - log_s; };
-  if (tid == 0) {
-    if (QMV_CHECK(in_range(r, 1, p.rows_len, p.err))) {
-      if (p.lse) p.lse[r] = none ? -INFINITY : fmaf(top, p.scale, log_s);
-      if (p.entropy) p.entropy[r] = none ? 0.f : log_s - 0.6931471805599453f * rt / (1.0f + rs);
+    for (int j = 0; j < MAX_PARTS; j += 32) {
+      q[j / 32] = LpPart{-INFINITY, 0.f, 0.f};
+      if (j + lane < n_parts) q[j / 32] = parts[j + lane];
+      top = fmaxf(top, q[j / 32].m);
+    }
+    top = warp_max(top);
+    int owner = n_parts;  // the warp whose largest stays out of s
+#pragma unroll
+    for (int j = 0; j < MAX_PARTS; j += 32)
+      if (q[j / 32].m == top) owner = min(owner, j + lane);
+    owner = __reduce_min_sync(0xffffffffu, owner);
+    float rs = 0.f, rt = 0.f;
+#pragma unroll
+    for (int j = 0; j < MAX_PARTS; j += 32) {
+      const LpPart& of = q[j / 32];
+      if (j + lane == owner || !(of.m > -INFINITY)) {
+        rs += of.s;  // (0 or NaN where there is no logit)
+        rt += of.t;
+      } else {
+        const float d = at_least((of.m - top) * k, LP_LOWEST), f = ex2(d);
+        rs += f * (1.0f + of.s);
+        rt += f * (of.t + d * (1.0f + of.s));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      rs += __shfl_xor_sync(0xffffffffu, rs, o);
+      rt += __shfl_xor_sync(0xffffffffu, rt, o);
+    }
+    if (top == INFINITY) rs = NAN;
+    const bool none = !(top > -INFINITY) && rs == rs;  // every logit is -inf
+    const float log_s = log1pf(rs);
+    if (lane == 0) {
+      s_top = none ? 0.f : top;
+      s_log = none ? INFINITY : log_s;
+      if (QMV_CHECK(in_range(r, 1, p.rows_len, p.err))) {
+        if (p.lse) p.lse[r] = none ? -INFINITY : fmaf(top, p.scale, log_s);
+        if (p.entropy) p.entropy[r] = none ? 0.f : log_s - 0.6931471805599453f * rt / (1.0f + rs);
+      }
     }
   }
+  if (ranks > 1 && n_top) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __syncthreads();
+  const float top = s_top, log_s = s_log;  // (0 and inf where every logit is -inf: log probabilities are -inf)
+  auto logp = [&](float l) { return (l - top) * p.scale - log_s; };
   if (tid < p.n_given && QMV_CHECK(in_range(r * p.n_given + tid, 1, p.given_len, p.err)))
     p.logp[r * p.n_given + tid] = token < 0 ? 0.f : token >= p.V ? NAN : logp(given);
   if (!n_top) return;
-  if (ranks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  else __syncthreads();
   auto list = [&](int at, unsigned long long c) {
     if (QMV_CHECK(in_range(r * n_top + at, 1, p.top_len, p.err))) {
       p.top_ids[r * n_top + at] = c ? index_of(c) : -1;
@@ -456,12 +470,14 @@ static cudaError_t launch_as(const LogprobsParams& p, int ranks, cudaStream_t st
 
 template <int DT>
 static cudaError_t launch_dt(const LogprobsParams& p, cudaStream_t stream) {
-  // Few rows: a cluster each, while all of them still fit the GPU and a CTA keeps a
-  // round of loads of its own.
+  // Few rows: a cluster each, while CTAs have a round of loads each and all clusters
+  // find room at once (an SM a CTA, and clusters do not fill their part of the GPU:
+  // 16 rows in clusters of 4 9 us, of 8 12 us); up to a row an SM two smaller CTAs.
   const int round = 512 * LP_UNROLL * LogitVec<DT>::N / 2;
   int ranks = 1;
-  while (ranks < LP_MAX_CLUSTER && p.rows * ranks <= device_sm_count() && p.V > (long long)ranks * round) ranks *= 2;
-  return ranks > 1 ? launch_as<DT, 512>(p, ranks, stream) : launch_as<DT, 256>(p, ranks, stream);
+  while (ranks < LP_MAX_CLUSTER && 4 * p.rows * ranks <= device_sm_count() && p.V > (long long)ranks * round) ranks *= 2;
+  if (ranks > 1) return launch_as<DT, 512>(p, ranks, stream);
+  return launch_as<DT, 256>(p, p.rows <= device_sm_count() && p.V > round ? 2 : 1, stream);
 }
 
 cudaError_t launch_logprobs(int dtype, const LogprobsParams& p, cudaStream_t stream) {

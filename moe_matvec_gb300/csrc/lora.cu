@@ -37,19 +37,19 @@ __device__ __forceinline__ LoraTokens lora_tokens(const LoraParams& p) {
       id[i] = -1;
     }
   }
-  const int low = min(p.n_tok, 32);
-  for (int j = 0; j < low; j++) {  // tokens of the same adapter before the lane's
-    const int other = __shfl_sync(0xffffffffu, id[0], j);
-    before[0] += other == id[0] && j < lane;
-    before[1] += other == id[1];
+  // tokens of the same adapter before the lane's
+  const unsigned below = (1u << lane) - 1;
+  before[0] = __popc(__match_any_sync(0xffffffffu, id[0]) & below);
+  if (p.n_tok > 32) {
+    before[1] = __popc(__match_any_sync(0xffffffffu, id[1]) & below);
+#pragma unroll
+    for (int j = 0; j < 32; j++) before[1] += __shfl_sync(0xffffffffu, id[0], j) == id[1];
   }
-  for (int j = 32; j < p.n_tok; j++) before[1] += __shfl_sync(0xffffffffu, id[1], j - 32) == id[1] && j < lane + 32;
   const unsigned lead0 = __ballot_sync(0xffffffffu, lane < p.n_tok && before[0] % LORA_TOK == 0);
   const unsigned lead1 = __ballot_sync(0xffffffffu, lane + 32 < p.n_tok && before[1] % LORA_TOK == 0);
   const int first = __popc(lead0), groups = first + __popc(lead1);
   const int g = (int)blockIdx.x % groups;
   // the group's first token: the g-th of those that lead one
-  const unsigned below = (1u << lane) - 1;
   const unsigned at0 = __ballot_sync(0xffffffffu, (lead0 >> lane & 1) && __popc(lead0 & below) == g);
   const unsigned at1 = __ballot_sync(0xffffffffu, (lead1 >> lane & 1) && first + __popc(lead1 & below) == g);
   const int t = at0 ? __ffs(at0) - 1 : __ffs(at1) + 31;

@@ -1,4 +1,5 @@
 // Norm of each query and key head and the position rotation, in one pass.
+#include "float2.cuh"
 #include "float_io.cuh"
 #include "kv_cache.cuh"
 #include "launch.h"
@@ -8,8 +9,8 @@ namespace qmv {
 
 constexpr int ROPE_WARPS = 4;         // warps of a CTA, each on its own
 constexpr int ROPE_MAX_PAIRS = 128;   // head_dim 256
-constexpr int ROPE_AHEAD = 2;
-constexpr int ROPE_CTAS = 5;          // CTAs an SM
+constexpr int ROPE_AHEAD = 3;         // head groups of a warp on their way
+constexpr int ROPE_CTAS = 4;          // CTAs an SM (5: 20.0 us, 6 with 2 ahead 22.4, for 17.8)
 
 // A frequency (radians a position) in turns a position, as a fraction of 2^64: a
 // position times it, modulo 2^64, is the turn's fraction, whatever the position (in
@@ -28,6 +29,26 @@ __device__ __forceinline__ float2 turn_of(int pos, unsigned long long freq, floa
   sincospif((float)left * 0x1p-31f, &s, &c);
   return make_float2(c * scale, s * scale);
 }
+
+// One float or two at once.
+template <int W>
+struct Wide {
+  using type = float;
+  __device__ __forceinline__ static float of(const float* x) { return *x; }
+  __device__ __forceinline__ static float both(float x) { return x; }
+  __device__ __forceinline__ static float fma(float a, float b, float c) { return fmaf(a, b, c); }
+  __device__ __forceinline__ static float sum(float a) { return a; }
+  __device__ __forceinline__ static void to(float a, float* x) { *x = a; }
+};
+template <>
+struct Wide<2> {
+  using type = F2;
+  __device__ __forceinline__ static F2 of(const float* x) { return F2::of(x[0], x[1]); }
+  __device__ __forceinline__ static F2 both(float x) { return F2::of(x, x); }
+  __device__ __forceinline__ static F2 fma(F2 a, F2 b, F2 c) { return fma2(a, b, c); }
+  __device__ __forceinline__ static float sum(F2 a) { return a.x() + a.y(); }
+  __device__ __forceinline__ static void to(F2 a, float* x) { x[0] = a.x(), x[1] = a.y(); }
+};
 
 // The 2 CH consecutive values (a, b) of a unit whose pairs are neighbours: the
 // pairs' first values and their second ones, and back.
@@ -80,11 +101,22 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
   int todo = (int)(per + (w < rest));
   unsigned t = g0 / (unsigned)steps;
   int s0 = (int)(g0 - t * steps);
+  // the lane's pairs of the token's angles
   unsigned long long freq[ROPE_MAX_PAIRS / 32];
+  int axis[ROPE_MAX_PAIRS / 32];
 #pragma unroll
   for (int i = 0; i < ROPE_MAX_PAIRS / 32; i++) {
     freq[i] = 0;
-    if (32 * i < p.R / 2) freq[i] = turns_a_position(lane + 32 * i < p.R / 2 ? p.freq[lane + 32 * i] : 0.f);
+    axis[i] = 0;
+    if (32 * i < p.R / 2) {
+      const int pair = lane + 32 * i;
+      freq[i] = turns_a_position(pair < p.R / 2 ? p.freq[pair] : 0.f);
+      if (p.axis && pair < p.R / 2) axis[i] = p.axis[pair];
+      if (axis[i] >= p.n_axes) {
+        if (p.pos) set_error(p.err, QMV_DEVERR_BATCH);
+        axis[i] = 0;
+      }
+    }
   }
   // the lane's unit i, and the places of its two chunks in a head
   auto unit = [&](int i) { return li + (i << lph_log); };
@@ -122,17 +154,21 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
     }
   };
   const float inv_d = 1.0f / (float)p.D;
+  // (cleared once: lanes without a unit keep zeros, lanes without a head what they had,
+  // which goes nowhere)
+  Chunk ra[PF][UL], rb[PF][UL];
+#pragma unroll
+  for (int k = 0; k < PF; k++)
+#pragma unroll
+    for (int i = 0; i < UL; i++) ra[k][i].clear(), rb[k][i].clear();
   for (; todo > 0; t++, s0 = 0) {
     const int s1 = min(s0 + todo, steps);
     todo -= s1 - s0;
-    Chunk ra[PF][UL], rb[PF][UL];
     Cursor in = group(s0, false), out = group(s0, true);
     int ahead = s0;
     auto fetch = [&](Chunk(&xa)[UL], Chunk(&xb)[UL]) {
 #pragma unroll
       for (int i = 0; i < UL; i++) {
-        xa[i].clear();
-        xb[i].clear();
         QMV_DEBUG_ONLY(const RopeHeads& h = ahead < q_steps ? p.q : p.k; const long long at = in.x - static_cast<const T*>(h.x);)
         if (ahead < s1 && sub < in.left && unit(i) < units && QMV_CHECK(in_range(at + pa[i], CH, h.x_len, p.err)) &&
             QMV_CHECK(in_range(at + pb[i], CH, h.x_len, p.err))) {
@@ -163,22 +199,15 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
     for (int i = 0; i < ROPE_MAX_PAIRS / 32; i++) {
       const int pair = lane + 32 * i;
       if (pair >= p.R / 2) break;
-      int at = pos;
-      if (p.pos) {
-        int ax = p.axis ? p.axis[pair] : 0;
-        if (ax >= p.n_axes) {
-          set_error(p.err, QMV_DEVERR_BATCH);
-          ax = 0;
-        }
-        at = p.pos[(long long)t * p.n_axes + ax];
-      }
+      const int at = p.pos ? p.pos[(long long)t * p.n_axes + axis[i]] : pos;
       turns[wid][pair] = turn_of(at, freq[i], p.scale);
     }
     __syncwarp();
     // Pair (a, b) becomes rstd (a ca - b sb, b cb + a sa): cosines and sines times the
-    // weights of a and b.
-    constexpr int NP = UL * CH;
-    float ca[NP], sa[NP], cb[NP], sb[NP];
+    // weights of a and b (sb holds -sb).  Two pairs at once where a lane has more than one.
+    constexpr int NP = UL * CH, W = CH > 1 ? 2 : 1;
+    using V = typename Wide<W>::type;
+    V ca[NP / W], sa[NP / W], cb[NP / W], sb[NP / W];
     auto factors = [&](const float* w) {
 #pragma unroll
       for (int i = 0; i < UL; i++) {
@@ -196,11 +225,18 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
           }
           if (INTER && turn) to_pairs(wa, wb);
         }
+        float c[CH], n[CH];
 #pragma unroll
         for (int j = 0; j < CH; j++) {
           const float2 cs = turn ? turns[wid][unit(i) * CH + j] : make_float2(1.f, 0.f);
-          ca[i * CH + j] = cs.x * wa[j], sa[i * CH + j] = cs.y * wa[j];
-          cb[i * CH + j] = cs.x * wb[j], sb[i * CH + j] = cs.y * wb[j];
+          c[j] = cs.x, n[j] = cs.y;
+        }
+#pragma unroll
+        for (int j = 0; j < CH; j += W) {
+          const int e = (i * CH + j) / W;
+          const V a = Wide<W>::of(&wa[j]), b = Wide<W>::of(&wb[j]), co = Wide<W>::of(&c[j]), si = Wide<W>::of(&n[j]);
+          ca[e] = co * a, sa[e] = si * a;
+          cb[e] = co * b, sb[e] = Wide<W>::both(-1.f) * (si * b);
         }
       }
     };
@@ -211,43 +247,40 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
         if (s + k >= s1) break;
         if (s + k == q_steps && s + k > s0) factors(p.k.w);  // from queries to keys
         const bool norm = (s + k < q_steps ? p.q.w : p.k.w) != nullptr;
-        float va[NP], vb[NP];
+        V va[NP / W], vb[NP / W];
 #pragma unroll
         for (int i = 0; i < UL; i++) {
           float xa[CH], xb[CH];
           ra[k][i].to(xa);
           rb[k][i].to(xb);
+          if (INTER && unit(i) < turning) to_pairs(xa, xb);
 #pragma unroll
-          for (int j = 0; j < CH; j++) va[i * CH + j] = xa[j], vb[i * CH + j] = xb[j];
+          for (int j = 0; j < CH; j += W) va[(i * CH + j) / W] = Wide<W>::of(&xa[j]), vb[(i * CH + j) / W] = Wide<W>::of(&xb[j]);
         }
         fetch(ra[k], rb[k]);
-        float rstd = 1.f;
+        V rstd = Wide<W>::both(1.f);
         if (norm) {
-          float sum = 0.f, other = 0.f;
+          V one = Wide<W>::both(0.f), two = one;
 #pragma unroll
-          for (int i = 0; i < NP; i++) {
-            sum = fmaf(va[i], va[i], sum);
-            other = fmaf(vb[i], vb[i], other);
+          for (int i = 0; i < NP / W; i++) {
+            one = Wide<W>::fma(va[i], va[i], one);
+            two = Wide<W>::fma(vb[i], vb[i], two);
           }
-          sum += other;
+          float sum = Wide<W>::sum(one + two);
           for (int o = 1; o < 1 << lph_log; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          rstd = rsqrtf(fmaf(sum, inv_d, p.eps));  // at most 2 units in the last place off
+          rstd = Wide<W>::both(rsqrtf(fmaf(sum, inv_d, p.eps)));  // at most 2 units in the last place off
         }
 #pragma unroll
         for (int i = 0; i < UL; i++) {
           Chunk oa, ob;
-          float xa[CH], xb[CH], ya[CH], yb[CH];
+          float ya[CH], yb[CH];
 #pragma unroll
-          for (int j = 0; j < CH; j++) xa[j] = va[i * CH + j], xb[j] = vb[i * CH + j];
-          const bool next = INTER && unit(i) < turning;
-          if (next) to_pairs(xa, xb);
-#pragma unroll
-          for (int j = 0; j < CH; j++) {
-            const int e = i * CH + j;
-            ya[j] = rstd * (xa[j] * ca[e] - xb[j] * sb[e]);
-            yb[j] = rstd * (xb[j] * cb[e] + xa[j] * sa[e]);
+          for (int j = 0; j < CH; j += W) {
+            const int e = (i * CH + j) / W;
+            Wide<W>::to(rstd * Wide<W>::fma(vb[e], sb[e], va[e] * ca[e]), &ya[j]);
+            Wide<W>::to(rstd * Wide<W>::fma(va[e], sa[e], vb[e] * cb[e]), &yb[j]);
           }
-          if (next) from_pairs(ya, yb);
+          if (INTER && unit(i) < turning) from_pairs(ya, yb);
           oa.from(ya);
           ob.from(yb);
           QMV_DEBUG_ONLY(const RopeHeads& h = s + k < q_steps ? p.q : p.k; const long long at = out.x - static_cast<const T*>(h.y);)

@@ -11,6 +11,12 @@ namespace qmv {
 
 constexpr int ROUTE_WARPS = 4;  // tokens of a CTA
 
+__device__ __forceinline__ float rcp(float x) {  // 1 ulp
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Where a lane's experts lie: each group of gs experts is given to 2^log lanes,
 // `per` consecutive experts to each, so that lane order is expert order.
 struct RoutePlace {
@@ -146,23 +152,23 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
 //
 // Each lane has consecutive experts (lane order is expert order) and sorts their
 // keys: the places of c, or without a bias of the logits, in the order of real
-// numbers, whose lowest bits give way to the expert's slot in the lane.  A pick is
-// then the largest of the lanes' first keys, the first lane that has it, and a shift
-// of that lane's keys; lane k keeps pick k.
+// numbers, whose lowest bits (8 for 8 experts a lane) give way to the expert's lane
+// and slot, the first ones largest.  A pick is then the largest of the lanes' first
+// keys and a shift of the keys of the lane that has it; lane k keeps pick k.
 //
 // What is compared carries errors: those of fp32 (score and sum are within about
-// 2^-21 of s + |bias|; a logit is exact) and the slot's bits.  Where two compared
+// 2^-21 of s + |bias|; a logit is exact) and the bits given way (0 in logits of 16).  Where two compared
 // values at a border (kept and next group; consecutive picks and the first left out)
 // lie closer than that, what is in doubt is decided in 64 bits: the groups about the
 // border by their exact scores, the picks by the exact values of the picks and of
 // all experts that are as close after them, one a lane.  So the picks are those of 64
-// bits everywhere, at the cost of 64-bit arithmetic for about one token in a hundred.
+// bits everywhere, at the cost of 64-bit arithmetic for a few tokens in a hundred.
 //
 // Bound by instructions.
 template <int PER, int DT, bool VEC>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_select_kernel(const RouteParams p, const RoutePlace pl) {
   using T = typename Elem<DT>::type;
-  constexpr uint32_t SLOT = PER - 1;  // the bits of a slot
+  constexpr uint32_t PLACE = 32 * PER - 1;  // the bits of a lane and slot
   __shared__ float scores[ROUTE_WARPS][32 * PER];
   pdl_launch_dependents();
   pdl_wait();
@@ -215,11 +221,12 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_select_kernel(const Ro
 #pragma unroll
     for (int i = 0; i < PER; i++) {
       s[i] = tame(s[i]);
-      top = fmaxf(top, s[i]);
       if (!biased) key[i] = order_of(s[i]);
     }
     float inv = 1.f;  // scores are inv * s
     if (soft) {
+#pragma unroll
+      for (int i = 0; i < PER; i++) top = fmaxf(top, s[i]);
       top = value_of(__reduce_max_sync(0xffffffffu, order_of(top)));
       float total = 0.f;
 #pragma unroll
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_select_kernel(const Ro
       inv = total > 0.f ? 1.0f / total : 0.f;
     } else {
 #pragma unroll
-      for (int i = 0; i < PER; i++) s[i] = __fdividef(1.0f, 1.0f + expf(-s[i]));  // (2 ulp; -inf: 1 / inf = 0)
+      for (int i = 0; i < PER; i++) s[i] = rcp(1.0f + expf(-s[i]));  // (-inf: 1 / inf = 0)
     }
     float c[PER];
 #pragma unroll
@@ -282,6 +289,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_select_kernel(const Ro
       const float score = p.group_top == 2 ? one + two : one;
       const uint32_t mine = order_of(score + 0.0f);
       int before = 0;
+#pragma unroll 8
       for (int j = 0; j < p.groups; j++) {
         const uint32_t other = __shfl_sync(0xffffffffu, mine, j << pl.log);
         before += other > mine || (other == mine && j < g);
@@ -326,55 +334,52 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_select_kernel(const Ro
       }
     }
 #pragma unroll
-    for (int i = 0; i < PER; i++) key[i] = i < have && key[i] ? (key[i] & ~SLOT) | (SLOT - i) : 0;
+    for (int i = 0; i < PER; i++) key[i] = i < have && key[i] ? (key[i] & ~PLACE) | (PLACE - lane * PER - i) : 0;
     sort_down(key);
 
-    uint32_t picked = 0;  // lane k: pick k's key, and its expert's lane and slot
-    int from = 0;
-    auto pick = [&](int k, int deep) {  // (keys past `deep` are not asked for any more)
-      const uint32_t head = key[0] & ~SLOT, best = __reduce_max_sync(0xffffffffu, head);
-      const int of = __ffs(__ballot_sync(0xffffffffu, head == best)) - 1;
-      const int slot = SLOT - (__shfl_sync(0xffffffffu, key[0], of) & SLOT);
-      if (lane == k) {
-        picked = best;
-        from = of * PER + slot;
-      }
-      if (lane == of) {
+    uint32_t picked = 0;  // lane k: pick k's key
+    auto pick = [&](int k) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
+      if (lane == k) picked = best;
+      if (key[0] == best) {
 #pragma unroll
-        for (int i = 0; i < PER; i++)
-          if (i < deep) key[i] = i + 1 < PER ? key[i + 1] : 0;
+        for (int i = 0; i < PER; i++) key[i] = i + 1 < PER ? key[i + 1] : 0;
       }
     };
 #pragma unroll
     for (int k = 0; k < QMV_MAX_TOPK; k++)
-      if (k < p.top_k) pick(k, PER);
+      if (k < p.top_k) pick(k);
     // consecutive picks, and the last one and what comes after it
-    const uint32_t after = __reduce_max_sync(0xffffffffu, key[0] & ~SLOT);
+    const uint32_t after = __reduce_max_sync(0xffffffffu, key[0]);
     auto near = [&](uint32_t a, uint32_t b) {  // b is not above a
-      if (!biased) return DT == QMV_DT_F32 && a == b;  // (the slot's bits are 0 in logits of 16)
+      a &= ~PLACE, b &= ~PLACE;
+      if (!biased) return DT == QMV_DT_F32 && a == b;  // (logits of 16 bits are whole in their keys)
       const float x = value_of(a), y = value_of(b);
-      return close(x, y, (float)PER * 0x1p-23f * fmaxf(fabsf(x), fabsf(y)));
+      return close(x, y, (float)(32 * PER) * 0x1p-23f * fmaxf(fabsf(x), fabsf(y)));
     };
     uint32_t follower = __shfl_down_sync(0xffffffffu, picked, 1);
     if (lane == p.top_k - 1) follower = after;
     const bool doubt = __any_sync(0xffffffffu, lane < p.top_k && follower && near(picked, follower));
+    int from = PLACE - (picked & PLACE);  // lane k: pick k's lane and slot
     __syncwarp();
-    if (!doubt) {
-      const float score = lane < p.top_k ? scores[warp][from] : 0.f;
-      float sum = score;
+    const float held = lane < p.top_k ? scores[warp][from] : 0.f;
+    float of_all = held;
 #pragma unroll
-      for (int o = QMV_MAX_TOPK / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane < p.top_k)
-        put(p, t, lane, expert(from), (p.renorm ? (sum > 0.f ? score / sum : 0.f) : score * inv) * p.scale);
-      __syncwarp();  // (the scores are read)
+    for (int o = QMV_MAX_TOPK / 2; o > 0; o >>= 1) of_all += __shfl_xor_sync(0xffffffffu, of_all, o);
+    of_all = __shfl_sync(0xffffffffu, of_all, 0);
+    __syncwarp();  // (the scores are read)
+    // (scores down to 2^-126 are whole: smaller sums are formed anew)
+    if (!doubt && (!p.renorm || of_all >= 0x1p-60f)) {
+      if (lane < p.top_k) put(p, t, lane, expert(from), (p.renorm ? held / of_all : held * inv) * p.scale);
       continue;
     }
     int n = p.top_k;
     while (n < 32) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, key[0] & ~SLOT);
+      const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
       if (!best || !near(__shfl_sync(0xffffffffu, picked, n - 1), best)) break;
-      pick(n++, PER);
+      pick(n++);
     }
+    from = PLACE - (picked & PLACE);
     if (n == 32) {  // more than a warp can hold
       select_exactly<PER, T>(p, pl, t);
       continue;
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_select_kernel(const Ro
         v = exact(e, score);
       } else {
         v = tame(to_float(row[e]));
-        score = (double)scores[warp][from] * inv;
+        score = exact_score((float)v) * (double)inv;
       }
     }
     int before = 0;
