@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_down_kernel(cons
   const LoraTokens q = lora_tokens(p);
   if (q.n == 0 || q.a < 0) return;
   if (q.n == 1) lora_down<DT, 1>(p, q, lora_x);
+  else if (q.n == 2) lora_down<DT, 2>(p, q, lora_x);
   else lora_down<DT, LORA_TOK>(p, q, lora_x);
 }
 
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_up_kernel(const 
     return;
   }
   if (q.n == 1) lora_up<DT, VW, LPR_LOG, 1>(p, q, v, m0, rows);
+  else if (q.n == 2) lora_up<DT, VW, LPR_LOG, 2>(p, q, v, m0, rows);
   else lora_up<DT, VW, LPR_LOG, LORA_TOK>(p, q, v, m0, rows);
 }
 

@@ -166,7 +166,7 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
 //
 // Bound by instructions.
 template <int PER, int DT, bool VEC>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS) route_select_kernel(const RouteParams p, const RoutePlace pl) {
+__global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4 : 2) route_select_kernel(const RouteParams p, const RoutePlace pl) {
   using T = typename Elem<DT>::type;
   constexpr uint32_t PLACE = 32 * PER - 1;  // the bits of a lane and slot
   __shared__ float scores[ROUTE_WARPS][32 * PER];
@@ -412,8 +412,10 @@ template <int DT, bool VEC>
 static cudaError_t launch_as(const RouteParams& p, RoutePlace pl, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  // as many CTAs as the SMs hold at once (up to eights experts a lane); warps take tokens by turns
-  const int ctas = (p.n_tok + ROUTE_WARPS - 1) / ROUTE_WARPS, cap = 8 * device_sm_count();
+  // as many CTAs as the SMs hold at once (80 registers a thread with up to 8 experts a
+  // lane, 122, 208); warps take tokens by turns
+  const int ctas = (p.n_tok + ROUTE_WARPS - 1) / ROUTE_WARPS;
+  const int cap = (pl.per <= 8 ? 6 : pl.per <= 16 ? 4 : 2) * device_sm_count();
   make_config(cfg, attr, dim3((unsigned)(ctas < cap ? ctas : cap)), dim3(32 * ROUTE_WARPS), 0, stream, true);
   if (pl.per <= 4) return cudaLaunchKernelEx(&cfg, route_select_kernel<4, DT, VEC>, p, pl);
   if (pl.per <= 8) return cudaLaunchKernelEx(&cfg, route_select_kernel<8, DT, VEC>, p, pl);
