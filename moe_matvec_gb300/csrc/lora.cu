@@ -8,24 +8,25 @@ namespace qmv {
 
 constexpr int LORA_WARPS = 4, LORA_THREADS = 32 * LORA_WARPS;
 constexpr int LORA_CTAS = 4;     // CTAs an SM
+constexpr int LORA_CLUSTER = 8;  // CTAs of a cluster, where one launch does both products
 constexpr int LORA_TOK = 4;      // tokens of one adapter that a CTA takes
 constexpr int LORA_COLS = 8;     // consecutive columns a lane
 constexpr int LORA_WIN = 32 * LORA_COLS;
 constexpr int LORA_ROWS = 4;     // rows of A a warp holds sums for
 constexpr int LORA_SMS = 152;    // what the splits of the columns are made for (on any device: they decide the sums' order)
 
-// The tokens of one CTA: up to LORA_TOK with the same adapter, and what part of
-// their work is its own.  The tokens of each adapter (and those without one) form
-// groups of LORA_TOK in their order; the call's CTAs are dealt out to the groups,
+// The tokens of one CTA (or cluster): up to LORA_TOK with the same adapter, and what
+// part of their work is its own.  The tokens of each adapter (and those without one)
+// form groups of LORA_TOK in their order; the call's CTAs are dealt out to the groups,
 // which only the device knows.
 struct LoraTokens {
   int a;             // the adapter, -1: none
-  int n;             // 0: nothing left for this CTA
-  int part, parts;   // this CTA's part of its group's work
+  int n;             // 0: nothing left for it
+  int part, parts;   // its part of its group's work
   int tok[LORA_TOK];
 };
 // (every warp of a CTA comes by them alone: a lane has tokens `lane` and `lane` + 32)
-__device__ __forceinline__ LoraTokens lora_tokens(const LoraParams& p) {
+__device__ __forceinline__ LoraTokens lora_tokens(const LoraParams& p, int unit, int units) {
   const int lane = threadIdx.x & 31;
   int id[2], before[2] = {0, 0};
 #pragma unroll
@@ -33,7 +34,7 @@ __device__ __forceinline__ LoraTokens lora_tokens(const LoraParams& p) {
     const int k = lane + 32 * i;
     id[i] = k < p.n_tok ? __ldcg(p.ids + k) : -2;
     if (k < p.n_tok && (id[i] < 0 || id[i] >= p.n)) {
-      if (id[i] >= p.n && blockIdx.x == 0) set_error(p.err, QMV_DEVERR_ADAPTER);
+      if (id[i] >= p.n && unit == 0) set_error(p.err, QMV_DEVERR_ADAPTER);
       id[i] = -1;
     }
   }
@@ -48,15 +49,15 @@ __device__ __forceinline__ LoraTokens lora_tokens(const LoraParams& p) {
   const unsigned lead0 = __ballot_sync(0xffffffffu, lane < p.n_tok && before[0] % LORA_TOK == 0);
   const unsigned lead1 = __ballot_sync(0xffffffffu, lane + 32 < p.n_tok && before[1] % LORA_TOK == 0);
   const int first = __popc(lead0), groups = first + __popc(lead1);
-  const int g = (int)blockIdx.x % groups;
+  const int g = unit % groups;
   // the group's first token: the g-th of those that lead one
   const unsigned at0 = __ballot_sync(0xffffffffu, (lead0 >> lane & 1) && __popc(lead0 & below) == g);
   const unsigned at1 = __ballot_sync(0xffffffffu, (lead1 >> lane & 1) && first + __popc(lead1 & below) == g);
   const int t = at0 ? __ffs(at0) - 1 : __ffs(at1) + 31;
   LoraTokens q;
   q.a = __shfl_sync(0xffffffffu, t < 32 ? id[0] : id[1], t & 31);
-  q.part = (int)blockIdx.x / groups;
-  q.parts = (int)gridDim.x / groups;
+  q.part = unit / groups;
+  q.parts = units / groups;
   unsigned long long same = (unsigned long long)__ballot_sync(0xffffffffu, id[1] == q.a) << 32 |
                             __ballot_sync(0xffffffffu, id[0] == q.a);
   same &= ~0ull << t;
@@ -81,19 +82,19 @@ __device__ __forceinline__ int rank_of(const LoraParams& p, int a) {
 // units.  The four rows' sums for up to four tokens are added over the lanes
 // together (16 shuffles for 16 sums).  x of the CTA's tokens lies in shared memory.
 // Adapter rows are read once per four of its tokens.
-template <int DT, int NT>
-__device__ __forceinline__ void lora_down(const LoraParams& p, const LoraTokens& q, float* lora_x) {
+template <int DT, int NT, class Store>
+__device__ __forceinline__ void lora_down(const LoraParams& p, const LoraTokens& q, float* lora_x, int split, int nth,
+                                          int of, Store store) {
   using T = typename Elem<DT>::type;
   using Row = Packed<T, LORA_COLS>;
   constexpr int AHEAD = DT == QMV_DT_F32 ? 1 : 2;  // windows on their way: 4 KB a warp
   constexpr int SUMS = LORA_ROWS * NT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = rank_of(p, q.a);
-  // this CTA's split of the columns and run of units
-  const int split = q.part % p.splits, nth = q.part / p.splits, of = q.parts / p.splits;
+  // the nth of `of` runs of units
   const int units = (rank + LORA_ROWS - 1) / LORA_ROWS;
   const int u0 = units * nth / of, u1 = units * (nth + 1) / of;
-  if (nth >= of || u0 == u1) return;
+  if (nth >= of || u0 == u1) return;  // (the whole CTA)
   const int c0 = split * p.window, cols = min(p.window, p.K - c0), wins = (cols + LORA_WIN - 1) / LORA_WIN;
   const T* A = static_cast<const T*>(p.A) + (long long)q.a * p.r * p.K + c0 + lane * LORA_COLS;
   Row w[AHEAD][LORA_ROWS];
@@ -175,11 +176,7 @@ __device__ __forceinline__ void lora_down(const LoraParams& p, const LoraTokens&
       s[0] += __shfl_xor_sync(0xffffffffu, s[0], 16);
       constexpr int SHARE = 16 / SUMS;  // lanes that end with the same sum
       const int at = (lane & 15) / SHARE, j = unit * LORA_ROWS + at / NT, k = at % NT;
-      int tok = q.tok[0];
-#pragma unroll
-      for (int i = 1; i < NT; i++)
-        if (i == k) tok = q.tok[i];
-      if (lane < 16 && lane % SHARE == 0 && j < rank && k < q.n) p.part[((long long)split * p.n_tok + tok) * p.r + j] = s[0];
+      if (lane < 16 && lane % SHARE == 0 && j < rank && k < q.n) store(k, j, s[0]);
       win = 0;
       unit += LORA_WARPS;
 #pragma unroll
@@ -197,22 +194,30 @@ __global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_down_kernel(cons
   // before this call is done.
   pdl_wait();
   pdl_launch_dependents();
-  const LoraTokens q = lora_tokens(p);
+  const LoraTokens q = lora_tokens(p, blockIdx.x, gridDim.x);
   if (q.n == 0 || q.a < 0) return;
-  if (q.n == 1) lora_down<DT, 1>(p, q, lora_x);
-  else if (q.n == 2) lora_down<DT, 2>(p, q, lora_x);
-  else lora_down<DT, LORA_TOK>(p, q, lora_x);
+  const int split = q.part % p.splits, nth = q.part / p.splits, of = q.parts / p.splits;
+  auto store = [&](int k, int j, float sum) {
+    int tok = q.tok[0];
+#pragma unroll
+    for (int i = 1; i < LORA_TOK; i++)
+      if (i == k) tok = q.tok[i];
+    p.part[((long long)split * p.n_tok + tok) * p.r + j] = sum;
+  };
+  if (q.n == 1) lora_down<DT, 1>(p, q, lora_x, split, nth, of, store);
+  else if (q.n == 2) lora_down<DT, 2>(p, q, lora_x, split, nth, of, store);
+  else lora_down<DT, LORA_TOK>(p, q, lora_x, split, nth, of, store);
 }
 
-// y = res + scale B v: v's parts are added in order, then each warp goes through
-// rows of its own, eight loads of 16 bytes a lane on their way (the first ones
-// before the first kernel has finished).  A row of B lies with 2^lpr_log lanes, VW
+// y = res + scale B v: v's parts (part(k, j, s) once ready() returns) are added in
+// order, then each warp goes through rows of its own, eight loads of 16 bytes a lane on
+// their way (the first ones before ready()).  A row of B lies with 2^lpr_log lanes, VW
 // values each; the partial sums of `gather` loads are added over those lanes
 // together, so that afterwards each lane has one row's sum and up to 32 consecutive
 // rows of y and res are read and written at once.
-template <int DT, int VW, int LPR_LOG, int NT>
+template <int DT, int VW, int LPR_LOG, int NT, class Ready, class Part>
 __device__ __forceinline__ void lora_up(const LoraParams& p, const LoraTokens& q, float (&v)[LORA_TOK][QMV_MAX_RANK],
-                                        long long m0, int rows) {
+                                        long long m0, int rows, Ready ready, Part part) {
   using T = typename Elem<DT>::type;
   using Row = Packed<T, VW>;
   constexpr int LPR = 1 << LPR_LOG, RPL = 32 >> LPR_LOG;               // lanes a row, rows a load
@@ -233,19 +238,13 @@ __device__ __forceinline__ void lora_up(const LoraParams& p, const LoraTokens& q
 #pragma unroll
   for (int i = 0; i < LOADS; i++) fetch(w[i], B + i * step, i * RPL);
   const float scale = p.scales ? __ldcg(p.scales + q.a) : 1.0f;
-  pdl_wait();
+  ready();
   for (int i = tid; i < NT * p.r; i += LORA_THREADS) {
     const int k = i / p.r, j = i - k * p.r;
     float sum = 0.f;
     if (k < q.n && j < rank) {
-      int tok = q.tok[0];
-#pragma unroll
-      for (int o = 1; o < NT; o++)
-        if (o == k) tok = q.tok[o];
-      const float* part = p.part + (long long)tok * p.r + j;
-      const int stride = p.n_tok * p.r;
 #pragma unroll 8
-      for (int s = 0; s < p.splits; s++) sum += __ldcg(part + (long long)s * stride);
+      for (int s = 0; s < p.splits; s++) sum += part(k, j, s);
     }
     v[k][j] = sum * scale;
   }
@@ -310,30 +309,109 @@ __device__ __forceinline__ void lora_up(const LoraParams& p, const LoraTokens& q
   }
 }
 
+// The rows of a warp, `nth` of `of`: equal runs, multiples of 32.
+__device__ __forceinline__ int lora_rows(long long M, long long nth, long long of, long long& m0) {
+  const int per = (int)(((M + of - 1) / of + 31) / 32 * 32);
+  m0 = min(nth * per, M);
+  return (int)min((long long)per, M - m0);
+}
+// Rows of tokens without an adapter.
+__device__ __forceinline__ void lora_copy(const LoraParams& p, const LoraTokens& q, long long m0, int rows) {
+  if (p.y == p.res) return;
+#pragma unroll
+  for (int k = 0; k < LORA_TOK; k++)
+    if (k < q.n)
+      for (int m = threadIdx.x & 31; m < rows; m += 32)
+        if (QMV_CHECK(in_range(q.tok[k] * p.M + m0 + m, 1, p.y_len, p.err)))
+          p.y[q.tok[k] * p.M + m0 + m] = p.res[q.tok[k] * p.M + m0 + m];
+}
+
 template <int DT, int VW, int LPR_LOG>
 __global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_up_kernel(const LoraParams p) {
   __shared__ float v[LORA_TOK][QMV_MAX_RANK];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch_dependents();
-  const LoraTokens q = lora_tokens(p);
+  const LoraTokens q = lora_tokens(p, blockIdx.x, gridDim.x);
   if (q.n == 0) return;  // (more CTAs than the groups' parts)
-  // this warp's rows: equal runs of at least 32, a multiple of 32
-  const long long warps = (long long)q.parts * LORA_WARPS;
-  const int per = (int)(((p.M + warps - 1) / warps + 31) / 32 * 32);
-  const long long m0 = min(((long long)q.part * LORA_WARPS + warp) * per, p.M);
-  const int rows = (int)min((long long)per, p.M - m0);
-  if (q.a < 0) {  // no adapter
+  long long m0;
+  const int rows = lora_rows(p.M, (long long)q.part * LORA_WARPS + (threadIdx.x >> 5), (long long)q.parts * LORA_WARPS, m0);
+  if (q.a < 0) {
     pdl_wait();
-    if (p.y != p.res)
-      for (int k = 0; k < q.n; k++)
-        for (int m = lane; m < rows; m += 32)
-          if (QMV_CHECK(in_range(q.tok[k] * p.M + m0 + m, 1, p.y_len, p.err)))
-            p.y[q.tok[k] * p.M + m0 + m] = p.res[q.tok[k] * p.M + m0 + m];
+    lora_copy(p, q, m0, rows);
     return;
   }
-  if (q.n == 1) lora_up<DT, VW, LPR_LOG, 1>(p, q, v, m0, rows);
-  else if (q.n == 2) lora_up<DT, VW, LPR_LOG, 2>(p, q, v, m0, rows);
-  else lora_up<DT, VW, LPR_LOG, LORA_TOK>(p, q, v, m0, rows);
+  auto ready = [] { pdl_wait(); };
+  auto part = [&](int k, int j, int s) {
+    int tok = q.tok[0];
+#pragma unroll
+    for (int o = 1; o < LORA_TOK; o++)
+      if (o == k) tok = q.tok[o];
+    return __ldcg(p.part + ((long long)s * p.n_tok + tok) * p.r + j);
+  };
+  if (q.n == 1) lora_up<DT, VW, LPR_LOG, 1>(p, q, v, m0, rows, ready, part);
+  else if (q.n == 2) lora_up<DT, VW, LPR_LOG, 2>(p, q, v, m0, rows, ready, part);
+  else lora_up<DT, VW, LPR_LOG, LORA_TOK>(p, q, v, m0, rows, ready, part);
+}
+
+// Both products in one launch, for a few tokens: a cluster of eight CTAs forms a
+// group's v, a split of the columns each, every CTA's parts going to all of them
+// through shared memory, and then its part of the rows.  Several clusters of a group
+// form the same v, from L2.
+//
+// One token, rank 16, 4096 -> 4096: two launches took 4.2 us and 2.5 us more of the
+// host.
+template <int DT, int VW, int LPR_LOG, int NT>
+__device__ __forceinline__ void lora_both(const LoraParams& p, const LoraTokens& q, float* lora_x,
+                                          float (&v)[LORA_TOK][QMV_MAX_RANK],
+                                          float (&parts)[LORA_CLUSTER][LORA_TOK][QMV_MAX_RANK], int rank) {
+  auto store = [&](int k, int j, float sum) {
+#pragma unroll
+    for (int i = 0; i < LORA_CLUSTER; i++) {
+      uint32_t to;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&parts[rank][k][j])), "r"(i));
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(sum) : "memory");
+    }
+  };
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all CTAs are there
+  if (rank < p.splits) lora_down<DT, NT>(p, q, lora_x, rank, 0, 1, store);
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  long long m0;
+  const int rows = lora_rows(p.M, ((long long)q.part * LORA_CLUSTER + rank) * LORA_WARPS + (threadIdx.x >> 5),
+                             (long long)q.parts * LORA_CLUSTER * LORA_WARPS, m0);
+  auto ready = [] { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); };
+  auto part = [&](int k, int j, int s) { return parts[s][k][j]; };
+  lora_up<DT, VW, LPR_LOG, NT>(p, q, v, m0, rows, ready, part);
+}
+
+template <int DT, int VW, int LPR_LOG>
+__global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_both_kernel(const LoraParams p) {
+  extern __shared__ __align__(16) float lora_x[];  // [LORA_TOK][window]
+  __shared__ float v[LORA_TOK][QMV_MAX_RANK];
+  __shared__ float parts[LORA_CLUSTER][LORA_TOK][QMV_MAX_RANK];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int rank = (int)blockIdx.x % LORA_CLUSTER;
+  const LoraTokens q = lora_tokens(p, blockIdx.x / LORA_CLUSTER, gridDim.x / LORA_CLUSTER);
+  if (q.n == 0) return;  // (all CTAs of a cluster have the same tokens)
+  if (q.a < 0) {
+    long long m0;
+    const int rows = lora_rows(p.M, ((long long)q.part * LORA_CLUSTER + rank) * LORA_WARPS + (threadIdx.x >> 5),
+                               (long long)q.parts * LORA_CLUSTER * LORA_WARPS, m0);
+    lora_copy(p, q, m0, rows);
+    return;
+  }
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (q.n == 1) lora_both<DT, VW, LPR_LOG, 1>(p, q, lora_x, v, parts, rank);
+  else if (q.n == 2) lora_both<DT, VW, LPR_LOG, 2>(p, q, lora_x, v, parts, rank);
+  else lora_both<DT, VW, LPR_LOG, LORA_TOK>(p, q, lora_x, v, parts, rank);
+}
+
+// One launch for both products: where there are few tokens (clusters of four SMs each
+// then hold a group's work) and a cluster's share of A is small: at most 64 KB a CTA, and
+// x of four tokens beside the parts in 48 KB of shared memory.
+static bool lora_one_launch(long long K, int n_tok, int r, int dtype) {
+  const long long window = ((K + LORA_WIN - 1) / LORA_WIN + LORA_CLUSTER - 1) / LORA_CLUSTER * LORA_WIN;
+  return n_tok <= 8 && window <= 1536 && window * r * (dtype == QMV_DT_F32 ? 4 : 2) <= 65536;
 }
 
 // Columns of a split: windows of 256, at most 8 (x of four tokens in shared memory)
@@ -341,7 +419,9 @@ __global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_up_kernel(const 
 // Taken are those for which a warp has the fewest windows to go through, each token
 // taken to have an adapter of its own and its share of four CTAs an SM; fewer
 // splits among equals.
-static int lora_window(long long K, int n_tok, int r) {
+static int lora_window(long long K, int n_tok, int r, int dtype) {
+  if (lora_one_launch(K, n_tok, r, dtype))
+    return (int)(((K + LORA_WIN - 1) / LORA_WIN + LORA_CLUSTER - 1) / LORA_CLUSTER * LORA_WIN);
   const int wins = (int)((K + LORA_WIN - 1) / LORA_WIN), units = (r + LORA_ROWS - 1) / LORA_ROWS;
   const int parts = LORA_CTAS * LORA_SMS / n_tok;
   int best = 8, least = 0;
@@ -353,8 +433,8 @@ static int lora_window(long long K, int n_tok, int r) {
   }
   return best * LORA_WIN;
 }
-int lora_splits(long long K, int n_tok, int r) {
-  const int w = lora_window(K, n_tok, r);
+int lora_splits(long long K, int n_tok, int r, int dtype) {
+  const int w = lora_window(K, n_tok, r, dtype);
   return (int)((K + w - 1) / w);
 }
 
@@ -370,7 +450,21 @@ static unsigned lora_grid(const LoraParams& p, long long units, long long least)
 template <int DT, int VW, int LPR_LOG>
 static cudaError_t launch_up(const LoraParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  if (lora_one_launch(p.K, p.n_tok, p.r, DT)) {
+    // clusters: a warp for every 32 rows of each token, as many as the GPU holds at once
+    long long clusters = (p.M + 32 * LORA_WARPS * LORA_CLUSTER - 1) / (32 * LORA_WARPS * LORA_CLUSTER) * p.n_tok;
+    const long long cap = (long long)LORA_CTAS * device_sm_count() / LORA_CLUSTER;
+    if (clusters > cap) clusters = cap;
+    make_config(cfg, attr, dim3((unsigned)(clusters * LORA_CLUSTER)), dim3(LORA_THREADS),
+                (size_t)LORA_TOK * p.window * sizeof(float), stream, true);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = LORA_CLUSTER;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, lora_both_kernel<DT, VW, LPR_LOG>, p);
+  }
   make_config(cfg, attr, dim3(lora_grid(p, (p.M + 32 * LORA_WARPS - 1) / (32 * LORA_WARPS), 1)), dim3(LORA_THREADS), 0, stream,
               true);
   return cudaLaunchKernelEx(&cfg, lora_up_kernel<DT, VW, LPR_LOG>, p);
@@ -388,22 +482,29 @@ static cudaError_t launch_vw(const LoraParams& p, cudaStream_t stream) {
 }
 
 template <int DT>
-static cudaError_t launch_dt(const LoraParams& p, cudaStream_t stream) {
+static cudaError_t launch_down(const LoraParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   const long long units = (p.r + LORA_WARPS * LORA_ROWS - 1) / (LORA_WARPS * LORA_ROWS);
   make_config(cfg, attr, dim3(lora_grid(p, p.splits * units, p.splits)), dim3(LORA_THREADS),
               (size_t)LORA_TOK * p.window * sizeof(float), stream, true);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_down_kernel<DT>, p);
-  if (e != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, lora_down_kernel<DT>, p);
+}
+
+template <int DT>
+static cudaError_t launch_dt(const LoraParams& p, cudaStream_t stream) {
+  if (!lora_one_launch(p.K, p.n_tok, p.r, DT)) {
+    const cudaError_t e = launch_down<DT>(p, stream);
+    if (e != cudaSuccess) return e;
+  }
   if constexpr (DT != QMV_DT_F32)
     if (p.r % 8 == 0) return launch_vw<DT, 8>(p, stream);
   return launch_vw<DT, 4>(p, stream);
 }
 
 cudaError_t launch_lora(int dtype, LoraParams p, cudaStream_t stream) {
-  p.window = lora_window(p.K, p.n_tok, p.r);
-  p.splits = lora_splits(p.K, p.n_tok, p.r);
+  p.window = lora_window(p.K, p.n_tok, p.r, dtype);
+  p.splits = lora_splits(p.K, p.n_tok, p.r, dtype);
   switch (dtype) {
     case QMV_DT_F16: return launch_dt<QMV_DT_F16>(p, stream);
     case QMV_DT_BF16: return launch_dt<QMV_DT_BF16>(p, stream);

@@ -95,7 +95,7 @@ int qmv_norm_rope(const qmv_rope* rope, int dtype, const void* q, int64_t q_stri
 
 size_t qmv_lora_workspace_bytes(const qmv_lora* l, int64_t K, int n_tok) {
   if (check_lora(l, K, n_tok)) return 0;
-  return (size_t)lora_splits(K, n_tok, l->rank) * n_tok * l->rank * sizeof(float);
+  return (size_t)lora_splits(K, n_tok, l->rank, l->dtype) * n_tok * l->rank * sizeof(float);
 }
 
 int qmv_lora_run(const qmv_lora* l, const int32_t* ids, const float* x, const float* res, float* y, int64_t K, int64_t M,

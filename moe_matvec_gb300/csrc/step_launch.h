@@ -83,7 +83,7 @@ struct LoraParams {
   long long a_len, b_len, y_len;
 #endif
 };
-int lora_splits(long long K, int n_tok, int r);
+int lora_splits(long long K, int n_tok, int r, int dtype);
 cudaError_t launch_lora(int dtype, LoraParams p, cudaStream_t stream);
 
 }  // namespace qmv
