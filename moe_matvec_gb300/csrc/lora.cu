@@ -126,7 +126,9 @@ __device__ __forceinline__ void lora_down(const LoraParams& p, const LoraTokens&
     for (int k = 0; k < NT; k++)
       if (k < q.n)
         *reinterpret_cast<float4*>(lora_x + k * p.window + i) =
-            i < cols ? *reinterpret_cast<const float4*>(p.x + (long long)q.tok[k] * p.K + c0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            i < cols && QMV_CHECK(in_range((long long)q.tok[k] * p.K + c0 + i, 4, p.x_len, p.err))
+                ? *reinterpret_cast<const float4*>(p.x + (long long)q.tok[k] * p.K + c0 + i)
+                : make_float4(0.f, 0.f, 0.f, 0.f);
   __syncthreads();
   int win = 0, unit = u0 + warp;
   float acc[LORA_ROWS][NT];
@@ -202,7 +204,8 @@ __global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_down_kernel(cons
 #pragma unroll
     for (int i = 1; i < LORA_TOK; i++)
       if (i == k) tok = q.tok[i];
-    p.part[((long long)split * p.n_tok + tok) * p.r + j] = sum;
+    const long long at = ((long long)split * p.n_tok + tok) * p.r + j;
+    if (QMV_CHECK(in_range(at, 1, p.part_len, p.err))) p.part[at] = sum;
   };
   if (q.n == 1) lora_down<DT, 1>(p, q, lora_x, split, nth, of, store);
   else if (q.n == 2) lora_down<DT, 2>(p, q, lora_x, split, nth, of, store);
@@ -272,7 +275,8 @@ __device__ __forceinline__ void lora_up(const LoraParams& p, const LoraTokens& q
       const int row = m + g * BLOCK;
       const bool here = writer && row + mine < rows;
 #pragma unroll
-      for (int k = 0; k < NT; k++) r[k] = here && k < q.n ? res[k][row] : 0.f;
+      for (int k = 0; k < NT; k++)
+        r[k] = here && k < q.n && QMV_CHECK(in_range(res[k] + row - p.res, 1, p.n_tok * p.M, p.err)) ? res[k][row] : 0.f;
 #pragma unroll
       for (int i = 0; i < GATHER; i++) {
         float b[VW];
@@ -345,7 +349,8 @@ __global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_up_kernel(const 
 #pragma unroll
     for (int o = 1; o < LORA_TOK; o++)
       if (o == k) tok = q.tok[o];
-    return __ldcg(p.part + ((long long)s * p.n_tok + tok) * p.r + j);
+    const long long at = ((long long)s * p.n_tok + tok) * p.r + j;
+    return QMV_CHECK(in_range(at, 1, p.part_len, p.err)) ? __ldcg(p.part + at) : 0.f;
   };
   if (q.n == 1) lora_up<DT, VW, LPR_LOG, 1>(p, q, v, m0, rows, ready, part);
   else if (q.n == 2) lora_up<DT, VW, LPR_LOG, 2>(p, q, v, m0, rows, ready, part);

@@ -170,10 +170,9 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
 #pragma unroll
       for (int i = 0; i < UL; i++) {
         QMV_DEBUG_ONLY(const RopeHeads& h = ahead < q_steps ? p.q : p.k; const long long at = in.x - static_cast<const T*>(h.x);)
-        if (ahead < s1 && sub < in.left && unit(i) < units && QMV_CHECK(in_range(at + pa[i], CH, h.x_len, p.err)) &&
-            QMV_CHECK(in_range(at + pb[i], CH, h.x_len, p.err))) {
-          xa[i].load(in.x + pa[i]);
-          xb[i].load(in.x + pb[i]);
+        if (ahead < s1 && sub < in.left && unit(i) < units) {
+          if (QMV_CHECK(in_range(at + pa[i], CH, h.x_len, p.err))) xa[i].load(in.x + pa[i]);
+          if (QMV_CHECK(in_range(at + pb[i], CH, h.x_len, p.err))) xb[i].load(in.x + pb[i]);
         }
       }
       advance(in, ++ahead, false);
@@ -284,10 +283,9 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
           oa.from(ya);
           ob.from(yb);
           QMV_DEBUG_ONLY(const RopeHeads& h = s + k < q_steps ? p.q : p.k; const long long at = out.x - static_cast<const T*>(h.y);)
-          if (sub < out.left && unit(i) < units && QMV_CHECK(in_range(at + pa[i], CH, h.y_len, p.err)) &&
-              QMV_CHECK(in_range(at + pb[i], CH, h.y_len, p.err))) {
-            oa.store(out.x + pa[i]);
-            ob.store(out.x + pb[i]);
+          if (sub < out.left && unit(i) < units) {
+            if (QMV_CHECK(in_range(at + pa[i], CH, h.y_len, p.err))) oa.store(out.x + pa[i]);
+            if (QMV_CHECK(in_range(at + pb[i], CH, h.y_len, p.err))) ob.store(out.x + pb[i]);
           }
         }
         advance(out, s + k + 1, true);

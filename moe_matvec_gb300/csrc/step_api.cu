@@ -126,6 +126,7 @@ int qmv_lora_run(const qmv_lora* l, const int32_t* ids, const float* x, const fl
   p.n_tok = n_tok;
   p.err = device_error_word();
   QMV_DEBUG_ONLY(p.a_len = (long long)p.n * p.r * K; p.b_len = (long long)p.n * p.r * M;
+                 p.x_len = n_tok * K; p.part_len = (long long)qmv_lora_workspace_bytes(l, K, n_tok) / 4;
                  p.y_len = output_extent(n_tok * M);)
   return status(launch_lora(l->dtype, p, stream));
 }

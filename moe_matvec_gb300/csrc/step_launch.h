@@ -80,7 +80,7 @@ struct LoraParams {
   int K, n, r, n_tok, splits, window;  // window: columns of a split
   unsigned* err;
 #ifdef QMV_DEBUG
-  long long a_len, b_len, y_len;
+  long long a_len, b_len, x_len, part_len, y_len;
 #endif
 };
 int lora_splits(long long K, int n_tok, int r, int dtype);
