@@ -21,6 +21,7 @@ constexpr int LORA_SMS = 152;    // what the splits of the columns are made for 
 // which only the device knows.
 struct LoraTokens {
   int a;             // the adapter, -1: none
+  int rank;          // how much of it counts
   int n;             // 0: nothing left for it
   int part, parts;   // its part of its group's work
   int tok[LORA_TOK];
@@ -38,6 +39,10 @@ __device__ __forceinline__ LoraTokens lora_tokens(const LoraParams& p, int unit,
       id[i] = -1;
     }
   }
+  // (the ranks travel while the groups are formed)
+  int rank[2];
+#pragma unroll
+  for (int i = 0; i < 2; i++) rank[i] = id[i] >= 0 && p.ranks ? __ldcg(p.ranks + id[i]) : p.r;
   // tokens of the same adapter before the lane's
   const unsigned below = (1u << lane) - 1;
   before[0] = __popc(__match_any_sync(0xffffffffu, id[0]) & below);
@@ -69,12 +74,9 @@ __device__ __forceinline__ LoraTokens lora_tokens(const LoraParams& p, int unit,
     same &= same - 1;
   }
   if (q.part >= q.parts) q.n = 0;
+  q.rank = min(max(__shfl_sync(0xffffffffu, t < 32 ? rank[0] : rank[1], t & 31), 0), p.r);
   return q;
 }
-__device__ __forceinline__ int rank_of(const LoraParams& p, int a) {
-  return p.ranks ? min(max(__ldcg(p.ranks + a), 0), p.r) : p.r;
-}
-
 // v = A x: part[split][token][row], each over one split of the columns.  The work
 // of a group of tokens is (split, four rows) units; a CTA takes a run of rows of one
 // split, a warp every fourth unit of it, and a lane has 8 columns of each window of
@@ -90,7 +92,7 @@ __device__ __forceinline__ void lora_down(const LoraParams& p, const LoraTokens&
   constexpr int AHEAD = DT == QMV_DT_F32 ? 1 : 2;  // windows on their way: 4 KB a warp
   constexpr int SUMS = LORA_ROWS * NT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = rank_of(p, q.a);
+  const int rank = q.rank;
   // the nth of `of` runs of units
   const int units = (rank + LORA_ROWS - 1) / LORA_ROWS;
   const int u0 = units * nth / of, u1 = units * (nth + 1) / of;
@@ -227,7 +229,7 @@ __device__ __forceinline__ void lora_up(const LoraParams& p, const LoraTokens& q
   constexpr int GATHER_LOG = LPR_LOG < 3 ? LPR_LOG : 3, GATHER = 1 << GATHER_LOG;
   constexpr int LOADS = 8, BLOCK = GATHER * RPL;                       // rows whose sums are gathered at once
   const int tid = threadIdx.x, lane = tid & 31;
-  const int rank = rank_of(p, q.a);
+  const int rank = q.rank;
   const int li = lane & (LPR - 1), j0 = li * VW, sub = lane >> LPR_LOG;
   const bool ragged = rank % VW != 0;  // a lane's values may end at the rank
   const T* B = static_cast<const T*>(p.B) + ((long long)q.a * p.M + m0 + sub) * p.r + j0;

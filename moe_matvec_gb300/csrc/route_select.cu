@@ -165,7 +165,7 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
 // bits everywhere, at the cost of 64-bit arithmetic for a few tokens in a hundred.
 //
 // Bound by instructions.
-template <int PER, int DT, bool VEC>
+template <int PER, int DT, bool VEC, bool FULL>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4 : 2) route_select_kernel(const RouteParams p, const RoutePlace pl) {
   using T = typename Elem<DT>::type;
   constexpr uint32_t PLACE = 32 * PER - 1;  // the bits of a lane and slot
@@ -174,9 +174,9 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lpg = 1 << pl.log, gs = p.size, g = lane >> pl.log;
-  const int first = (lane & (lpg - 1)) * pl.per;
-  const int have = g < p.groups ? max(0, min(pl.per, gs - first)) : 0;
-  const int e0 = g * gs + first;
+  const int per = FULL ? PER : pl.per, first = (lane & (lpg - 1)) * per;
+  const int have = FULL ? PER : g < p.groups ? max(0, min(per, gs - first)) : 0;
+  const int e0 = FULL ? lane * PER : g * gs + first;
   const bool soft = p.gating == QMV_GATING_SOFTMAX, biased = p.bias != nullptr;
   float bias[PER], widest = 0.f;
 #pragma unroll
@@ -194,8 +194,9 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
   };
   auto expert = [&](int f) {  // of lane f / PER, slot f % PER
     const int of = f / PER;
-    return (of >> pl.log) * gs + (of & (lpg - 1)) * pl.per + f % PER;
+    return FULL ? f : (of >> pl.log) * gs + (of & (lpg - 1)) * per + f % PER;
   };
+  auto placed = [&](float v, int i) { return i < have ? (order_of(v) & ~PLACE) | (PLACE - lane * PER - i) : 0u; };
   for (int t = blockIdx.x * ROUTE_WARPS + warp; t < p.n_tok; t += gridDim.x * ROUTE_WARPS) {
     const T* row = static_cast<const T*>(p.logits) + (long long)t * p.ld;
     float s[PER];
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
 #pragma unroll
     for (int i = 0; i < PER; i++) {
       s[i] = tame(s[i]);
-      if (!biased) key[i] = order_of(s[i]);
+      if (!biased) key[i] = placed(s[i], i);
     }
     float inv = 1.f;  // scores are inv * s
     if (soft) {
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
     for (int i = 0; i < PER; i++) {
       scores[warp][lane * PER + i] = s[i];
       c[i] = fmaf(s[i], inv, bias[i]);
-      if (biased) key[i] = order_of(c[i]);
+      if (biased) key[i] = placed(c[i], i);
     }
 
     // Exact values, by the whole warp where something is in doubt.  Scores of a softmax
@@ -333,8 +334,6 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
         for (int i = 0; i < PER; i++) key[i] = 0;
       }
     }
-#pragma unroll
-    for (int i = 0; i < PER; i++) key[i] = i < have && key[i] ? (key[i] & ~PLACE) | (PLACE - lane * PER - i) : 0;
     sort_down(key);
 
     uint32_t picked = 0;  // lane k: pick k's key
@@ -417,10 +416,18 @@ static cudaError_t launch_as(const RouteParams& p, RoutePlace pl, cudaStream_t s
   const int ctas = (p.n_tok + ROUTE_WARPS - 1) / ROUTE_WARPS;
   const int cap = (pl.per <= 8 ? 6 : pl.per <= 16 ? 4 : 2) * device_sm_count();
   make_config(cfg, attr, dim3((unsigned)(ctas < cap ? ctas : cap)), dim3(32 * ROUTE_WARPS), 0, stream, true);
-  if (pl.per <= 4) return cudaLaunchKernelEx(&cfg, route_select_kernel<4, DT, VEC>, p, pl);
-  if (pl.per <= 8) return cudaLaunchKernelEx(&cfg, route_select_kernel<8, DT, VEC>, p, pl);
-  if (pl.per <= 16) return cudaLaunchKernelEx(&cfg, route_select_kernel<16, DT, VEC>, p, pl);
-  return cudaLaunchKernelEx(&cfg, route_select_kernel<32, DT, VEC>, p, pl);
+  if constexpr (VEC) {
+    // every lane full (128, 256, 512 experts in 1, 2, 4 .. groups): nothing to ask for
+    if (p.groups << pl.log == 32 && p.size == pl.per << pl.log) {
+      if (pl.per == 4) return cudaLaunchKernelEx(&cfg, route_select_kernel<4, DT, true, true>, p, pl);
+      if (pl.per == 8) return cudaLaunchKernelEx(&cfg, route_select_kernel<8, DT, true, true>, p, pl);
+      if (pl.per == 16) return cudaLaunchKernelEx(&cfg, route_select_kernel<16, DT, true, true>, p, pl);
+    }
+  }
+  if (pl.per <= 4) return cudaLaunchKernelEx(&cfg, route_select_kernel<4, DT, VEC, false>, p, pl);
+  if (pl.per <= 8) return cudaLaunchKernelEx(&cfg, route_select_kernel<8, DT, VEC, false>, p, pl);
+  if (pl.per <= 16) return cudaLaunchKernelEx(&cfg, route_select_kernel<16, DT, VEC, false>, p, pl);
+  return cudaLaunchKernelEx(&cfg, route_select_kernel<32, DT, VEC, false>, p, pl);
 }
 
 template <int DT>
