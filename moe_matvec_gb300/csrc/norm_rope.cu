@@ -73,7 +73,7 @@ __device__ __forceinline__ void from_pairs(float (&a)[CH], float (&b)[CH]) {
 // the first R values becomes (a cos - b sin, b cos + a sin).
 //
 // A head is D / (2 CH) units of two chunks of CH consecutive values, one unit a
-// lane (UL units for CH = 1): the two halves of CH pairs (pair i: values i and
+// lane (up to UL units for short chunks): the two halves of CH pairs (pair i: values i and
 // i + R / 2), or 2 CH consecutive values (pair i: 2i, 2i + 1), or two chunks
 // that do not turn.  So a lane holds whole pairs, the norm is a sum over the
 // head's lanes, and the same lane has the same pairs in every head: the products
@@ -84,11 +84,11 @@ __device__ __forceinline__ void from_pairs(float (&a)[CH], float (&b)[CH]) {
 //
 // Bound by HBM for many tokens.
 template <int DT, int CH, int UL, bool INTER>
-__global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
+__global__ void __launch_bounds__(32 * ROPE_WARPS, UL <= 2 ? ROPE_CTAS : 3)
     norm_rope_kernel(const RopeParams p, int lph_log, unsigned per, unsigned rest) {
   using T = typename Elem<DT>::type;
   using Chunk = Packed<T, CH>;
-  constexpr int PF = UL == 1 ? ROPE_AHEAD : 1;  // head groups on their way
+  constexpr int PF = UL == 1 ? ROPE_AHEAD : UL == 2 ? 2 : 1;  // head groups on their way
   __shared__ float2 turns[ROPE_WARPS][ROPE_MAX_PAIRS];
   pdl_launch_dependents();
   pdl_wait();
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
     auto factors = [&](const float* w) {
 #pragma unroll
       for (int i = 0; i < UL; i++) {
-        const bool turn = unit(i) < turning;
+        const int pair0 = unit(i) * CH;  // pairs below R / 2 turn (whole units but where pairs are neighbours)
         float wa[CH], wb[CH];
 #pragma unroll
         for (int j = 0; j < CH; j++) wa[j] = wb[j] = 1.f;
@@ -222,12 +222,12 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
             wa[0] = w[pa[i]];
             wb[0] = w[pb[i]];
           }
-          if (INTER && turn) to_pairs(wa, wb);
+          if (INTER) to_pairs(wa, wb);
         }
         float c[CH], n[CH];
 #pragma unroll
         for (int j = 0; j < CH; j++) {
-          const float2 cs = turn ? turns[wid][unit(i) * CH + j] : make_float2(1.f, 0.f);
+          const float2 cs = pair0 + j < p.R / 2 ? turns[wid][pair0 + j] : make_float2(1.f, 0.f);
           c[j] = cs.x, n[j] = cs.y;
         }
 #pragma unroll
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
           float xa[CH], xb[CH];
           ra[k][i].to(xa);
           rb[k][i].to(xb);
-          if (INTER && unit(i) < turning) to_pairs(xa, xb);
+          if (INTER) to_pairs(xa, xb);
 #pragma unroll
           for (int j = 0; j < CH; j += W) va[(i * CH + j) / W] = Wide<W>::of(&xa[j]), vb[(i * CH + j) / W] = Wide<W>::of(&xb[j]);
         }
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL == 1 ? ROPE_CTAS : 3)
             Wide<W>::to(rstd * Wide<W>::fma(vb[e], sb[e], va[e] * ca[e]), &ya[j]);
             Wide<W>::to(rstd * Wide<W>::fma(va[e], sa[e], vb[e] * cb[e]), &yb[j]);
           }
-          if (INTER && unit(i) < turning) from_pairs(ya, yb);
+          if (INTER) from_pairs(ya, yb);
           oa.from(ya);
           ob.from(yb);
           QMV_DEBUG_ONLY(const RopeHeads& h = s + k < q_steps ? p.q : p.k; const long long at = out.x - static_cast<const T*>(h.y);)
@@ -303,7 +303,7 @@ static cudaError_t launch_as(bool interleaved, const RopeParams& p, cudaStream_t
   const int steps = (p.q.n + hpw - 1) / hpw + (p.k.n + hpw - 1) / hpw;
   // As many warps as the GPU holds at once, or a group of heads each.
   const long long total = (long long)p.n_tok * steps, ctas = (total + ROPE_WARPS - 1) / ROPE_WARPS;
-  const long long cap = (long long)(UL == 1 ? ROPE_CTAS : 3) * device_sm_count();
+  const long long cap = (long long)(UL <= 2 ? ROPE_CTAS : 3) * device_sm_count();
   const unsigned grid = (unsigned)(ctas < cap ? ctas : cap);
   const unsigned per = (unsigned)(total / (grid * ROPE_WARPS)), rest = (unsigned)(total % (grid * ROPE_WARPS));
   cudaLaunchConfig_t cfg;
@@ -313,14 +313,18 @@ static cudaError_t launch_as(bool interleaved, const RopeParams& p, cudaStream_t
   return cudaLaunchKernelEx(&cfg, norm_rope_kernel<DT, CH, UL, false>, p, log, per, rest);
 }
 
-// Chunks of 16 bytes where whole ones pair up (of 8 for 16-bit types whose sizes
-// leave that), else single values.
+// Chunks of 16 bytes where whole ones pair up, else shorter ones, down to single
+// values (4096 x 40 heads of 128 bfloat16, the halves of R values as pairs: R 128 18 us,
+// 120 23, 124 and 126 42).  Where pairs are neighbours only the head's size counts.
 template <int DT>
 static cudaError_t launch_dt(bool interleaved, const RopeParams& p, cudaStream_t stream) {
+  const int R = interleaved ? 0 : p.R;
   if constexpr (DT != QMV_DT_F32)
-    if (p.D % 16 == 0 && p.R % 16 == 0) return launch_as<DT, 8, 1>(interleaved, p, stream);
-  if (p.D % 8 == 0 && p.R % 8 == 0) return launch_as<DT, 4, 1>(interleaved, p, stream);
-  return launch_as<DT, 1, 4>(interleaved, p, stream);
+    if (p.D % 16 == 0 && R % 16 == 0) return launch_as<DT, 8, 1>(interleaved, p, stream);
+  if (p.D % 8 == 0 && R % 8 == 0) return launch_as<DT, 4, 1>(interleaved, p, stream);
+  if (p.D % 4 == 0 && R % 4 == 0)
+    return p.D <= 128 ? launch_as<DT, 2, 1>(interleaved, p, stream) : launch_as<DT, 2, 2>(interleaved, p, stream);
+  return p.D <= 128 ? launch_as<DT, 1, 2>(interleaved, p, stream) : launch_as<DT, 1, 4>(interleaved, p, stream);
 }
 
 cudaError_t launch_norm_rope(int dtype, bool interleaved, const RopeParams& p, cudaStream_t stream) {

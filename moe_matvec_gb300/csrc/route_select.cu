@@ -17,6 +17,13 @@ __device__ __forceinline__ float rcp(float x) {  // 1 ulp
   return y;
 }
 
+__device__ __forceinline__ float ex2(float x) {  // 2 ulp
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+
 // Where a lane's experts lie: each group of gs experts is given to 2^log lanes,
 // `per` consecutive experts to each, so that lane order is expert order.
 struct RoutePlace {
@@ -129,6 +136,87 @@ __device__ __noinline__ void select_exactly(const RouteParams& p, RoutePlace pl,
   if (lane < p.top_k) put(p, t, lane, pick, (p.renorm ? (sum > 0 ? mine / sum : 0.0) : mine) * (double)p.scale);
 }
 
+// Exact values of token t's experts, where some are in doubt.  Scores of a softmax
+// without a bias are compared without their common divisor.
+template <class T>
+struct Exact {
+  const RouteParams& p;
+  const T* row;
+  double top, total = 1;
+  __device__ __forceinline__ Exact(const RouteParams& p, int t, float top)
+      : p(p), row(static_cast<const T*>(p.logits) + (long long)t * p.ld), top(top) {
+    if (p.gating != QMV_GATING_SOFTMAX || !p.bias) return;
+    total = 0;
+    for (int e = threadIdx.x & 31; e < p.E; e += 32) {
+      const float l = tame(to_float(row[e]));
+      total += l > -INFINITY ? exp((double)l - this->top) : 0.0;
+    }
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  __device__ __forceinline__ double score(float l) const {
+    if (!(l > -INFINITY)) return 0.0;
+    return p.gating == QMV_GATING_SOFTMAX ? exp((double)l - top) / total : 1.0 / (1.0 + exp(-(double)l));
+  }
+  __device__ __forceinline__ double choice(int e, double s) const { return p.bias ? s + (double)tame(p.bias[e]) : s; }
+};
+
+// Groups about the border: whether the lane's group, if it is `open`, is among the
+// `want` largest of the open ones.
+template <class T>
+__device__ __noinline__ bool settle_groups(const RouteParams& p, int log, int t, float top, bool open, int want) {
+  const int lane = threadIdx.x & 31, g = lane >> log;
+  const unsigned opened = __ballot_sync(0xffffffffu, open && (lane & ((1 << log) - 1)) == 0);
+  const Exact<T> exact(p, t, top);
+  double value = 0;  // of the lane's group
+  for (unsigned todo = opened; todo; todo &= todo - 1) {
+    const int group = (__ffs(todo) - 1) >> log;
+    double a = -INFINITY, b = -INFINITY;
+    for (int i = lane; i < p.size; i += 32) {
+      const int e = group * p.size + i;
+      const double v = exact.choice(e, exact.score(tame(to_float(exact.row[e]))));
+      if (v > a) b = a, a = v;
+      else if (v > b) b = v;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+      const double x = __shfl_xor_sync(0xffffffffu, a, o), y = __shfl_xor_sync(0xffffffffu, b, o);
+      b = fmax(fmin(a, x), a >= x ? b : y);
+      a = fmax(a, x);
+    }
+    if (g == group) value = p.group_top == 2 ? a + b : a;
+  }
+  int ahead = 0;
+  for (unsigned todo = opened; todo; todo &= todo - 1) {
+    const int of = __ffs(todo) - 1;
+    const double other = __shfl_sync(0xffffffffu, value, of);
+    ahead += other > value || (other == value && (of >> log) < g);
+  }
+  return ahead < want;
+}
+
+// The token's picks and gates from n candidates, expert e of each of the first n lanes.
+template <class T>
+__device__ __noinline__ void settle_picks(const RouteParams& p, int t, float top, float inv, int n, int e) {
+  const int lane = threadIdx.x & 31;
+  const Exact<T> exact(p, t, top);
+  double v = -INFINITY, score = 0;
+  if (lane < n) {
+    const float l = tame(to_float(exact.row[e]));
+    score = exact.score(l);
+    v = p.bias ? exact.choice(e, score) : (double)l;
+    if (!p.bias) score *= (double)inv;
+  }
+  int before = 0;
+  for (int j = 0; j < n; j++) {
+    const double other = __shfl_sync(0xffffffffu, v, j);
+    const int i = __shfl_sync(0xffffffffu, e, j);
+    before += other > v || (other == v && i < e);
+  }
+  const bool in = lane < n && before < p.top_k;
+  double sum = in ? score : 0.0;
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (in) put(p, t, before, e, (p.renorm ? (sum > 0 ? score / sum : 0.0) : score) * (double)p.scale);
+}
+
 // Largest first, by a bitonic network.
 template <int N>
 __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
@@ -156,9 +244,9 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
 // and slot, the first ones largest.  A pick is then the largest of the lanes' first
 // keys and a shift of the keys of the lane that has it; lane k keeps pick k.
 //
-// What is compared carries errors: those of fp32 (score and sum are within about
-// 2^-21 of s + |bias|; a logit is exact) and the bits given way (0 in logits of 16).  Where two compared
-// values at a border (kept and next group; consecutive picks and the first left out)
+// What is compared carries errors: those of fp32 (a score's exponent is rounded twice,
+// s |l| 2^-24 at most 2^-25 s + 2^-24, and the rest is within about 2^-21 of s + |bias|; a logit is
+// exact) and the bits given way (0 in logits of 16).  Where two compared values at a border (kept and next group; consecutive picks and the first left out)
 // lie closer than that, what is in doubt is decided in 64 bits: the groups about the
 // border by their exact scores, the picks by the exact values of the picks and of
 // all experts that are as close after them, one a lane.  So the picks are those of 64
@@ -166,10 +254,9 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
 //
 // Bound by instructions.
 template <int PER, int DT, bool VEC, bool FULL>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4 : 2) route_select_kernel(const RouteParams p, const RoutePlace pl) {
+__global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4 : 2) route_select_kernel(const __grid_constant__ RouteParams p, const RoutePlace pl) {
   using T = typename Elem<DT>::type;
   constexpr uint32_t PLACE = 32 * PER - 1;  // the bits of a lane and slot
-  __shared__ float scores[ROUTE_WARPS][32 * PER];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -190,7 +277,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
   widest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(widest)));
   // scores that this close may stand the other way round
   auto close = [&](float a, float b, float more) {
-    return a == b || fabsf(a - b) <= 0x1p-20f * (fabsf(a) + fabsf(b) + 2.0f * widest) + 0x1p-24f + more;
+    return a == b || fabsf(a - b) <= 0x1p-20f * (fabsf(a) + fabsf(b) + 2.0f * widest) + 0x1p-22f + more;
   };
   auto expert = [&](int f) {  // of lane f / PER, slot f % PER
     const int of = f / PER;
@@ -232,7 +319,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
       float total = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; i++) {
-        s[i] = s[i] > -INFINITY ? expf(s[i] - top) : 0.f;
+        s[i] = s[i] > -INFINITY ? ex2((s[i] - top) * LOG2E) : 0.f;
         total += s[i];
       }
 #pragma unroll
@@ -240,39 +327,14 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
       inv = total > 0.f ? 1.0f / total : 0.f;
     } else {
 #pragma unroll
-      for (int i = 0; i < PER; i++) s[i] = rcp(1.0f + expf(-s[i]));  // (-inf: 1 / inf = 0)
+      for (int i = 0; i < PER; i++) s[i] = rcp(1.0f + ex2(-LOG2E * s[i]));  // (-inf: 1 / inf = 0)
     }
     float c[PER];
 #pragma unroll
     for (int i = 0; i < PER; i++) {
-      scores[warp][lane * PER + i] = s[i];
       c[i] = fmaf(s[i], inv, bias[i]);
       if (biased) key[i] = placed(c[i], i);
     }
-
-    // Exact values, by the whole warp where something is in doubt.  Scores of a softmax
-    // without a bias are compared without their common divisor.
-    double total = 1;
-    bool summed = false;
-    auto exact_sum = [&]() {
-      if (!soft || !biased || summed) return;
-      summed = true;
-      total = 0;
-#pragma unroll
-      for (int i = 0; i < PER; i++) {
-        const float l = i < have ? tame(to_float(row[e0 + i])) : -INFINITY;
-        total += l > -INFINITY ? exp((double)l - (double)top) : 0.0;
-      }
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    };
-    auto exact_score = [&](float l) -> double {
-      if (!(l > -INFINITY)) return 0.0;
-      return soft ? exp((double)l - (double)top) / total : 1.0 / (1.0 + exp(-(double)l));
-    };
-    auto exact = [&](int e, double& score) -> double {
-      score = exact_score(tame(to_float(row[e])));
-      return biased ? score + (double)tame(p.bias[e]) : score;
-    };
 
     if (p.keep < p.groups) {
       float one = -INFINITY, two = -INFINITY;
@@ -300,34 +362,10 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
       const float next = value_of(__reduce_max_sync(0xffffffffu, in || g >= p.groups ? 0u : mine));
       if (close(last, next, 0.f)) {
         const bool open = g < p.groups && (close(score, last, 0.f) || close(score, next, 0.f));
-        const unsigned lead = (lane & (lpg - 1)) == 0 ? 0xffffffffu : 0u;
-        unsigned opened = __ballot_sync(0xffffffffu, open && lead);
         // what is left to be kept of these groups
-        const int want = p.keep - __popc(__ballot_sync(0xffffffffu, in && !open && lead));
-        exact_sum();
-        double value = 0;  // of the lane's group
-        for (unsigned todo = opened; todo; todo &= todo - 1) {
-          const int of = __ffs(todo) - 1, group = of >> pl.log;
-          double a = -INFINITY, b = -INFINITY, sc;
-          for (int i = lane; i < gs; i += 32) {
-            const double v = exact(group * gs + i, sc);
-            if (v > a) b = a, a = v;
-            else if (v > b) b = v;
-          }
-          for (int o = 16; o > 0; o >>= 1) {
-            const double x = __shfl_xor_sync(0xffffffffu, a, o), y = __shfl_xor_sync(0xffffffffu, b, o);
-            b = fmax(fmin(a, x), a >= x ? b : y);
-            a = fmax(a, x);
-          }
-          if (g == group) value = p.group_top == 2 ? a + b : a;
-        }
-        int ahead = 0;
-        for (unsigned todo = opened; todo; todo &= todo - 1) {
-          const int of = __ffs(todo) - 1;
-          const double other = __shfl_sync(0xffffffffu, value, of);
-          ahead += other > value || (other == value && (of >> pl.log) < g);
-        }
-        if (open) in = ahead < want;
+        const int sure = __popc(__ballot_sync(0xffffffffu, in && !open && (lane & (lpg - 1)) == 0));
+        const bool among = settle_groups<T>(p, pl.log, t, top, open, p.keep - sure);
+        if (open) in = among;
       }
       if (!in) {
 #pragma unroll
@@ -360,13 +398,17 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
     if (lane == p.top_k - 1) follower = after;
     const bool doubt = __any_sync(0xffffffffu, lane < p.top_k && follower && near(picked, follower));
     int from = PLACE - (picked & PLACE);  // lane k: pick k's lane and slot
-    __syncwarp();
-    const float held = lane < p.top_k ? scores[warp][from] : 0.f;
+    // The picks' scores, as they enter the gates: lane k's (rather than those above, whose
+    // exponents are rounded once too often for small scores).
+    float held = 0.f;
+    if (lane < p.top_k) {
+      const float l = tame(to_float(row[expert(from)]));
+      held = l > -INFINITY ? (soft ? expf(l - top) : __frcp_rn(1.0f + expf(-l))) : 0.f;
+    }
     float of_all = held;
 #pragma unroll
     for (int o = QMV_MAX_TOPK / 2; o > 0; o >>= 1) of_all += __shfl_xor_sync(0xffffffffu, of_all, o);
     of_all = __shfl_sync(0xffffffffu, of_all, 0);
-    __syncwarp();  // (the scores are read)
     // (scores down to 2^-126 are whole: smaller sums are formed anew)
     if (!doubt && (!p.renorm || of_all >= 0x1p-60f)) {
       if (lane < p.top_k) put(p, t, lane, expert(from), (p.renorm ? held / of_all : held * inv) * p.scale);
@@ -383,27 +425,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
       select_exactly<PER, T>(p, pl, t);
       continue;
     }
-    const int e = expert(from);
-    double v = -INFINITY, score = 0;
-    if (biased) exact_sum();
-    if (lane < n) {
-      if (biased) {
-        v = exact(e, score);
-      } else {
-        v = tame(to_float(row[e]));
-        score = exact_score((float)v) * (double)inv;
-      }
-    }
-    int before = 0;
-    for (int j = 0; j < n; j++) {
-      const double other = __shfl_sync(0xffffffffu, v, j);
-      const int i = __shfl_sync(0xffffffffu, e, j);
-      before += other > v || (other == v && i < e);
-    }
-    const bool in = lane < n && before < p.top_k;
-    double sum = in ? score : 0.0;
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (in) put(p, t, before, e, (p.renorm ? (sum > 0 ? score / sum : 0.0) : score) * (double)p.scale);
+    settle_picks<T>(p, t, top, inv, n, expert(from));
   }
 }
 

@@ -56,7 +56,7 @@ def check(out, x, w, eps, pos, axis, freq, inter, scale, dtype):
 @pytest.mark.parametrize("norm", [True, False])
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("D,R,H,Hk", [(128, 128, 8, 2), (64, 64, 5, 1), (64, 32, 3, 3), (192, 64, 2, 1), (256, 256, 3, 2),
-                                      (80, 80, 4, 1), (72, 40, 2, 2), (128, 2, 3, 1), (128, 90, 4, 4), (8, 6, 2, 1),
+                                      (80, 80, 4, 1), (72, 40, 2, 2), (128, 2, 3, 1), (128, 90, 4, 4), (128, 92, 3, 1), (68, 36, 4, 2), (8, 6, 2, 1),
                                       (256, 254, 1, 1)])
 def test_explicit_positions(lib, dtype, norm, inter, D, R, H, Hk):
     n = 7
