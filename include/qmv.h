@@ -715,7 +715,8 @@ int moe_route_select(int dtype, const void* logits, int64_t ld, const float* bia
  * top_ids and top_logp with n_top.  One launch, no workspace; results are bitwise
  * reproducible.
  * Constraints: 1 <= rows <= 2^24, 1 <= V <= 2^28, ld >= V, 0 <= n_given <=
- * QMV_MAX_GIVEN, 0 <= n_top <= QMV_MAX_TOP, 0 < scale < inf, at least one result. */
+ * QMV_MAX_GIVEN, 0 <= n_top <= QMV_MAX_TOP, 2^-100 <= scale <= 2^126, at least one result;
+ * logits aligned to their type. */
 int qmv_logprobs(int dtype, const void* logits, int64_t ld, int64_t rows, int64_t V, float scale,
                  const int32_t* tokens, int n_given, float* logp, float* lse, float* entropy, int n_top,
                  int32_t* top_ids, float* top_logp, cudaStream_t stream);

@@ -602,6 +602,14 @@ def _stp():
     return _step
 
 
+def _together(first: torch.Tensor, *rest) -> int:
+    """The index + 1 of the device that all these tensors are on."""
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return first.device.index + 1
+
+
 def rope(head_dim: int, freq: torch.Tensor, axis: torch.Tensor | None = None, n_axes: int = 1,
          interleaved: bool = False, scale: float = 1.0) -> Rope:
     """How a model's heads turn (qmv_rope).  freq fp32 [R / 2]: radians a position of each
@@ -614,6 +622,7 @@ def rope(head_dim: int, freq: torch.Tensor, axis: torch.Tensor | None = None, n_
     if axis is not None and (axis.dtype is not torch.uint8 or axis.shape != freq.shape):
         raise ValueError(f"axis: torch.uint8 {tuple(freq.shape)} wanted, got {axis.dtype} {tuple(axis.shape)}")
     r = Rope(int(head_dim), 2 * freq.numel(), int(interleaved), int(n_axes), float(scale), 0, _ptr(freq), _ptr(axis))
+    r.reserved = _together(freq, axis)
     r._tensors = (freq, axis)
     return r
 
@@ -644,6 +653,7 @@ def lora(A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor | None = None,
         if t is not None and (t.dtype is not dt or t.shape != (n,)):
             raise ValueError(f"{what}: {dt} ({n},) wanted, got {t.dtype} {tuple(t.shape)}")
     d = Lora(n, rank, _DTYPES[A.dtype], 0, _ptr(A), _ptr(B), _ptr(ranks), _ptr(scales))
+    d.reserved = _together(A, B, ranks, scales)
     d._tensors = (A, B, ranks, scales)
     d.K, d.M = K, B.shape[1]
     return d

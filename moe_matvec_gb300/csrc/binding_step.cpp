@@ -46,6 +46,14 @@ struct Here {
   }
 };
 
+// A descriptor's tensors: `mark` is their device's index + 1, as api.py keeps it in the
+// reserved field (0: not known).
+void there(const Here& here, int32_t mark, const char* what) {
+  if (mark > 0 && mark - 1 != here.dev)
+    value_error(std::string(what) + " has its tensors on cuda:" + std::to_string(mark - 1) + ", but the current device is cuda:" +
+                std::to_string(here.dev));
+}
+
 // An optional tensor of this type and shape: its address or NULL.
 void* maybe(const Here& here, PyObject* o, at::ScalarType type, at::IntArrayRef shape, const char* what) {
   if (o == Py_None) return nullptr;
@@ -146,6 +154,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dt = dtype_code(q.scalar_type());
     int64_t qs, ks = 0, qos, kos = 0, kv = 0;
     void *qp = heads_of(here, q, D, "q", qs), *kp = nullptr;
+    there(here, rope->reserved, "rope");
     const int64_t n_tok = q.size(0);
     const bool has_k = a[2] != Py_None;
     if (has_k) {
@@ -216,6 +225,7 @@ PyObject* lora_run(PyObject*, PyObject* const* a, Py_ssize_t n) {
     here(x);
     here(ids);
     here(r);
+    there(here, l->reserved, "lora");
     const cudaStream_t st = stream_of(a[8]);
     Part out{a[6], at::kFloat, {n_tok, M}, "out", {}};
     allot(here, {&out}, st);

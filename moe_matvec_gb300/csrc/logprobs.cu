@@ -411,7 +411,8 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 3) logprobs_kernel(const L
   if (ranks > 1 && n_top) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   const float top = s_top, log_s = s_log;  // (0 and inf where every logit is -inf: log probabilities are -inf)
-  auto logp = [&](float l) { return (l - top) * p.scale - log_s; };
+  // (halves: the difference of finite logits stays finite)
+  auto logp = [&](float l) { return (0.5f * l - 0.5f * top) * (2.0f * p.scale) - log_s; };
   if (tid < p.n_given && QMV_CHECK(in_range(r * p.n_given + tid, 1, p.given_len, p.err)))
     p.logp[r * p.n_given + tid] = token < 0 ? 0.f : token >= p.V ? NAN : logp(given);
   if (!n_top) return;

@@ -172,12 +172,12 @@ int qmv_logprobs(int dtype, const void* logits, int64_t ld, int64_t rows, int64_
                  cudaStream_t stream) {
   if (!dtype_ok(dtype)) return QMV_ERR_FORMAT;
   if (rows < 1 || rows > (1 << 24) || V < 1 || V > (1 << 28) || ld < V || ld > (1ll << 40) || n_given < 0 ||
-      n_given > QMV_MAX_GIVEN || n_top < 0 || n_top > QMV_MAX_TOP || !(scale > 0.f) || std::isinf(scale))
+      n_given > QMV_MAX_GIVEN || n_top < 0 || n_top > QMV_MAX_TOP || !(scale >= 0x1p-100f) || scale > 0x1p126f)
     return QMV_ERR_SHAPE;
   if (!logits || (n_given && (!tokens || !logp)) || (n_top && (!top_ids || !top_logp)) ||
       (!n_given && !n_top && !lse && !entropy))
     return QMV_ERR_NULL;
-  if (!al16(logits) || !al16(tokens) || !al16(logp) || !al16(lse) || !al16(entropy) || !al16(top_ids) || !al16(top_logp))
+  if (reinterpret_cast<uintptr_t>(logits) % dtype_bytes(dtype) || !al16(tokens) || !al16(logp) || !al16(lse) || !al16(entropy) || !al16(top_ids) || !al16(top_logp))
     return QMV_ERR_ALIGN;
   int rc = check_device();
   if (rc) return rc;

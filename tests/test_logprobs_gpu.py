@@ -131,7 +131,7 @@ def test_masks_and_odd_values(lib, dtype):
 
 
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("V,ld,off", [(1003, 1003, 0), (1003, 1009, 0), (5000, 5001, 8), (151937, 151939, 0)])
+@pytest.mark.parametrize("V,ld,off", [(1003, 1003, 0), (1003, 1009, 0), (5000, 5001, 8), (151937, 151939, 0), (700, 705, 3), (40, 40, 1)])
 def test_rows_of_any_alignment(lib, dtype, V, ld, off):
     g = torch.Generator().manual_seed(V)
     buf = torch.full((off + 9 * ld,), float("nan"), dtype=dtype, device="cuda")  # what lies between rows is not looked at
@@ -153,6 +153,18 @@ def test_every_division_of_a_row_gives_the_definition(lib, n):
     check(logits[:1], torch.tensor([[77]], dtype=torch.int32), 32)
     again = api.logprobs(logits, torch.full((n, 1), 77, dtype=torch.int32).cuda(), 32)
     assert all(torch.equal(a, b) for a, b in zip((logp, lse, entropy, ids, top), again))
+
+
+def test_extreme_scales(lib):
+    t = torch.tensor([[0.0, 1e-30, -5.0, 3e38, -3e38], [1.0, 1.0, 1.0, 0.5, 1.0]], device="cuda")
+    tokens = torch.tensor([[0, 3], [3, 1]], dtype=torch.int32)
+    for scale in (1e-30, 1e-6, 1e20, 8e37):
+        got = api.logprobs(t, tokens.cuda(), 2, scale)
+        want = step_ref.logprobs(t.double().cpu().numpy(), tokens.numpy(), 2, float(np.float32(scale)))
+        assert np.array_equal(got[3].cpu().numpy(), want[3])
+        for g, w in zip(got[:3], want[:3]):
+            w = np.where(np.abs(w) > 3.4028235e38, np.sign(w) * np.inf, w)  # (fp32 has no more)
+            assert np.allclose(g.double().cpu().numpy(), w, rtol=1e-5, atol=1e-30)
 
 
 def test_only_what_is_asked_for(lib):

@@ -93,13 +93,14 @@ def test_logprobs(L):
     assert call(rows=0) == -2 and call(rows=(1 << 24) + 1) == -2 and call(V=0) == -2 and call(ld=99) == -2
     assert call(V=(1 << 28) + 1, ld=1 << 29) == -2
     assert call(given=-1) == -2 and call(given=65) == -2 and call(n_top=-1) == -2 and call(n_top=33) == -2
-    for s in (0.0, -1.0, NAN, INF):
+    for s in (0.0, -1.0, NAN, INF, 1e38, 1e-38):
         assert call(scale=s) == -2
     assert call(logits=None) == -4 and call(tokens=None) == -4 and call(logp=None) == -4
     assert call(ids=None) == -4 and call(top=None) == -4
     assert call(given=0, n_top=0, lse=None, entropy=None) == -4
-    for name in ("logits", "tokens", "logp", "lse", "entropy", "ids", "top"):
+    for name in ("tokens", "logp", "lse", "entropy", "ids", "top"):
         assert call(**{name: MIS}) == -5
+    assert call(logits=A + 2) == -5 and call(logits=A + 1, dt=1) == -5  # their type's alignment is enough
 
 
 def test_binding_refuses_mismatched_tensors():

@@ -265,3 +265,14 @@ def test_results_do_not_change_from_call_to_call(lib):
         want = call()
         for _ in range(5):
             assert all(same_bits(a, b) for a, b in zip(call(), want))
+
+
+def test_descriptors_of_another_device_are_refused(lib):
+    r = api.rope(64, torch.ones(32).cuda())
+    d = api.lora(rnd(1, 2, 4, 64), rnd(2, 2, 10, 4))
+    assert r.reserved == d.reserved == torch.cuda.current_device() + 1
+    r.reserved = d.reserved = 2 + torch.cuda.current_device()  # as if they had been made there
+    with pytest.raises(ValueError, match="current device"):
+        api.norm_rope(r, rnd(3, 2, 1, 64), pos=ints(1, 2)[:, None].contiguous())
+    with pytest.raises(ValueError, match="current device"):
+        api.lora_run(d, ints(0, 1), rnd(4, 2, 64), rnd(5, 2, 10))
