@@ -138,7 +138,10 @@ __device__ __forceinline__ uint32_t peer(const void* here, int rank) {  // the s
 // index), so no order of arrival shows; where they overflow shared memory (many equal
 // logits) the list is found entry by entry, each by a pass of its own.
 //
-// Bound by HBM for many rows: about 6 instructions a logit.
+// Bound by HBM for many rows, with about 8 instructions a logit: 2048 x 151936 bfloat16
+// (622 MB) 119 us, 5.2 TB/s (three CTAs of 256 threads an SM with the next loads on
+// their way; four without 121, two 139).  One row of 151936 fp32 6.6 us: three rounds of
+// loads, two barriers of the cluster and the loads of the candidates in turn.
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 3) logprobs_kernel(const LogprobsParams p, int ranks) {
   using Vec = LogitVec<DT>;

@@ -8,7 +8,7 @@
 namespace qmv {
 
 constexpr int ROPE_WARPS = 4;         // warps of a CTA, each on its own
-constexpr int ROPE_MAX_PAIRS = 128;   // head_dim 256
+constexpr int ROPE_MAX_PAIRS = 128;   // of a head of 256 values
 constexpr int ROPE_AHEAD = 3;         // head groups of a warp on their way
 constexpr int ROPE_CTAS = 4;          // CTAs an SM (5: 20.0 us, 6 with 2 ahead 22.4, for 17.8)
 
@@ -82,7 +82,10 @@ __device__ __forceinline__ void from_pairs(float (&a)[CH], float (&b)[CH]) {
 // their way.  The warp's lanes share out the token's angles (64 bits, the only
 // costly arithmetic) through shared memory; meanwhile the first heads travel.
 //
-// Bound by HBM for many tokens.
+// Bound by HBM for many tokens, and by what a token costs before its heads (angles,
+// products with the weights: a third of the instructions): 4096 x 40 heads of 128
+// bfloat16 (84 MB) 17.7 us, 4.7 TB/s.  One token of 40 heads 2.9 us: a load, the angle, the
+// sum and the store in turn.
 template <int DT, int CH, int UL, bool INTER>
 __global__ void __launch_bounds__(32 * ROPE_WARPS, UL <= 2 ? ROPE_CTAS : 3)
     norm_rope_kernel(const RopeParams p, int lph_log, unsigned per, unsigned rest) {
