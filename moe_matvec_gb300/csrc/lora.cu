@@ -442,9 +442,10 @@ __global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_both_kernel(cons
   else lora_both<DT, VW, LPR_LOG, LORA_TOK>(p, q, lora_x, v, parts, rank);
 }
 
-// One launch for both products: where there are few tokens (clusters of four SMs each
-// then hold a group's work) and a cluster's share of A is small: at most 64 KB a CTA, and
-// x of four tokens beside the parts in 48 KB of shared memory.
+// One launch for both products, in clusters of eight CTAs: where a CTA's share of A is
+// at most 64 KB (one token of rank 64, K 5120, 82 KB: 7.7 us, in two launches 5.0) and
+// up to 32 tokens (64 on one adapter: 25 us for 18), x of four tokens beside the
+// parts in 48 KB of shared memory.
 static bool lora_one_launch(long long K, int n_tok, int r, int dtype) {
   const long long window = ((K + LORA_WIN - 1) / LORA_WIN + LORA_CLUSTER - 1) / LORA_CLUSTER * LORA_WIN;
   return n_tok <= 32 && window <= 1536 && window * r * (dtype == QMV_DT_F32 ? 4 : 2) <= 65536;
