@@ -168,6 +168,21 @@ def test_edges_of_values_and_contradictions(lib):
     assert lib.get_device_error() == api.DEVERR_BATCH
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,R", [(128, 64), (128, 90), (128, 92), (72, 40), (256, 254), (192, 2)])
+def test_what_does_not_turn_is_left_as_it_is(lib, D, R, inter, dtype):
+    x = torch.randn(3, 8, D, device="cuda").to(dtype)
+    x[:, :, R] = float("inf")
+    x[:, :, R + 1::3] = -0.0
+    x[1, 1:, D - 1] = -float("inf")
+    pos = torch.tensor([[0], [5], [70000]], dtype=torch.int32).cuda()
+    y = api.norm_rope(api.rope(D, freqs(R).cuda(), interleaved=inter), x, pos=pos)[0]
+    bits = torch.int32 if dtype is torch.float32 else torch.int16
+    assert torch.equal(y[:, :, R:].view(bits), x[:, :, R:].view(bits))
+    assert torch.isfinite(y[:, :, :R]).all()
+
+
 def test_many_tokens_and_far_strides(lib):
     n = 65535
     x = torch.randn(n, 1, 8, device="cuda", dtype=torch.bfloat16)
