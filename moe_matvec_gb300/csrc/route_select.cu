@@ -245,8 +245,9 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
 // keys and a shift of the keys of the lane that has it; lane k keeps pick k.
 //
 // What is compared carries errors: those of fp32 (a score's exponent is rounded twice,
-// s |l| 2^-24 at most 2^-25 s + 2^-24, and the rest is within about 2^-21 of s + |bias|; a logit is
-// exact) and the bits given way (0 in logits of 16).  Where two compared values at a border (kept and next group; consecutive picks and the first left out)
+// s |l| 2^-24 at most 2^-25 s + 2^-24, and the rest is within 2^-20 of two scores with
+// up to 8 experts a lane, and c's own rounding; a logit is exact) and the bits given
+// way (0 in logits of 16).  Where two compared values at a border (kept and next group; consecutive picks and the first left out)
 // lie closer than that, what is in doubt is decided in 64 bits: the groups about the
 // border by their exact scores, the picks by the exact values of the picks and of
 // all experts that are as close after them, one a lane.  So the picks are those of 64
@@ -279,10 +280,11 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
     }
   }
   widest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(widest)));
-  // scores that this close may stand the other way round
-  auto close = [&](float a, float b, float more) {
-    return a == b || fabsf(a - b) <= 0x1p-20f * (fabsf(a) + fabsf(b) + 2.0f * widest) + 0x1p-22f + more;
-  };
+  // How far c of up to two scores whose values add up to `of` may be off: s (at most 1,
+  // and at most |c| + |bias|) by the roundings of the softmax's sum, exp2, quotient and
+  // exponent, c by its own.  Infinite ones (of a bias) are not off.
+  constexpr float REL = PER <= 8 ? 0x1p-20f : PER <= 16 ? 0x1p-19f : 0x1p-18f;
+  auto off = [&](float of) { return fminf(REL * fminf(of + 2.0f * widest, 2.0f) + 0x1p-22f * of + 0x1p-22f, FLT_MAX); };
   auto expert = [&](int f) {  // of lane f / PER, slot f % PER
     const int of = f / PER;
     return FULL ? f : (of >> pl.log) * gs + (of & (lpg - 1)) * per + f % PER;
@@ -362,10 +364,13 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
         before += other > mine || (other == mine && j < g);
       }
       bool in = g < p.groups && before < p.keep;
-      const float last = value_of(__reduce_min_sync(0xffffffffu, in ? mine : 0xffffffffu));
-      const float next = value_of(__reduce_max_sync(0xffffffffu, in || g >= p.groups ? 0u : mine));
-      if (close(last, next, 0.f)) {
-        const bool open = g < p.groups && (close(score, last, 0.f) || close(score, next, 0.f));
+      const float err = off(fabsf(one) + (p.group_top == 2 ? fabsf(two) : 0.f));
+      const uint32_t lo = order_of(score - err + 0.0f), hi = order_of(score + err + 0.0f);
+      // the least that a group that is in may have, and the most of one that is not
+      const uint32_t last = __reduce_min_sync(0xffffffffu, in ? lo : 0xffffffffu);
+      const uint32_t next = __reduce_max_sync(0xffffffffu, in || g >= p.groups ? 0u : hi);
+      if (next >= last) {
+        const bool open = g < p.groups && (in ? lo <= next : hi >= last);
         // what is left to be kept of these groups
         const int sure = __popc(__ballot_sync(0xffffffffu, in && !open && (lane & (lpg - 1)) == 0));
         const bool among = settle_groups<T>(p, pl.log, t, top, open, p.keep - sure);
@@ -396,7 +401,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4
       a &= ~PLACE, b &= ~PLACE;
       if (!biased) return DT == QMV_DT_F32 && a == b;  // (logits of 16 bits are whole in their keys)
       const float x = value_of(a), y = value_of(b);
-      return close(x, y, (float)(32 * PER) * 0x1p-23f * fmaxf(fabsf(x), fabsf(y)));
+      return x - y <= off(fabsf(x) + fabsf(y)) + (float)(32 * PER) * 0x1p-23f * fmaxf(fabsf(x), fabsf(y));
     };
     uint32_t follower = __shfl_down_sync(0xffffffffu, picked, 1);
     if (lane == p.top_k - 1) follower = after;

@@ -118,6 +118,28 @@ def test_masked_and_odd_logits(lib, gating):
     ids, _ = check(t[7:], 6, gating, out)
     assert ids[0].tolist()[:4] == [3, 2, 1, 0]
     check(t, 8, gating, out, 8, 3, 2)
+    # experts out of use by a low bias: in whole groups, and all but one of a group
+    for low in (-inf, -1e9, torch.finfo(torch.float32).min):
+        some = 0.1 * torch.randn(32, generator=g).cuda()
+        some[12:] = low
+        for one in (None, 13):
+            if one:
+                some[one] = 0.2
+            for keep, top in ((3, 2), (4, 2), (4, 1), (5, 2)):
+                ids, _ = check(t, 8, gating, some, 8, keep, top)
+            check(t, 8, gating, some)
+
+
+@pytest.mark.parametrize("gating", [0, 1])
+@pytest.mark.parametrize("E,G,keep,top", [(64, 8, 3, 2), (64, 8, 3, 1), (512, 1, 1, 1), (510, 17, 5, 2), (300, 2, 1, 2)])
+def test_large_biases(lib, gating, E, G, keep, top):
+    # up to 2^30: scores count for nothing beside some, for all beside others, and pairs cancel
+    g = torch.Generator().manual_seed(E + G + gating)
+    logits = (2 * torch.randn(200, E, generator=g)).cuda()
+    bias = (2.0 ** torch.randint(-4, 31, (E,), generator=g)) * (torch.randint(0, 2, (E,), generator=g) * 2 - 1)
+    check(logits, 8, gating, bias.cuda(), G, keep, top)
+    check(logits, 8, gating, (bias / 2.0 ** 20).cuda(), G, keep, top)
+    check(logits, 8, gating, bias.sign().cuda() * 2.0 ** 22, G, keep, top)
 
 
 def test_strided_rows_and_given_results(lib):
