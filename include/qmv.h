@@ -662,9 +662,9 @@ typedef struct qmv_lora {
  *   y[t] = res[t] + scales[a] * (B_a (A_a x[t])),  a = ids[t]
  * ids int32 [n_tok]; a token whose id is negative has none (y = res), one whose id
  * is n_adapters or more likewise and sets QMV_DEVERR_ADAPTER.  x fp32 [n_tok][K], res
- * and y fp32 [n_tok][M] (y may be res).  All sums are fp32, in an order that
- * depends on K, n_tok and the pool's rank and type alone, so a token's result does not depend on the
- * other tokens' adapters.  Each adapter in use is read once per four of its tokens.
+ * and y fp32 [n_tok][M] (y is res, or overlaps neither it nor x).  All sums are fp32,
+ * in an order that depends on K, n_tok and the pool's rank and type alone, so a
+ * token's result does not depend on the other tokens' adapters.  Each adapter in use is read once per four of its tokens.
  * Constraints: K % 8 == 0, 8 <= K <= 2^20, 1 <= M <= 2^30, 1 <= n_tok <= 64.
  * ws: qmv_lora_workspace_bytes bytes, any content.  Two launches, or one for up to 32
  * tokens of small adapters. */

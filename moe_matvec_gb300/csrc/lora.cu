@@ -493,6 +493,7 @@ static cudaError_t launch_up(const LoraParams& p, cudaStream_t stream) {
     long long clusters = (p.M + 32 * LORA_WARPS * LORA_CLUSTER - 1) / (32 * LORA_WARPS * LORA_CLUSTER) * p.n_tok;
     const long long cap = (long long)LORA_CTAS * device_sm_count() / LORA_CLUSTER;
     if (clusters > cap) clusters = cap;
+    if (clusters < p.n_tok) clusters = p.n_tok;  // (one for each group at least)
     make_config(cfg, attr, dim3((unsigned)(clusters * LORA_CLUSTER)), dim3(LORA_THREADS),
                 (size_t)LORA_TOK * p.window * sizeof(float), stream, true);
     attr[1].id = cudaLaunchAttributeClusterDimension;

@@ -108,6 +108,9 @@ int qmv_lora_run(const qmv_lora* l, const int32_t* ids, const float* x, const fl
       !al16(y) || !al16(ws))
     return QMV_ERR_ALIGN;
   if (ws_bytes < qmv_lora_workspace_bytes(l, K, n_tok)) return QMV_ERR_WORKSPACE;
+  // y is res, or has nothing of res and x (other CTAs read those meanwhile)
+  auto apart = [&](const float* a, int64_t n) { return y + n_tok * M <= a || a + n <= y; };
+  if ((y != res && !apart(res, n_tok * M)) || !apart(x, n_tok * K)) return QMV_ERR_SHAPE;
   if ((rc = check_device())) return rc;
   LoraParams p{};
   p.A = l->A;

@@ -64,6 +64,9 @@ def test_lora(L):
         assert call(**{name: None}) == -4 and call(**{name: MIS}) == -5
     assert call(pool(a=None)) == -4 and call(pool(b=None)) == -4 and call(pool(a=MIS)) == -5 and call(pool(b=MIS)) == -5
     assert call(pool(ranks=MIS)) == -5 and call(pool(scales=MIS)) == -5
+    # y over x (256 * 4 bytes), or over a part of res (400 * 4 bytes)
+    assert call() == -2 and call(x=A + 1584) == -2 and call(x=A - 1008) == -2
+    assert call(x=4 * A, y=A + 16) == -2 and call(x=4 * A, res=A + 1584) == -2
     need = L.qmv_lora_workspace_bytes(R(pool()), 64, 4)
     assert need == 4 * 8 * 4 and call(wsb=need - 1) == -6
     assert L.qmv_lora_workspace_bytes(R(pool(r=6)), 64, 4) == 0 and L.qmv_lora_workspace_bytes(None, 64, 4) == 0
