@@ -708,12 +708,13 @@ int moe_route_select(int dtype, const void* logits, int64_t ld, const float* bia
  * tokens int32 [rows][n_given]: a negative one gives 0, one of V or more NaN and
  * QMV_DEVERR_TOKEN.  A row of -inf alone has lse and logp -inf and entropy 0;
  * a row with a NaN or +inf has NaN for lse, logp, entropy and top_logp.
- * Results are fp32 (exponentials fp32, within 2^-21; sums of at most some
- * hundreds of terms in a row before they are joined), and formed without the
+ * Results are fp32 (exponentials fp32, within 2^-21; sums fp32 for at most 512
+ * terms, which are joined in fp64), and formed without the
  * row's largest term: log probabilities near 0 and entropies near 0 keep their
  * relative precision.  lse and entropy NULL where not wanted; logp and tokens go with n_given,
  * top_ids and top_logp with n_top.  One launch, no workspace; results are bitwise
- * reproducible.
+ * reproducible (a row's last bits depend on the call's number of rows, which decides
+ * how many CTAs share a row, and on the row's alignment to 16 bytes).
  * Constraints: 1 <= rows <= 2^24, 1 <= V <= 2^28, ld >= V, 0 <= n_given <=
  * QMV_MAX_GIVEN, 0 <= n_top <= QMV_MAX_TOP, 2^-100 <= scale <= 2^126, at least one result;
  * logits aligned to their type. */

@@ -14,6 +14,7 @@ constexpr int LP_UNROLL = 4;        // 16-byte loads of a thread on their way
 constexpr int LP_MAX_CLUSTER = 8;
 constexpr int LP_SEGS = 16;         // stretches of a thread's loads whose largest logit is kept
 constexpr int LP_CAND = 1024;       // candidates for the top list that shared memory holds
+constexpr int LP_CHAIN = 512;       // terms that a thread adds up in 32 bits before they join its sums in 64
 // The smallest exponent (of 2) that matters; also what exp2 of a masked logit takes,
 // so that 0 * -inf never enters a sum.
 constexpr float LP_LOWEST = -1.0e4f;
@@ -142,12 +143,23 @@ __device__ __forceinline__ uint32_t peer(const void* here, int rank) {  // the s
 // (622 MB) 119 us, 5.2 TB/s (three CTAs of 256 threads an SM with the next loads on
 // their way; four without 121, two 139).  One row of 151936 fp32 6.6 us: three rounds of
 // loads, two barriers of the cluster and the loads of the candidates in turn.
+//
+// LONG: more than FOLD vectors a CTA.  There a thread's sums join sums in 64 bits every
+// LP_CHAIN terms: in 32 bits alone rows of 2^24 logits were off by 5e-5 where all were
+// equal, and by 1.1e-4 where they rose slowly (a rescaling a step).  Shorter rows, which
+// never fold, keep a loop without it (16 rows of 151936 fp32 7.3 us, with it 7.7; 2048 of
+// bfloat16 119 and 123).
 template <int DT, int NT>
+constexpr int lp_fold() {  // vectors from one fold to the next
+  return NT * LP_CHAIN / (LogitVec<DT>::N / 2);
+}
+template <int DT, int NT, bool LONG>
 __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 3) logprobs_kernel(const LogprobsParams p, int ranks) {
   using Vec = LogitVec<DT>;
   using T = typename Vec::T;
   constexpr int N = Vec::N, WARPS = NT / 32, MAX_PARTS = (NT == 512 ? LP_MAX_CLUSTER : 2) * WARPS;
-  __shared__ unsigned long long cand[LP_CAND];     // the first CTA's: the row's
+  static_assert(sizeof(double2) * NT <= sizeof(unsigned long long) * LP_CAND, "the threads' long sums lie in cand");
+  __shared__ __align__(16) unsigned long long cand[LP_CAND];  // the first CTA's: the row's
   __shared__ float seg_max[LP_SEGS][NT];
   __shared__ LpPart parts[MAX_PARTS];              // the first CTA's: all warps'
   __shared__ float reach[MAX_PARTS];               // all warps' r-th largest thread maxima
@@ -201,7 +213,21 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 3) logprobs_kernel(const L
   float m = -FLT_MAX, mine = -INFINITY, stretch = -INFINITY;
   bool out = false;  // the warp's largest is left out of the sums
   F2 S = F2::of(0.f, 0.f), D = S;
-  constexpr int STEP = NT * LP_UNROLL;
+  constexpr int STEP = NT * LP_UNROLL, FOLD = lp_fold<DT, NT>();
+  static_assert(FOLD % STEP == 0, "whole steps");
+  // s and t of the vectors folded before (until the candidates come), relative to fold_m
+  double2& folded = reinterpret_cast<double2*>(cand)[tid];
+  float fold_m = -FLT_MAX;
+  auto fold = [&](bool some) {
+    double2 sum = some ? folded : make_double2(0., 0.);
+    if (some && fold_m != m) {  // (seldom: exp2 in 64 bits takes as long as some steps)
+      const double d = fmax(((double)fold_m - m) * k, (double)LP_LOWEST), f = exp2(d);
+      sum = make_double2(f * sum.x, f * (sum.y + d * sum.x));
+    }
+    sum.x += (double)S.x() + (double)S.y();
+    sum.y += (double)D.x() + (double)D.y();
+    return sum;
+  };
   const int steps = (v1 - v0 + STEP - 1) / STEP, per_seg = (steps + LP_SEGS - 1) / LP_SEGS;
   int seg = 0, in_seg = 0;
   auto fetch = [&](int v, Vec(&x)[LP_UNROLL]) {
@@ -218,56 +244,68 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 3) logprobs_kernel(const L
   };
   Vec next[LP_UNROLL];
   fetch(v0 + tid, next);
+  for (int v = v0 + tid;;) {
+    const int end = LONG ? min(v1, v - tid + FOLD) : v1;
 #pragma unroll 2
-  for (int v = v0 + tid; v - tid < v1; v += STEP) {
-    Vec x[LP_UNROLL];
+    for (; v - tid < end; v += STEP) {
+      Vec x[LP_UNROLL];
 #pragma unroll
-    for (int u = 0; u < LP_UNROLL; u++) x[u] = next[u];
-    fetch(v + STEP, next);  // (the next step's are on their way)
-    const float bm = largest(x);
-    mine = fmaxf(mine, bm);
-    stretch = fmaxf(stretch, bm);
-    if (++in_seg == per_seg) {
-      seg_max[seg][tid] = stretch;
-      seg++;
-      in_seg = 0;
-      stretch = -INFINITY;
-    }
-    const unsigned above = __ballot_sync(0xffffffffu, bm > m || (!out && bm == m));
-    if (above) {
-      const float now = warp_max(bm), d = fmaxf((m - now) * k, LP_LOWEST), f = ex2(d);
-      const F2 f2 = F2::of(f, f), was = F2::of(out && lane == 0 ? 1.f : 0.f, 0.f);
-      // the former largest joins the sums (d is 0 for it)
-      S = S + was;
-      D = f2 * fma2(F2::of(d, d), S, D);
-      S = f2 * S;
-      m = now;
-      out = true;
-      if (lane == __ffs(__ballot_sync(0xffffffffu, bm == now)) - 1) {
-        bool left = false;
-#pragma unroll
-        for (int u = 0; u < LP_UNROLL; u++)
-          if (!left) left = x[u].leave_out(now);
+      for (int u = 0; u < LP_UNROLL; u++) x[u] = next[u];
+      fetch(v + STEP, next);  // (the next step's are on their way)
+      const float bm = largest(x);
+      mine = fmaxf(mine, bm);
+      stretch = fmaxf(stretch, bm);
+      if (++in_seg == per_seg) {
+        seg_max[seg][tid] = stretch;
+        seg++;
+        in_seg = 0;
+        stretch = -INFINITY;
       }
-    }
-    const F2 m2 = F2::of(-m, -m);
+      const unsigned above = __ballot_sync(0xffffffffu, bm > m || (!out && bm == m));
+      if (above) {
+        const float now = warp_max(bm), d = fmaxf((m - now) * k, LP_LOWEST), f = ex2(d);
+        const F2 f2 = F2::of(f, f), was = F2::of(out && lane == 0 ? 1.f : 0.f, 0.f);
+        // the former largest joins the sums (d is 0 for it)
+        S = S + was;
+        D = f2 * fma2(F2::of(d, d), S, D);
+        S = f2 * S;
+        m = now;
+        out = true;
+        if (lane == __ffs(__ballot_sync(0xffffffffu, bm == now)) - 1) {
+          bool left = false;
 #pragma unroll
-    for (int u = 0; u < LP_UNROLL; u++)
-#pragma unroll
-      for (int i = 0; i < N / 2; i++) {
-        const float2 l = x[u].pair(i);
-        F2 d = (F2::of(l.x, l.y) + m2) * k2;
-        d = F2::of(at_least(d.x(), LP_LOWEST), at_least(d.y(), LP_LOWEST));
-        const F2 e = F2::of(ex2(d.x()), ex2(d.y()));
-        S = S + e;
-        D = fma2(e, d, D);
+          for (int u = 0; u < LP_UNROLL; u++)
+            if (!left) left = x[u].leave_out(now);
+        }
       }
+      const F2 m2 = F2::of(-m, -m);
+#pragma unroll
+      for (int u = 0; u < LP_UNROLL; u++)
+#pragma unroll
+        for (int i = 0; i < N / 2; i++) {
+          const float2 l = x[u].pair(i);
+          F2 d = (F2::of(l.x, l.y) + m2) * k2;
+          d = F2::of(at_least(d.x(), LP_LOWEST), at_least(d.y(), LP_LOWEST));
+          const F2 e = F2::of(ex2(d.x()), ex2(d.y()));
+          S = S + e;
+          D = fma2(e, d, D);
+        }
+    }
+    if (!LONG || v - tid >= v1) break;
+    folded = fold(v - tid - v0 > FOLD);
+    fold_m = m;
+    S = D = F2::of(0.f, 0.f);
   }
   if (in_seg) seg_max[seg][tid] = stretch;
 
   const int n_top = p.n_top;
   const int nr = (2 * n_top + n_parts - 1) / n_parts, nq = nr ? (n_top + nr - 1) / nr : 0;  // (n_parts is at least 8)
   float s = S.x() + S.y(), t = D.x() + D.y();
+  if (LONG && v1 - v0 > FOLD) {
+    const double2 sum = fold(true);
+    s = (float)sum.x;
+    t = (float)sum.y;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -459,8 +497,8 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 3) logprobs_kernel(const L
   }
 }
 
-template <int DT, int NT>
-static cudaError_t launch_as(const LogprobsParams& p, int ranks, cudaStream_t stream) {
+template <int DT, int NT, bool LONG>
+static cudaError_t launch_long(const LogprobsParams& p, int ranks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   make_config(cfg, attr, dim3((unsigned)(p.rows * ranks)), dim3(NT), 0, stream, true);
@@ -469,7 +507,13 @@ static cudaError_t launch_as(const LogprobsParams& p, int ranks, cudaStream_t st
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = ranks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, NT>, p, ranks);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, NT, LONG>, p, ranks);
+}
+template <int DT, int NT>
+static cudaError_t launch_as(const LogprobsParams& p, int ranks, cudaStream_t stream) {
+  // (a CTA's vectors, with the two that a row may begin and end in)
+  const int vecs = (p.V / LogitVec<DT>::N + 2) / ranks + 1;
+  return vecs > lp_fold<DT, NT>() ? launch_long<DT, NT, true>(p, ranks, stream) : launch_long<DT, NT, false>(p, ranks, stream);
 }
 
 template <int DT>
