@@ -631,8 +631,10 @@ typedef struct qmv_rope {
  * Positions: pos int32 [n_tok][n_axes], or NULL and the batch's lens int32
  * [n_seq] and starts int32 [n_seq + 1] as in qmv_kv_batch (starts NULL: one token
  * per sequence): token i of sequence s lies at lens[s] - (starts[s+1] -
- * starts[s]) + i on every axis.  Rows that no sequence covers are not written; starts
- * and lens that contradict n_tok set QMV_DEVERR_BATCH.
+ * starts[s]) + i on every axis.  Rows that no sequence covers are not written.  What
+ * contradicts n_tok is clamped as in the cache calls and sets QMV_DEVERR_BATCH; so do
+ * more new tokens than lens[s] (but for lens[s] = 0, an empty slot), of which the
+ * first turn by positions below 0.
  * Constraints: 1 <= n_tok <= QMV_MAX_BATCH_TOKENS, n_heads and n_kv_heads <=
  * 16384; pointers and token strides multiples of 16 bytes. */
 int qmv_norm_rope(const qmv_rope* rope, int dtype, const void* q, int64_t q_stride, void* q_out,

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL <= 2 ? ROPE_CTAS : 3)
       freq[i] = turns_a_position(pair < p.R / 2 ? p.freq[pair] : 0.f);
       if (p.axis && pair < p.R / 2) axis[i] = p.axis[pair];
       if (axis[i] >= p.n_axes) {
-        if (p.pos) set_error(p.err, QMV_DEVERR_BATCH);
+        set_error(p.err, QMV_DEVERR_BATCH);
         axis[i] = 0;
       }
     }
@@ -196,10 +196,16 @@ __global__ void __launch_bounds__(32 * ROPE_WARPS, UL <= 2 ? ROPE_CTAS : 3)
         a = p.starts[seq];
         b = p.starts[seq + 1];
       }
-      const int len = p.lens[seq];
-      if (a < 0 || b < a || b > p.n_tok || len < 0) set_error(p.err, QMV_DEVERR_BATCH);
+      int len = p.lens[seq];
+      if (a < 0 || b < a || b > p.n_tok || len < 0) {  // clamped as by the cache calls (kv_seq)
+        set_error(p.err, QMV_DEVERR_BATCH);
+        a = min(max(a, 0), p.n_tok);
+        b = min(max(b, a), p.n_tok);
+        len = max(len, 0);
+      }
       if ((int)t < a || (int)t >= b) continue;  // no sequence's token (the whole warp)
-      pos = (int)((long long)max(len, 0) - b + t);
+      if (len > 0 && len < b - a) set_error(p.err, QMV_DEVERR_BATCH);  // tokens before the first
+      pos = len - b + (int)t;
     }
     __syncwarp();  // (the last token's turns are read)
 #pragma unroll
