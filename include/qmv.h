@@ -627,7 +627,8 @@ typedef struct qmv_rope {
  * The angle is formed and reduced in 64 bits (any int32 position), everything
  * else is fp32.  q [n_tok][n_heads][D] with tokens q_stride elements apart, q_out
  * likewise (q itself with the same stride: in place); k the same with n_kv_heads
- * (NULL with n_kv_heads 0: none).
+ * (NULL with n_kv_heads 0: none).  But for that, no row of q_out or k_out has a byte of
+ * q, k or each other (QMV_ERR_SHAPE).
  * Positions: pos int32 [n_tok][n_axes], or NULL and the batch's lens int32
  * [n_seq] and starts int32 [n_seq + 1] as in qmv_kv_batch (starts NULL: one token
  * per sequence): token i of sequence s lies at lens[s] - (starts[s+1] -

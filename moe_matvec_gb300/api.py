@@ -635,7 +635,7 @@ def norm_rope(rope: Rope, q: torch.Tensor, k: torch.Tensor | None = None, q_w: t
     and k [n_tok][n_kv_heads][D] (tokens may be strided), q_w and k_w fp32 [D] (None: no norm).
     Positions: pos int32 [n_tok][n_axes], or lens int32 [n_seq] and starts int32 [n_seq + 1] (None:
     one token per sequence) as for kv_append.  q_out and k_out may be strided, and q and k
-    themselves.  Returns (q_out, k_out)."""
+    themselves; else they overlap neither these nor each other.  Returns (q_out, k_out)."""
     return _stp().norm_rope(ctypes.addressof(rope), q, k, q_w, k_w, eps, pos, lens, starts, q_out, k_out, _on(stream))
 
 

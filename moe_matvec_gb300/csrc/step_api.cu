@@ -26,6 +26,39 @@ static int check_heads(int dtype, int D, int n_tok, const RopeHeads& h) {
   return QMV_OK;
 }
 
+// Rows of `len` bytes, `step` bytes apart (step >= len), one a token.
+struct Rows {
+  const char* at;
+  long long step, len;
+};
+static long long floor_div(long long a, long long b) { return a / b - (a % b < 0); }
+// Whether a row of a and a row of b have a byte in common.
+static bool meet(const Rows& a, const Rows& b, int n) {
+  const long long d = reinterpret_cast<intptr_t>(b.at) - reinterpret_cast<intptr_t>(a.at);  // of the first rows
+  if (d >= (n - 1) * a.step + a.len || -d >= (n - 1) * b.step + b.len) return false;
+  if (n == 1) return true;
+  if (a.step == b.step) {  // parts of one buffer's rows: row j of b lies d + (j - i) step after row i of a
+    const long long m = floor_div(d, a.step), r = d - m * a.step;
+    return (r < a.len && m > -n && m < n) || (a.step - r < b.len && m + 1 > -n && m + 1 < n);
+  }
+  for (long long i = 0; i < n; i++) {  // (rows of two steps among one another: row by row)
+    const long long x = i * a.step - d, first = floor_div(x - b.len, b.step) + 1, last = floor_div(x + a.len - 1, b.step);
+    if (first < n && last >= 0 && first <= last) return true;
+  }
+  return false;
+}
+// Heads are read by other warps while results are written: results take exactly the
+// place of their own input, or lie apart from both inputs and one another.
+static bool results_apart(int dtype, int D, int n_tok, const RopeHeads& q, const RopeHeads& k) {
+  const long long e = dtype_bytes(dtype);
+  auto in = [&](const RopeHeads& h) { return Rows{static_cast<const char*>(h.x), h.xs * e, h.n * D * e}; };
+  auto out = [&](const RopeHeads& h) { return Rows{static_cast<const char*>(h.y), h.ys * e, h.n * D * e}; };
+  if (q.y != q.x && meet(in(q), out(q), n_tok)) return false;
+  if (!k.n) return true;
+  return (k.y == k.x || !meet(in(k), out(k), n_tok)) && !meet(in(k), out(q), n_tok) && !meet(in(q), out(k), n_tok) &&
+         !meet(out(q), out(k), n_tok);
+}
+
 static int check_lora(const qmv_lora* l, int64_t K, int n_tok) {
   if (!l) return QMV_ERR_NULL;
   if (!dtype_ok(l->dtype)) return QMV_ERR_FORMAT;
@@ -72,6 +105,7 @@ int qmv_norm_rope(const qmv_rope* rope, int dtype, const void* q, int64_t q_stri
     if (starts && (n_seq < 1 || n_seq > QMV_MAX_SEQS)) return QMV_ERR_SHAPE;
     if (!starts && n_seq != n_tok) return QMV_ERR_NTOK;
   }
+  if (!results_apart(dtype, D, n_tok, p.q, p.k)) return QMV_ERR_SHAPE;
   if ((rc = check_device())) return rc;
   p.freq = rope->freq;
   p.axis = rope->axis;
