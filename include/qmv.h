@@ -669,7 +669,8 @@ typedef struct qmv_lora {
  * in an order that depends on K, n_tok and the pool's rank and type alone, so a
  * token's result does not depend on the other tokens' adapters.  Each adapter in use is read once per four of its tokens.
  * Constraints: K % 8 == 0, 8 <= K <= 2^20, 1 <= M <= 2^30, 1 <= n_tok <= 64.
- * ws: qmv_lora_workspace_bytes bytes, any content.  Two launches, or one for up to 32
+ * ws: qmv_lora_workspace_bytes bytes, any content, none of them of x, res or y
+ * (QMV_ERR_SHAPE).  Two launches, or one for up to 32
  * tokens of small adapters. */
 size_t qmv_lora_workspace_bytes(const qmv_lora* l, int64_t K, int n_tok);
 int qmv_lora_run(const qmv_lora* l, const int32_t* ids, const float* x, const float* res, float* y, int64_t K,

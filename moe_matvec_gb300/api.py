@@ -667,7 +667,7 @@ def lora_run(lora: Lora, ids: torch.Tensor, x: torch.Tensor, r: torch.Tensor, ou
              ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y[t] = r[t] + scale_a B_a (A_a x[t]) with a = ids[t], none for a negative id (qmv_lora_run):
     adapters of many requests beside a shared projection whose result is r.  ids int32 [n_tok], x
-    fp32 [n_tok][K], r fp32 [n_tok][M]; out may be r (and overlaps nothing else)."""
+    fp32 [n_tok][K], r fp32 [n_tok][M]; out may be r, else out and ws overlap nothing."""
     return _stp().lora_run(ctypes.addressof(lora), lora.K, lora.M, ids, x, r, out, ws, _on(stream))
 
 

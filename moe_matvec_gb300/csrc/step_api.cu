@@ -141,10 +141,14 @@ int qmv_lora_run(const qmv_lora* l, const int32_t* ids, const float* x, const fl
   if (!al16(l->A) || !al16(l->B) || !al16(l->ranks) || !al16(l->scales) || !al16(ids) || !al16(x) || !al16(res) ||
       !al16(y) || !al16(ws))
     return QMV_ERR_ALIGN;
-  if (ws_bytes < qmv_lora_workspace_bytes(l, K, n_tok)) return QMV_ERR_WORKSPACE;
-  // y is res, or has nothing of res and x (other CTAs read those meanwhile)
-  auto apart = [&](const float* a, int64_t n) { return y + n_tok * M <= a || a + n <= y; };
-  if ((y != res && !apart(res, n_tok * M)) || !apart(x, n_tok * K)) return QMV_ERR_SHAPE;
+  const size_t need = qmv_lora_workspace_bytes(l, K, n_tok);
+  if (ws_bytes < need) return QMV_ERR_WORKSPACE;
+  // y is res, or has nothing of res and x, and the workspace has nothing of the three
+  // (other CTAs read res, x and the workspace meanwhile)
+  const Rows ry{reinterpret_cast<const char*>(y), 0, n_tok * M * 4}, rr{reinterpret_cast<const char*>(res), 0, n_tok * M * 4},
+      rx{reinterpret_cast<const char*>(x), 0, n_tok * K * 4}, rw{static_cast<const char*>(ws), 0, (long long)need};
+  if ((y != res && meet(ry, rr, 1)) || meet(ry, rx, 1) || meet(rw, ry, 1) || meet(rw, rr, 1) || meet(rw, rx, 1))
+    return QMV_ERR_SHAPE;
   if ((rc = check_device())) return rc;
   LoraParams p{};
   p.A = l->A;

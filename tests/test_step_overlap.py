@@ -84,6 +84,33 @@ def test_what_is_refused_is_what_overlaps(L):
     assert min(got.values()) > 2000
 
 
+def lora(L, x, res, y, ws, wsb=1 << 20, K=64, M=100, n=4, rank=8):
+    """Addresses in units of 16 bytes: x 64 units, res and y 100, the workspace 8 (one split)."""
+    at = lambda a: A + 16 * a  # noqa: E731
+    d = api.Lora(3, rank, 2, 0, A, A, None, None)
+    return L.qmv_lora_run(ctypes.byref(d), A, at(x), at(res), at(y), K, M, n, at(ws), wsb, None)
+
+
+def test_an_adapters_workspace_that_overlaps(L):
+    x, res, y = 0, 1000, 2000
+    for ws in (x, x - 7, x + 63, res, res - 7, res + 99, y, y - 7, y + 99):
+        assert lora(L, x, res, y, ws) == SHAPE and lora(L, x, res, y, ws, wsb=8 * 16) == SHAPE
+        assert lora(L, x, res, res, ws if ws < y - 7 else ws - 1000) == SHAPE   # in place
+    # rank 128 and 40000 columns: 20 splits of 4 x 128 sums, 2560 units
+    for ws in (6001 - 2560, 6000 + 99):
+        assert lora(L, 100000, 6000, 9000, ws, K=40000, rank=128) == SHAPE
+    d = api.Lora(3, 128, 2, 0, A, A, None, None)
+    assert L.qmv_lora_workspace_bytes(ctypes.byref(d), 40000, 4) == 2560 * 16
+
+
+@no_device
+def test_a_workspace_beside_the_tensors(L):
+    for ws in (64, 1000 - 8, 1100, 2000 - 8, 2100):
+        assert lora(L, 0, 1000, 2000, ws) in (-7, -8)  # (a larger buffer's unused rest may be anything)
+    assert lora(L, 0, 1000, 1000, 2000) in (-7, -8)
+    assert lora(L, 100000, 6000, 9000, 6000 - 2560, K=40000, rank=128) in (-7, -8)
+
+
 @no_device
 def test_far_rows(L):
     # tokens 2^20 elements apart (2^18 units of fp32), 65535 of them: extents of 2^38 bytes
