@@ -452,7 +452,8 @@ static bool lora_one_launch(long long K, int n_tok, int r, int dtype) {
 }
 
 // Columns of a split: windows of 256, at most 8 (x of four tokens in shared memory)
-// and at most 16 splits (the second kernel adds them) where that leaves a choice.
+// and at most 16 splits (the second kernel adds them) where that leaves a choice (not
+// above 32768 columns, or 18432 with 64 tokens: 8 windows a split, up to 512 splits).
 // Taken are those for which a warp has the fewest windows to go through, each token
 // taken to have an adapter of its own and its share of four CTAs an SM; fewer
 // splits among equals.
