@@ -715,10 +715,12 @@ int moe_route_select(int dtype, const void* logits, int64_t ld, const float* bia
  * Results are fp32 (exponentials fp32, within 2^-21; sums fp32 for at most 512
  * terms, which are joined in fp64), and formed without the
  * row's largest term: log probabilities near 0 and entropies near 0 keep their
- * relative precision.  lse and entropy NULL where not wanted; logp and tokens go with n_given,
+ * relative precision (terms below 2^-126 of the largest count as 0).  lse and entropy NULL where not wanted; logp and tokens go with n_given,
  * top_ids and top_logp with n_top.  One launch, no workspace; results are bitwise
  * reproducible (a row's last bits depend on the call's number of rows, which decides
- * how many CTAs share a row, and on the row's alignment to 16 bytes).
+ * how many CTAs share a row, and on the row's alignment to 16 bytes).  Where more than
+ * 1024 logits of a row may be of its top list (equal ones at the top), the row is read
+ * n_top more times by one CTA.
  * Constraints: 1 <= rows <= 2^24, 1 <= V <= 2^28, ld >= V, 0 <= n_given <=
  * QMV_MAX_GIVEN, 0 <= n_top <= QMV_MAX_TOP, 2^-100 <= scale <= 2^126, at least one result;
  * logits aligned to their type. */

@@ -137,7 +137,8 @@ __device__ __forceinline__ uint32_t peer(const void* here, int rank) {  // the s
 // warps' r-th largest thread maxima, q r >= n_top.  Every logit of the list is at least
 // that floor and lies in such a stretch.  These candidates are ordered by (value,
 // index), so no order of arrival shows; where they overflow shared memory (many equal
-// logits) the list is found entry by entry, each by a pass of its own.
+// logits) the list is found entry by entry, each by a pass of its own of one CTA over the
+// row: 20 of a row of 151936 equal fp32 logits 485 us (7.5 where they differ), of 2^20 3.2 ms.
 //
 // Bound by HBM for many rows, with about 8 instructions a logit: 2048 x 151936 bfloat16
 // (622 MB) 119 us, 5.2 TB/s (three CTAs of 256 threads an SM with the next loads on

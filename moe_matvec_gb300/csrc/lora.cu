@@ -228,9 +228,15 @@ __global__ void __launch_bounds__(LORA_THREADS, LORA_CTAS) lora_down_kernel(cons
 // together, so that afterwards each lane has one row's sum and up to 32 consecutive
 // rows of y and res are read and written at once.
 //
+// A kernel holds the variants of one, two and four tokens, and the widest takes all 128
+// registers: 76 bytes spill (132 are read back) for bfloat16 with 8 lanes a row, the rank
+// 64 of the cases below, and 160 (220) in lora_both_kernel with 2 lanes, rank 16.
+//
 // Bound by HBM for many adapters: 64 of rank 64, M 17408 (152 MB) 32.8 us by itself, 4.6 TB/s,
 // both products 37.6; a few groups of tokens by the chain of ids, v's parts, rows and res:
-// 24 tokens on 10 adapters (21 MB in all) 16.7 us.
+// 24 tokens on 10 adapters (21 MB in all) 16.7 us.  Tokens that share an adapter are far
+// from their bytes: each group of four reads and converts it anew (64 tokens on one, 13 MB
+// in all, 18.9 us; on eight 21.2).
 template <int DT, int VW, int LPR_LOG, int NT, class Ready, class Part>
 __device__ __forceinline__ void lora_up(const LoraParams& p, const LoraTokens& q, float (&v)[LORA_TOK][QMV_MAX_RANK],
                                         long long m0, int rows, Ready ready, Part part) {

@@ -86,10 +86,12 @@ __device__ __forceinline__ void from_pairs(float (&a)[CH], float (&b)[CH]) {
 // their way.  The warp's lanes share out the token's angles (64 bits, the only
 // costly arithmetic) through shared memory; meanwhile the first heads travel.
 //
-// Bound by HBM for many tokens, and by what a token costs before its heads (angles,
-// products with the weights: a third of the instructions): 4096 x 40 heads of 128
-// bfloat16 (84 MB) 17.7 us, 4.7 TB/s.  One token of 40 heads 2.9 us: a load, the angle, the
-// sum and the store in turn.
+// Bound for many tokens by latency with few warps: 4096 x 40 heads of 128 bfloat16 (84
+// MB) 17.7 us, 4.7 TB/s, with 47% of the issue slots taken by 23% of the warps, which wait
+// for their own chains, for the turns in shared memory and for loads, in this order.  The
+// loads run dry at each token's end: the next one's first heads and angles (with the
+// products with the weights a third of the instructions) begin there.  One token of 40
+// heads 2.8 us: a load, the angle, the sum and the store in turn.
 // ALL: every pair turns (R = D).
 template <int DT, int CH, int UL, bool INTER, bool ALL>
 __global__ void __launch_bounds__(32 * ROPE_WARPS, UL <= 2 ? ROPE_CTAS : 3)
@@ -343,8 +345,10 @@ static cudaError_t launch_as(bool interleaved, const RopeParams& p, cudaStream_t
 }
 
 // Chunks of 16 bytes where whole ones pair up, else shorter ones, down to single
-// values (4096 x 40 heads of 128 bfloat16, the halves of R values as pairs: R 128 18 us,
-// 120 23, 124 and 126 42).  Where pairs are neighbours only the head's size counts.
+// values (4096 x 40 heads of 128 bfloat16, the halves of R values as pairs: R 64 and 128
+// 18 us, 120 24, 124 and 126 43).  Where pairs are neighbours only the head's size counts
+// (19 us).  The lanes of a head are a power of two: with heads of 72 values (21.6 us), 80
+// (17.3) and 192 (31.4) 44, 38 and 25% of them have no unit.
 template <int DT>
 static cudaError_t launch_dt(bool interleaved, const RopeParams& p, cudaStream_t stream) {
   const int R = interleaved ? 0 : p.R;

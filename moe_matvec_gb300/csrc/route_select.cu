@@ -255,9 +255,9 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
 //
 // Bound by a token's dependent steps (eight picks one after another, each a maximum over
 // the warp) and about 700 instructions, the ALU pipe half full: 16384 tokens of 256
-// experts in 8 groups with a bias 19 us, without both 13; one token 2.5 us.  More or
-// fewer CTAs an SM (8, 5), the next token's logits on their way and cheaper scores
-// changed that by less than a tenth.
+// experts in 8 groups with a bias 19 us, without groups 16, softmax without both 14; one
+// token 2.6 us.  More or fewer CTAs an SM (8, 5), the next token's logits on their way and
+// cheaper scores changed that by less than a tenth.
 template <int PER, int DT, bool VEC, bool FULL>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS, PER <= 8 ? 6 : PER <= 16 ? 4 : 2) route_select_kernel(const __grid_constant__ RouteParams p, const RoutePlace pl) {
   using T = typename Elem<DT>::type;
@@ -442,8 +442,9 @@ template <int DT, bool VEC>
 static cudaError_t launch_as(const RouteParams& p, RoutePlace pl, cudaStream_t stream) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  // as many CTAs as the SMs hold at once (80 registers a thread with up to 8 experts a
-  // lane, 122, 208); warps take tokens by turns
+  // as many CTAs as the SMs hold at once (80 registers a thread with up to 8 experts a lane,
+  // of which 64 to 68 bytes spill, 128 with 16, where 80 to 84 do, 246 with 32); warps take
+  // tokens by turns
   const int ctas = (p.n_tok + ROUTE_WARPS - 1) / ROUTE_WARPS;
   const int cap = (pl.per <= 8 ? 6 : pl.per <= 16 ? 4 : 2) * device_sm_count();
   make_config(cfg, attr, dim3((unsigned)(ctas < cap ? ctas : cap)), dim3(32 * ROUTE_WARPS), 0, stream, true);

@@ -145,8 +145,8 @@ int qmv_lora_run(const qmv_lora* l, const int32_t* ids, const float* x, const fl
   if (ws_bytes < need) return QMV_ERR_WORKSPACE;
   // y is res, or has nothing of res and x, and the workspace has nothing of the three
   // (other CTAs read res, x and the workspace meanwhile)
-  const Rows ry{reinterpret_cast<const char*>(y), 0, n_tok * M * 4}, rr{reinterpret_cast<const char*>(res), 0, n_tok * M * 4},
-      rx{reinterpret_cast<const char*>(x), 0, n_tok * K * 4}, rw{static_cast<const char*>(ws), 0, (long long)need};
+  auto of = [](const void* p, long long bytes) { return Rows{static_cast<const char*>(p), 0, bytes}; };
+  const Rows ry = of(y, n_tok * M * 4), rr = of(res, n_tok * M * 4), rx = of(x, n_tok * K * 4), rw = of(ws, need);
   if ((y != res && meet(ry, rr, 1)) || meet(ry, rx, 1) || meet(rw, ry, 1) || meet(rw, rr, 1) || meet(rw, rx, 1))
     return QMV_ERR_SHAPE;
   if ((rc = check_device())) return rc;
